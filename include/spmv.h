@@ -479,6 +479,202 @@ spmv_status_t spmv_spgemm_device_status(spmv_spgemm_t handle, int32_t *flags);
 /* Free the handle's workspace (waits for the device).  NULL is a no-op. */
 spmv_status_t spmv_spgemm_destroy(spmv_spgemm_t handle);
 
+/*
+ * Operators of language models whose data is ragged the way a sparse
+ * matrix's rows are.  The pages have no counterpart.  In a decoder with
+ * mixtures of experts two index structures decide what is read:
+ *
+ *   - the routing matrix R, tokens by experts with top_k entries per row:
+ *     its transpose lists each expert's tokens (spmv_route_build: the
+ *     tokens sorted by expert), R^T X gathers their rows
+ *     (spmv_route_dispatch), and R weighted by the router, times the
+ *     experts' rows, brings them back (spmv_route_combine);
+ *   - the page table of a key-value cache, requests by pages, rows of one
+ *     page to thousands: spmv_pages_append extends it and maps each new
+ *     token to its slot, spmv_paged_store writes keys and values there, and
+ *     spmv_paged_attention reduces each request's row of it.
+ *
+ * All of them are asynchronous on `stream`, allocate nothing and never
+ * synchronise, so they can be captured in a CUDA graph; index arrays and
+ * workspaces are the caller's (device).  Row strides (ld...) count
+ * elements and may exceed the row's length, or be 0 or negative where
+ * only reads use them.  Inputs and outputs must not overlap unless a
+ * function says so.  Sums, dot products and softmax statistics are held in
+ * 32 bits and rounded once; no result depends on the order in which blocks
+ * run.
+ */
+typedef enum { SPMV_ELEM_F32 = 0, SPMV_ELEM_BF16 = 1, SPMV_ELEM_F16 = 2 } spmv_elem_t;
+
+/* Bytes of workspace (HOST *bytes; 0 possible) spmv_route_build needs. */
+spmv_status_t spmv_route_workspace(int32_t tokens, int32_t top_k, int32_t experts, size_t *bytes);
+
+/*
+ * Sort the entries of the routing matrix by expert.  Entry i = t * top_k + j
+ * is token t's j-th choice, the expert expert_ids[t * ld_ids + j] (device,
+ * int32 if id_bytes is 4, int64 if 8).  An id outside [0, experts) marks a
+ * dropped entry (over an expert's capacity, held by another device, or
+ * padding).  Writes
+ *   expert_ptr[experts + 1]  row pointers: expert e owns the positions
+ *                            expert_ptr[e] .. expert_ptr[e+1] - 1;
+ *   entry[tokens * top_k]    the entry at each position, increasing within
+ *                            an expert; the dropped entries, increasing,
+ *                            fill the positions from expert_ptr[experts];
+ *   slot[tokens * top_k]     the inverse: entry i's position p, or -1 - p
+ *                            for a dropped entry.
+ * Limits: tokens * top_k < 2^31, 1 <= experts <= 2048.  The workspace holds
+ * at least spmv_route_workspace bytes, 16-byte aligned; its contents do not
+ * matter.
+ * Errors: INVALID_ARG, CUDA.
+ */
+spmv_status_t spmv_route_build(int32_t tokens, int32_t top_k, int32_t experts, const void *expert_ids,
+                               int32_t id_bytes, int64_t ld_ids, int32_t *expert_ptr, int32_t *entry, int32_t *slot,
+                               void *workspace, size_t workspace_bytes, spmv_stream_t stream);
+
+/*
+ * xs[p] = x[entry[p] / top_k] for every position p of the sorted order: x is
+ * tokens-by-hidden, xs (tokens * top_k)-by-hidden, row-major.  Rows of
+ * dropped entries (the last ones of xs) are set to zero, so xs is written
+ * whole.  A copy: NaN payloads and signed zeros are kept.  The gradient of x
+ * is spmv_route_combine of xs's gradient with null weights.
+ * Errors: INVALID_ARG, CUDA.  tokens, top_k or hidden of 0 is a no-op.
+ */
+spmv_status_t spmv_route_dispatch(int32_t tokens, int32_t top_k, int32_t hidden, spmv_elem_t elem,
+                                  const int32_t *slot, const void *x, int64_t ldx, void *xs, int64_t ldxs,
+                                  spmv_stream_t stream);
+
+/*
+ * y[t] = sum over j, in order, of weights[t * ldw + j] * ys[slot[t, j]]; a
+ * dropped entry adds nothing, whatever its weight and row hold, and a token
+ * with every entry dropped gets zeros.  weights is float32; null means 1.
+ * Errors: as spmv_route_dispatch.  top_k of 0 sets y to zero.
+ */
+spmv_status_t spmv_route_combine(int32_t tokens, int32_t top_k, int32_t hidden, spmv_elem_t elem,
+                                 const int32_t *slot, const float *weights, int64_t ldw, const void *ys,
+                                 int64_t ldys, void *y, int64_t ldy, spmv_stream_t stream);
+
+/*
+ * The gradient of spmv_route_combine: from dy (tokens-by-hidden) and the
+ * forward pass's ys and weights,
+ *   dys[slot[t, j]] = weights[t, j] * dy[t]      (elem; null weights: dy[t])
+ *   dweights[t * lddw + j] = <dy[t], ys[slot[t, j]]>   (float32)
+ * Rows of dropped entries of dys and their dweights are set to zero.
+ * dweights may be null (ys is then not read and may be null too).  dys may
+ * be ys itself (the same pointer and row stride).
+ * Errors: as spmv_route_dispatch.
+ */
+spmv_status_t spmv_route_combine_backward(int32_t tokens, int32_t top_k, int32_t hidden, spmv_elem_t elem,
+                                          const int32_t *slot, const float *weights, int64_t ldw, const void *dy,
+                                          int64_t lddy, const void *ys, int64_t ldys, void *dys, int64_t lddys,
+                                          float *dweights, int64_t lddw, spmv_stream_t stream);
+
+/* Bytes of workspace (HOST *bytes; 0 possible) spmv_pages_append needs. */
+spmv_status_t spmv_pages_workspace(int32_t requests, size_t *bytes);
+
+/*
+ * Extend the page tables of a step's requests and map their new tokens to
+ * cache slots.  Request r holds past[r] tokens, so the first
+ * ceil(past[r] / page_size) entries of its table row (table + r * ld_table,
+ * room for max_pages) are its pages; fresh[r] >= 0 tokens are added to it.
+ * The pages they need beyond those held are taken from free_pages[num_free]
+ * in its order, request by request, and written into the row.  Writes
+ *   token_ptr[requests + 1]  prefix sums of fresh: request r's new tokens
+ *                            are token_ptr[r] .. token_ptr[r+1] - 1;
+ *   lens[requests]           past + fresh;
+ *   positions[max_tokens]    each new token's position in its request;
+ *   slots[max_tokens]        page * page_size + position % page_size;
+ *   taken[1]                 how many of free_pages are used up (a prefix);
+ *   status[1]                0, or the flags below.
+ * Entries of slots and positions past the last new token are set to -1.  A
+ * request that does not fit whole (the free list ends, the row would be
+ * longer than max_pages, or its new tokens end past max_tokens) is not
+ * served: its lens stays at past, its slots are -1 and its row is unchanged.
+ * One that would outgrow its row takes no pages; the others still count in
+ * the free list's order, so after one for which the list ends no later one
+ * that needs pages is served.  Flags: bit 0 the free list ended; bit 1 a row
+ * is too short; bit 2 more than max_tokens new tokens; bit 3 a negative past
+ * or fresh (taken as 0), or a past beyond the row (that request is not
+ * served); bit 4 a page outside [0, num_pages) among those used (its tokens'
+ * slots are -1).
+ * Limits: page_size >= 1, num_pages * page_size < 2^31, the sums of past and
+ * fresh over the requests < 2^31.  The workspace holds at least
+ * spmv_pages_workspace bytes, 16-byte aligned.
+ * Errors: INVALID_ARG, CUDA.
+ */
+spmv_status_t spmv_pages_append(int32_t requests, const int32_t *past, const int32_t *fresh, int32_t page_size,
+                                int32_t num_pages, const int32_t *free_pages, int32_t num_free, int32_t *table,
+                                int64_t ld_table, int32_t max_pages, int32_t max_tokens, int32_t *token_ptr,
+                                int32_t *lens, int32_t *slots, int32_t *positions, int32_t *taken, int32_t *status,
+                                void *workspace, size_t workspace_bytes, spmv_stream_t stream);
+
+/*
+ * Write the keys and values of `tokens` new tokens into a paged cache: for
+ * each i with slots[i] in [0, num_pages * page_size), page = slots[i] /
+ * page_size, s = slots[i] % page_size, and every head h,
+ *   k_cache[page * k_cache_stride[0] + s * k_cache_stride[1] + h * k_cache_stride[2] + d]
+ *     = k[i * k_stride[0] + h * k_stride[1] + d],   0 <= d < head_dim,
+ * and likewise v.  Other slots are skipped.  Strides (HOST arrays) count
+ * elements; the last index is contiguous.  Two tokens must not share a slot.
+ * Errors: INVALID_ARG, CUDA.
+ */
+spmv_status_t spmv_paged_store(int32_t tokens, int32_t heads, int32_t head_dim, spmv_elem_t elem,
+                               const int32_t *slots, int32_t num_pages, int32_t page_size, const void *k,
+                               const int64_t *k_stride, const void *v, const int64_t *v_stride, void *k_cache,
+                               const int64_t *k_cache_stride, void *v_cache, const int64_t *v_cache_stride,
+                               spmv_stream_t stream);
+
+/*
+ * Attention of one new token per request over a paged cache.  For request b
+ * and query head h, with kv head c = h / (q_heads / kv_heads) and positions
+ * t < lens[b], the key and value of position t in slot t % page_size of page
+ * table[b * table_stride + t / page_size]:
+ *   s_t = scale * <q[b, h], k_t>,   lse[b, h] = log sum_t exp(s_t),
+ *   out[b, h] = sum_t exp(s_t - lse[b, h]) v_t.
+ * A request of length 0 gets out = 0 and lse = -infinity.  Table entries past
+ * a request's last page, and cache contents past its length, are not used
+ * (they may hold anything, NaN included).
+ *
+ * The positions of all requests and kv heads together are cut into equal
+ * shares, one per warp, whatever the lengths (the equal shares of the
+ * merge-path SpMV); requests cut between warps and blocks are joined in a
+ * fixed order, so results do not change from call to call.
+ */
+typedef struct {
+    int32_t batch, q_heads, kv_heads, head_dim; /* q_heads a multiple of kv_heads; head_dim a
+                                                   multiple of 8, at most 256 */
+    int32_t page_size, num_pages, max_pages;    /* max_pages: entries in a table row */
+    int32_t elem;                               /* spmv_elem_t of q, the caches and out */
+    float scale;
+    int32_t reserved;
+    int64_t q_stride[2];   /* request, head (elements, as all strides) */
+    int64_t k_stride[3];   /* page, position in it, head; multiples of 16 bytes */
+    int64_t v_stride[3];
+    int64_t out_stride[2]; /* request, head */
+    int64_t table_stride;
+    const void *q;
+    const void *k_cache;   /* 16-byte aligned */
+    const void *v_cache;
+    const int32_t *table;
+    const int32_t *lens;
+    void *out;
+    float *lse;            /* [batch * q_heads], or null */
+    void *workspace;       /* spmv_paged_attention_workspace bytes, 16-byte aligned; zeroed once by
+                              the caller, every call leaves it ready for the next; calls that may
+                              overlap on the GPU need workspaces of their own */
+    size_t workspace_bytes;
+    int32_t *status;       /* device int32; flags are OR-ed in.  Bit 0: a page outside
+                              [0, num_pages) (its positions are left out); bit 1: a length that is
+                              negative or longer than its row (taken as 0, or cut) */
+} spmv_paged_attention_t;
+
+/* Bytes of workspace (HOST *bytes) spmv_paged_attention needs for up to
+ * max_batch requests, on the current device. */
+spmv_status_t spmv_paged_attention_workspace(int32_t max_batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                             spmv_elem_t elem, size_t *bytes);
+
+/* args is a HOST structure, read before the call returns.
+ * Errors: INVALID_ARG, CUDA. */
+spmv_status_t spmv_paged_attention(const spmv_paged_attention_t *args, spmv_stream_t stream);
+
 /* Static text for a status code. */
 const char *spmv_status_string(spmv_status_t status);
 

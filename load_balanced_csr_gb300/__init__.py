@@ -8,6 +8,10 @@ the import of ``lib()`` raises.
     import torch, load_balanced_csr_gb300 as lb
     plan = lb.Plan(row_ptr, col_idx, vals, n)      # CUDA tensors: int32, int32, f32/f64
     plan(x, y, alpha=1.0, beta=0.0)               # y = alpha*A*x + beta*y on the current stream
+
+The language-model operators -- routing to experts (``ExpertRoute``), page
+tables and the paged cache (``PageTable``, ``paged_store``) and its attention
+(``PagedAttention``) -- are in ``routing`` and ``paged``.
 """
 from __future__ import annotations
 
@@ -17,7 +21,7 @@ import os
 from . import _build
 
 __all__ = ["Plan", "SpGEMM", "spgemm", "SpmvError", "lib", "KERNELS", "EXPORTS", "header_functions",
-           "gather_ceiling", "GATHER_PATHS"]
+           "gather_ceiling", "GATHER_PATHS", "ExpertRoute", "PageTable", "PagedAttention", "paged_store"]
 
 KERNELS = {"auto": 0, "merge_path": 1, "thread_row": 2, "rgcsr": 3, "long_rows": 4, "rgcsr_sorted": 5,
            "group_mapped": 6}
@@ -106,6 +110,7 @@ def _load(path: str) -> ctypes.CDLL:
         raise RuntimeError(f"{os.path.basename(path)} is missing and could not be built")
     L = ctypes.CDLL(path)
     vp, i32, sz, dbl = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_double
+    i64 = ctypes.c_int64
     sigs = {
         "spmv_plan_create": [ctypes.POINTER(vp), i32, i32, i32, vp, vp, vp, ctypes.c_int, vp],
         "spmv_plan_create_ex": [ctypes.POINTER(vp), i32, i32, i32, vp, vp, vp, ctypes.c_int,
@@ -128,6 +133,17 @@ def _load(path: str) -> ctypes.CDLL:
         "spmv_spgemm_device_status": [vp, ctypes.POINTER(i32)],
         "spmv_spgemm_destroy": [vp],
         "spmv_gather_ceiling": [i32, i32, vp, i32, vp, vp, ctypes.c_int, vp, vp, vp],
+        "spmv_route_workspace": [i32, i32, i32, ctypes.POINTER(sz)],
+        "spmv_route_build": [i32, i32, i32, vp, i32, i64, vp, vp, vp, vp, sz, vp],
+        "spmv_route_dispatch": [i32, i32, i32, ctypes.c_int, vp, vp, i64, vp, i64, vp],
+        "spmv_route_combine": [i32, i32, i32, ctypes.c_int, vp, vp, i64, vp, i64, vp, i64, vp],
+        "spmv_route_combine_backward": [i32, i32, i32, ctypes.c_int, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                        vp],
+        "spmv_pages_workspace": [i32, ctypes.POINTER(sz)],
+        "spmv_pages_append": [i32, vp, vp, i32, i32, vp, i32, vp, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "spmv_paged_store": [i32, i32, i32, ctypes.c_int, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp],
+        "spmv_paged_attention_workspace": [i32, i32, i32, i32, ctypes.c_int, ctypes.POINTER(sz)],
+        "spmv_paged_attention": [vp, vp],
     }
     for name, args in sigs.items():
         fn = getattr(L, name)
@@ -446,3 +462,17 @@ def gather_ceiling(path: str, col_idx, x, checksum, error, stream=None, vals=Non
                                     _ptr(vals) if vals is not None else None, _dtype_code(x), checksum.data_ptr(),
                                     error.data_ptr(), _stream_handle(stream)),
           f"spmv_gather_ceiling({path})")
+
+
+def __getattr__(name):
+    # the operators' modules import torch, which the rest of this module only
+    # does when it is used
+    if name == "ExpertRoute":
+        from .routing import ExpertRoute as found
+    elif name in ("PageTable", "PagedAttention", "paged_store"):
+        from . import paged
+        found = getattr(paged, name)
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    globals()[name] = found
+    return found

@@ -1,0 +1,74 @@
+"""Shared by the language-model operators' bindings: streams, outputs, checks."""
+from __future__ import annotations
+
+import torch
+
+ELEMS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def elem(dtype) -> int:
+    try:
+        return ELEMS[dtype]
+    except KeyError:
+        raise TypeError(f"elements must be float32, bfloat16 or float16, got {dtype}") from None
+
+
+def handle(stream, device) -> int:
+    """The cudaStream_t of ``stream`` (None: the device's current stream)."""
+    if stream is None:
+        return _raw_stream(device.index)
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def empty(stream, device, shape, dtype):
+    """An output for a launch on ``stream``, taken from that stream's own
+    memory: memory of another stream could still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle(stream, device), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def call(fn, what, device, *args) -> None:
+    """One library call with ``device`` current; raises SpmvError."""
+    from . import check
+    if device.index == torch.cuda.current_device():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status:
+        check(status, what)
+
+
+def cuda_device(device):
+    """``device`` with its index filled in."""
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise TypeError("a CUDA device is needed")
+    return device if device.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
+def rows(name, t, shape, dtype, device):
+    """Checks a row-major matrix (unit stride in a row) and returns its row stride."""
+    if t.dtype != dtype or t.device != device:
+        raise TypeError(f"{name} must be a {dtype} tensor on {device}, got {t.dtype} on {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    ld, unit = t.stride()
+    if unit != 1 and shape[1] > 1 and shape[0] > 0:
+        raise ValueError(f"{name} must have contiguous rows")
+    return ld if shape[0] > 1 else max(ld, shape[1])
+
+
+def vector(name, t, n, dtype, device):
+    """Checks a contiguous vector of at least n entries."""
+    if t.dtype != dtype or t.device != device:
+        raise TypeError(f"{name} must be a {dtype} tensor on {device}, got {t.dtype} on {t.device}")
+    if t.dim() != 1 or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of at least {n} entries")
+    return t.data_ptr() or None

@@ -15,6 +15,7 @@
 #include <string>
 #include <vector>
 
+#include "llm.cuh"
 #include "row_spmm.cuh"
 #include "spgemm.cuh"
 
@@ -175,6 +176,16 @@ struct FaultScope {
 };
 
 }  // namespace
+
+// For the entry points of other translation units (llm.cuh).
+spmv_status_t lbcsr::llm_fail(spmv_status_t s, const char *what, const char *detail) noexcept {
+    try {
+        g_last_error = what;
+        if (detail) g_last_error.append(": ").append(detail);
+    } catch (...) {  // out of host memory: the status still says what failed
+    }
+    return s;
+}
 
 // A launch step of a creation call (the injected failure skips the launch).
 #define LAUNCH(call) (launch_fault() ? cudaErrorLaunchFailure : (call))

@@ -1,0 +1,52 @@
+// Shared by the language-model operators (route.cu, pages.cu,
+// paged_attention.cu): errors of their C entry points, vectors of elements
+// and their conversion to and from 32 bits.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "spmv.h"
+
+namespace lbcsr {
+
+// Records the calling thread's last error (spmv_last_error) and returns s.
+spmv_status_t llm_fail(spmv_status_t s, const char *what, const char *detail = nullptr) noexcept;
+
+inline spmv_status_t llm_bad(const char *what) noexcept { return llm_fail(SPMV_ERR_INVALID_ARG, what); }
+
+inline spmv_status_t llm_launched(const char *what, cudaError_t e) noexcept {
+    return e == cudaSuccess ? SPMV_OK : llm_fail(SPMV_ERR_CUDA, what, cudaGetErrorString(e));
+}
+
+inline bool elem_ok(int elem) { return elem == SPMV_ELEM_F32 || elem == SPMV_ELEM_BF16 || elem == SPMV_ELEM_F16; }
+inline int elem_size(int elem) { return elem == SPMV_ELEM_F32 ? 4 : 2; }
+
+inline bool aligned_to(const void *p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
+
+// N consecutive elements, moved by one load or store of sizeof(Vec) bytes.
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Vec {
+    T v[N];
+};
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
+
+template <typename T>
+__device__ __forceinline__ T zero_of() { return from_float<T>(0.0f); }
+
+}  // namespace lbcsr

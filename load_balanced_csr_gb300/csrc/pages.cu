@@ -1,0 +1,255 @@
+// Page tables of a key-value cache and the stores through them.
+//
+// spmv_pages_append: with held_r = ceil(past_r / P), a prefix sum over the
+// requests of (fresh_r, pages needed) gives each new token's place and each
+// new page's place in the free list; then one thread per new token finds its
+// request by binary search in the prefix sums (as a merge-path tile finds its
+// first row), computes its slot from the table or, for a page not held
+// before, from the free list, and the token that opens a page writes the
+// table's entry.
+#include <algorithm>
+#include <climits>
+
+#include "llm.cuh"
+
+namespace lbcsr {
+
+namespace {
+
+// ---------------------------------------------------------------- append
+constexpr int kScanThreads = 1024;
+constexpr int kExpandThreads = 256;
+
+enum { kFreeEnded = 1, kRowShort = 2, kTooManyTokens = 4, kBadLength = 8, kBadPage = 16 };
+
+struct AppendArgs {
+    int32_t requests, page, num_pages, num_free, max_pages, max_tokens;
+    const int32_t *past, *fresh, *free_pages;
+    int32_t *table;
+    int64_t ld_table;
+    int32_t *token_ptr, *lens, *slots, *positions, *taken, *status;
+    int32_t *first;  // workspace [requests]: place of the request's first new page in the free list,
+                     // -1: not served
+};
+
+__global__ void __launch_bounds__(kScanThreads) pages_scan_kernel(AppendArgs a) {
+    __shared__ long long warp_sum[kScanThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long carry = 0;  // pages << 32 | tokens
+    int32_t flags = 0, used = 0;
+    for (int r0 = 0; r0 < a.requests; r0 += kScanThreads) {
+        const int r = r0 + threadIdx.x;
+        int32_t past = 0, fresh = 0, need = 0;
+        bool fits = true;
+        if (r < a.requests) {
+            past = a.past[r], fresh = a.fresh[r];
+            if (past < 0 || fresh < 0) flags |= kBadLength, past = max(past, 0), fresh = max(fresh, 0);
+            const long long held = ((long long)past + a.page - 1) / a.page;
+            const long long want = ((long long)past + fresh + a.page - 1) / a.page;
+            if (held > a.max_pages) fits = false, flags |= kBadLength;
+            else if (want > a.max_pages) fits = false, flags |= kRowShort;
+            else need = (int32_t)(want - held);
+        }
+        const long long mine = ((long long)need << 32) + fresh;
+        long long scan = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, scan, d);
+            if (lane >= d) scan += up;
+        }
+        if (lane == 31) warp_sum[warp] = scan;
+        __syncthreads();
+        long long start = carry + scan - mine;
+#pragma unroll
+        for (int w = 0; w < kScanThreads / 32; ++w) {
+            const long long s = warp_sum[w];
+            if (w < warp) start += s;
+            carry += s;
+        }
+        if (r < a.requests) {
+            const int32_t first = (int32_t)(start >> 32), tokens = (int32_t)start;
+            bool served = fits;
+            if (need > 0 && (long long)first + need > a.num_free) served = false, flags |= kFreeEnded;
+            if (fresh > 0 && (long long)tokens + fresh > a.max_tokens) served = false, flags |= kTooManyTokens;
+            if (served && need > 0) used = max(used, first + need);
+            a.token_ptr[r] = tokens;
+            a.lens[r] = served ? past + fresh : past;
+            a.first[r] = served ? first : -1;
+        }
+        __syncthreads();
+    }
+    __shared__ int32_t all_flags, all_used;
+    if (threadIdx.x == 0) all_flags = 0, all_used = 0, a.token_ptr[a.requests] = (int32_t)carry;
+    __syncthreads();
+    if (flags) atomicOr(&all_flags, flags);
+    if (used) atomicMax(&all_used, used);
+    __syncthreads();
+    if (threadIdx.x == 0) *a.status = all_flags, *a.taken = all_used;
+}
+
+__global__ void __launch_bounds__(kExpandThreads) pages_expand_kernel(AppendArgs a) {
+    const int64_t i = (int64_t)blockIdx.x * kExpandThreads + threadIdx.x;
+    if (i >= a.max_tokens) return;
+    if (i >= a.token_ptr[a.requests]) {
+        a.slots[i] = -1, a.positions[i] = -1;
+        return;
+    }
+    int lo = 0, hi = a.requests - 1;  // the last request with token_ptr[r] <= i: the one that holds i
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.token_ptr[mid] <= i) lo = mid;
+        else hi = mid - 1;
+    }
+    const int32_t past = max(a.past[lo], 0), at = past + (int32_t)(i - a.token_ptr[lo]);
+    const int32_t first = a.first[lo], page = at / a.page, inside = at - page * a.page;
+    a.positions[i] = at;
+    if (first < 0 || i - a.token_ptr[lo] >= a.fresh[lo]) {  // the latter only if the sums passed 32 bits
+        a.slots[i] = -1;
+        return;
+    }
+    const int32_t held = (int32_t)(((long long)past + a.page - 1) / a.page);
+    int32_t *entry = a.table + lo * a.ld_table + page;
+    int32_t id;
+    if (page < held) {
+        id = *entry;
+    } else {
+        id = a.free_pages[first + page - held];
+        if (inside == 0) *entry = id;
+    }
+    const bool good = id >= 0 && id < a.num_pages;
+    if (!good) atomicOr(a.status, kBadPage);
+    a.slots[i] = good ? id * a.page + inside : -1;
+}
+
+// ---------------------------------------------------------------- store
+constexpr int kStoreThreads = 256;
+
+struct StoreArgs {
+    int32_t tokens, heads, vecs, num_pages, page;  // vecs: vectors in a head
+    const int32_t *slots;
+    int64_t ks[2], vs[2], kc[3], vc[3];
+};
+
+// A warp per token.
+template <typename T, int N>
+__global__ void __launch_bounds__(kStoreThreads)
+paged_store_kernel(StoreArgs a, const T *__restrict__ k, const T *__restrict__ v, T *__restrict__ kc,
+                   T *__restrict__ vc) {
+    using V = Vec<T, N>;
+    const int lane = threadIdx.x & 31;
+    const int64_t i = (int64_t)blockIdx.x * (kStoreThreads / 32) + (threadIdx.x >> 5);
+    if (i >= a.tokens) return;
+    const int32_t slot = __ldg(a.slots + i);
+    if (slot < 0 || slot / a.page >= a.num_pages) return;
+    const int64_t page = slot / a.page, in = slot % a.page;
+    const int total = a.heads * a.vecs;
+    for (int e = lane; e < total; e += 32) {
+        const int64_t h = e / a.vecs, d = (int64_t)(e % a.vecs) * N;
+        const V kv = *reinterpret_cast<const V *>(k + i * a.ks[0] + h * a.ks[1] + d);
+        const V vv = *reinterpret_cast<const V *>(v + i * a.vs[0] + h * a.vs[1] + d);
+        *reinterpret_cast<V *>(kc + page * a.kc[0] + in * a.kc[1] + h * a.kc[2] + d) = kv;
+        *reinterpret_cast<V *>(vc + page * a.vc[0] + in * a.vc[1] + h * a.vc[2] + d) = vv;
+    }
+}
+
+template <typename T, int N>
+cudaError_t launch_store(const StoreArgs &a, const void *k, const void *v, void *kc, void *vc, cudaStream_t stream) {
+    const unsigned blocks = (unsigned)((a.tokens + (int64_t)kStoreThreads / 32 - 1) / (kStoreThreads / 32));
+    paged_store_kernel<T, N><<<blocks, kStoreThreads, 0, stream>>>(a, static_cast<const T *>(k), static_cast<const T *>(v),
+                                                                   static_cast<T *>(kc), static_cast<T *>(vc));
+    return cudaGetLastError();
+}
+
+bool on_16(const void *p, const int64_t *strides, int n, int size) {
+    if (!aligned_to(p, 16)) return false;
+    for (int i = 0; i < n; ++i)
+        if (strides[i] * size % 16) return false;
+    return true;
+}
+
+}  // namespace
+
+}  // namespace lbcsr
+
+using namespace lbcsr;
+
+extern "C" {
+
+spmv_status_t spmv_pages_workspace(int32_t requests, size_t *bytes) {
+    if (!bytes) return llm_bad("bytes is NULL");
+    *bytes = 0;
+    if (requests < 0) return llm_bad("negative size");
+    *bytes = 4 * (size_t)requests;
+    return SPMV_OK;
+}
+
+spmv_status_t spmv_pages_append(int32_t requests, const int32_t *past, const int32_t *fresh, int32_t page_size,
+                                int32_t num_pages, const int32_t *free_pages, int32_t num_free, int32_t *table,
+                                int64_t ld_table, int32_t max_pages, int32_t max_tokens, int32_t *token_ptr,
+                                int32_t *lens, int32_t *slots, int32_t *positions, int32_t *taken, int32_t *status,
+                                void *workspace, size_t workspace_bytes, spmv_stream_t stream_handle) {
+    size_t need = 0;
+    const spmv_status_t st = spmv_pages_workspace(requests, &need);
+    if (st != SPMV_OK) return st;
+    if (num_pages < 0 || num_free < 0 || max_pages < 0 || max_tokens < 0) return llm_bad("negative size");
+    if (page_size < 1) return llm_bad("page_size must be at least 1");
+    if ((int64_t)num_pages * page_size >= (1LL << 31)) return llm_bad("num_pages * page_size must be < 2^31");
+    if (!token_ptr || !taken || !status) return llm_bad("token_ptr, taken or status is NULL");
+    if (requests > 0 && (!past || !fresh || !lens)) return llm_bad("past, fresh or lens is NULL");
+    if (requests > 0 && max_pages > 0 && !table) return llm_bad("table is NULL");
+    if (ld_table < max_pages) return llm_bad("ld_table is smaller than max_pages");
+    if (num_free > 0 && !free_pages) return llm_bad("free_pages is NULL");
+    if (max_tokens > 0 && (!slots || !positions)) return llm_bad("slots or positions is NULL");
+    if (need && (!workspace || workspace_bytes < need || !aligned_to(workspace, 16)))
+        return llm_bad("workspace is NULL, too small or not 16-byte aligned");
+    AppendArgs a;
+    a.requests = requests, a.page = page_size, a.num_pages = num_pages, a.num_free = num_free;
+    a.max_pages = max_pages, a.max_tokens = max_tokens;
+    a.past = past, a.fresh = fresh, a.free_pages = free_pages;
+    a.table = table, a.ld_table = ld_table;
+    a.token_ptr = token_ptr, a.lens = lens, a.slots = slots, a.positions = positions, a.taken = taken;
+    a.status = status;
+    a.first = static_cast<int32_t *>(workspace);
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
+    pages_scan_kernel<<<1, kScanThreads, 0, stream>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && max_tokens > 0) {
+        pages_expand_kernel<<<(unsigned)(((int64_t)max_tokens + kExpandThreads - 1) / kExpandThreads), kExpandThreads, 0,
+                              stream>>>(a);
+        e = cudaGetLastError();
+    }
+    return llm_launched("spmv_pages_append launch", e);
+}
+
+spmv_status_t spmv_paged_store(int32_t tokens, int32_t heads, int32_t head_dim, spmv_elem_t elem,
+                               const int32_t *slots, int32_t num_pages, int32_t page_size, const void *k,
+                               const int64_t *k_stride, const void *v, const int64_t *v_stride, void *k_cache,
+                               const int64_t *k_cache_stride, void *v_cache, const int64_t *v_cache_stride,
+                               spmv_stream_t stream_handle) {
+    if (tokens < 0 || heads < 0 || head_dim < 0 || num_pages < 0) return llm_bad("negative size");
+    if (page_size < 1) return llm_bad("page_size must be at least 1");
+    if ((int64_t)num_pages * page_size >= (1LL << 31)) return llm_bad("num_pages * page_size must be < 2^31");
+    if ((int64_t)heads * head_dim >= (1LL << 31)) return llm_bad("heads * head_dim must be < 2^31");
+    if (!elem_ok(elem)) return llm_bad("unknown element type");
+    if (!k_stride || !v_stride || !k_cache_stride || !v_cache_stride) return llm_bad("a stride array is NULL");
+    if (tokens == 0 || heads == 0 || head_dim == 0 || num_pages == 0) return SPMV_OK;
+    if (!slots || !k || !v || !k_cache || !v_cache) return llm_bad("slots, k, v or a cache is NULL");
+    const int size = elem_size(elem);
+    if (!aligned_to(k, size) || !aligned_to(v, size) || !aligned_to(k_cache, size) || !aligned_to(v_cache, size))
+        return llm_bad("k, v or a cache is not aligned to its type");
+    const bool wide = head_dim * size % 16 == 0 && on_16(k, k_stride, 2, size) && on_16(v, v_stride, 2, size) &&
+                      on_16(k_cache, k_cache_stride, 3, size) && on_16(v_cache, v_cache_stride, 3, size);
+    StoreArgs a;
+    a.tokens = tokens, a.heads = heads, a.num_pages = num_pages, a.page = page_size, a.slots = slots;
+    a.vecs = wide ? head_dim * size / 16 : head_dim;
+    for (int i = 0; i < 2; ++i) a.ks[i] = k_stride[i], a.vs[i] = v_stride[i];
+    for (int i = 0; i < 3; ++i) a.kc[i] = k_cache_stride[i], a.vc[i] = v_cache_stride[i];
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
+    const cudaError_t e = size == 4 ? (wide ? launch_store<float, 4>(a, k, v, k_cache, v_cache, stream)
+                                            : launch_store<float, 1>(a, k, v, k_cache, v_cache, stream))
+                                    : (wide ? launch_store<__half, 8>(a, k, v, k_cache, v_cache, stream)
+                                            : launch_store<__half, 1>(a, k, v, k_cache, v_cache, stream));
+    return llm_launched("spmv_paged_store launch", e);
+}
+
+}  // extern "C"

@@ -1,0 +1,472 @@
+// Routing tokens to experts: the transpose of the routing matrix (tokens by
+// experts, top_k entries per row) by a stable counting sort, its product
+// with the tokens' rows (dispatch), the weighted product back (combine) and
+// the gradient of both.
+//
+//   build             slot = the stable rank of entry i = t * top_k + j by
+//                     expert; entry = its inverse; expert_ptr = row pointers
+//   dispatch          xs[slot(t, j)] = x[t]
+//   combine           y[t] = sum_j w(t, j) ys[slot(t, j)]
+//   combine_backward  dys[slot(t, j)] = w(t, j) dy[t],
+//                     dw(t, j) = <dy[t], ys[slot(t, j)]>
+//
+// The rows' passes are bound by memory and go token by token: a token's own
+// row is read or written once and stays in registers while its top_k expert
+// rows pass.
+#include <algorithm>
+
+#include "llm.cuh"
+
+namespace lbcsr {
+
+namespace {
+
+// ---------------------------------------------------------------- build
+constexpr int kBuildThreads = 512;
+constexpr int kBuildWarps = kBuildThreads / 32;
+constexpr int kMaxExperts = 2048;
+constexpr int kMaxTiles = 152;      // one tile per SM at most
+constexpr int kMinTile = 4096;      // entries
+
+int64_t build_tile(int64_t n) {
+    const int64_t t = std::max<int64_t>((n + kMaxTiles - 1) / kMaxTiles, kMinTile);
+    return (t + kBuildThreads - 1) / kBuildThreads * kBuildThreads;
+}
+int build_tiles(int64_t n) { return (int)std::max<int64_t>(1, (n + build_tile(n) - 1) / build_tile(n)); }
+
+template <typename I>
+__device__ __forceinline__ int key_of(const I *__restrict__ ids, int64_t ld, int k, int experts, int64_t i) {
+    const I id = ld == k ? ids[i] : ids[(i / k) * ld + i % k];
+    return id >= 0 && id < (I)experts ? (int)id : experts;  // the last bin: dropped
+}
+
+// hist[tile * (experts + 1) + bin]: entries of the tile in each bin
+template <typename I>
+__global__ void __launch_bounds__(kBuildThreads)
+route_hist_kernel(const I *__restrict__ ids, int64_t ld, int k, int64_t n, int experts, int64_t tile,
+                  int32_t *__restrict__ hist) {
+    extern __shared__ int32_t h[];
+    const int bins = experts + 1;
+    for (int b = threadIdx.x; b < bins; b += kBuildThreads) h[b] = 0;
+    __syncthreads();
+    const int64_t t0 = (int64_t)blockIdx.x * tile, t1 = min(t0 + tile, n);
+    for (int64_t i = t0 + threadIdx.x; i < t1; i += kBuildThreads) atomicAdd(&h[key_of(ids, ld, k, experts, i)], 1);
+    __syncthreads();
+    for (int b = threadIdx.x; b < bins; b += kBuildThreads) hist[(int64_t)blockIdx.x * bins + b] = h[b];
+}
+
+// Ranks of one tile.  Each warp owns a run of consecutive entries; base[w][b]
+// becomes the position of warp w's first entry in bin b: the bin's start,
+// plus the earlier tiles' counts, plus the earlier warps'.
+template <typename I>
+__global__ void __launch_bounds__(kBuildThreads)
+route_rank_kernel(const I *__restrict__ ids, int64_t ld, int k, int64_t n, int experts, int64_t tile, int tiles,
+                  const int32_t *__restrict__ hist, int32_t *__restrict__ expert_ptr, int32_t *__restrict__ entry,
+                  int32_t *__restrict__ slot) {
+    extern __shared__ int32_t base[];  // [warps][bins]
+    __shared__ int32_t warp_sum[kBuildWarps];
+    const int bins = experts + 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t0 = (int64_t)blockIdx.x * tile;
+    const int64_t run = ((tile + kBuildWarps - 1) / kBuildWarps + 31) / 32 * 32;
+    const int64_t w0 = t0 + warp * run, w1 = min(min(w0 + run, t0 + tile), n);
+    int32_t *mine = base + warp * bins;
+    for (int b = lane; b < bins; b += 32) mine[b] = 0;
+    __syncwarp();
+    for (int64_t i0 = w0; i0 < w1; i0 += 32) {
+        const int64_t i = i0 + lane;
+        const int key = i < w1 ? key_of(ids, ld, k, experts, i) : bins;
+        const unsigned peers = __match_any_sync(0xffffffffu, key);
+        if (i < w1 && lane == __ffs(peers) - 1) mine[key] += __popc(peers);
+        __syncwarp();
+    }
+    __syncthreads();
+    // bins in blocks of one per thread; carry: the entries of earlier blocks
+    int32_t carry = 0;
+    for (int b0 = 0; b0 < bins; b0 += kBuildThreads) {
+        const int b = b0 + threadIdx.x;
+        int32_t total = 0, before = 0;
+        if (b < bins) {
+            if (tiles == 1) {
+                for (int w = 0; w < kBuildWarps; ++w) total += base[w * bins + b];
+            } else {
+#pragma unroll 8
+                for (int t = 0; t < tiles; ++t) {
+                    const int32_t c = __ldg(hist + (int64_t)t * bins + b);
+                    total += c;
+                    if (t < blockIdx.x) before += c;
+                }
+            }
+        }
+        // exclusive prefix sum of the totals over the block's threads
+        int32_t scan = total;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t up = __shfl_up_sync(0xffffffffu, scan, d);
+            if (lane >= d) scan += up;
+        }
+        if (lane == 31) warp_sum[warp] = scan;
+        __syncthreads();
+        int32_t start = carry + scan - total, all = 0;
+#pragma unroll
+        for (int w = 0; w < kBuildWarps; ++w) {
+            const int32_t s = warp_sum[w];
+            if (w < warp) start += s;
+            all += s;
+        }
+        carry += all;
+        if (b < bins) {
+            if (blockIdx.x == 0) expert_ptr[b] = start;  // bin `experts` starts where the experts end
+            int32_t at = start + before;
+            for (int w = 0; w < kBuildWarps; ++w) {
+                const int32_t c = base[w * bins + b];
+                base[w * bins + b] = at;
+                at += c;
+            }
+        }
+        __syncthreads();
+    }
+    const unsigned lt = (1u << lane) - 1u;
+    for (int64_t i0 = w0; i0 < w1; i0 += 32) {
+        const int64_t i = i0 + lane;
+        const int key = i < w1 ? key_of(ids, ld, k, experts, i) : bins;
+        const unsigned peers = __match_any_sync(0xffffffffu, key);
+        if (i < w1) {
+            const int32_t p = mine[key] + __popc(peers & lt);
+            entry[p] = (int32_t)i;
+            slot[i] = key < experts ? p : -1 - p;
+        }
+        __syncwarp();
+        if (i < w1 && lane == __ffs(peers) - 1) mine[key] += __popc(peers);
+        __syncwarp();
+    }
+}
+
+template <typename I>
+cudaError_t launch_build(int64_t n, int k, int experts, const I *ids, int64_t ld, int32_t *expert_ptr, int32_t *entry,
+                         int32_t *slot, int32_t *hist, cudaStream_t stream) {
+    const int64_t tile = build_tile(n);
+    const int tiles = build_tiles(n);
+    const size_t bins = (size_t)experts + 1, smem = bins * kBuildWarps * 4;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(route_rank_kernel<I>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    if (tiles > 1)
+        route_hist_kernel<I><<<tiles, kBuildThreads, bins * 4, stream>>>(ids, ld, k, n, experts, tile, hist);
+    route_rank_kernel<I><<<tiles, kBuildThreads, smem, stream>>>(ids, ld, k, n, experts, tile, tiles, hist, expert_ptr,
+                                                                 entry, slot);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- rows
+constexpr int kRowThreads = 256;
+
+// One warp per (token, span of 32 * U vectors of its row).
+struct RowArgs {
+    int64_t items;   // tokens * spans
+    int32_t spans;
+    int32_t k;
+    int32_t vecs;    // vectors in a row
+    const int32_t *slot;
+    const float *w;
+    int64_t ldw;
+};
+
+template <typename T, int N, int U>
+__global__ void __launch_bounds__(kRowThreads)
+route_dispatch_kernel(RowArgs a, const T *__restrict__ x, int64_t ldx, T *__restrict__ xs, int64_t ldxs) {
+    using V = Vec<T, N>;
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    if (item >= a.items) return;
+    const int64_t t = item / a.spans;
+    const int v0 = (int)(item % a.spans) * (32 * U) + lane;
+    const V *src = reinterpret_cast<const V *>(x + t * ldx);
+    V row[U], none;
+#pragma unroll
+    for (int n = 0; n < N; ++n) none.v[n] = zero_of<T>();
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (v0 + 32 * u < a.vecs) row[u] = src[v0 + 32 * u];
+    for (int j = 0; j < a.k; ++j) {
+        const int32_t p = __ldg(a.slot + t * a.k + j);
+        V *dst = reinterpret_cast<V *>(xs + (int64_t)(p < 0 ? -1 - p : p) * ldxs);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v0 + 32 * u < a.vecs) dst[v0 + 32 * u] = p < 0 ? none : row[u];
+    }
+}
+
+template <typename T, int N, int U>
+__global__ void __launch_bounds__(kRowThreads)
+route_combine_kernel(RowArgs a, const T *__restrict__ ys, int64_t ldys, T *__restrict__ y, int64_t ldy) {
+    using V = Vec<T, N>;
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    if (item >= a.items) return;
+    const int64_t t = item / a.spans;
+    const int v0 = (int)(item % a.spans) * (32 * U) + lane;
+    float sum[U][N];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int n = 0; n < N; ++n) sum[u][n] = 0.0f;
+#pragma unroll 4
+    for (int j = 0; j < a.k; ++j) {
+        const int32_t p = __ldg(a.slot + t * a.k + j);
+        if (p < 0) continue;
+        const float w = a.w ? __ldg(a.w + t * a.ldw + j) : 1.0f;
+        const V *src = reinterpret_cast<const V *>(ys + (int64_t)p * ldys);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v0 + 32 * u < a.vecs) {
+                const V r = src[v0 + 32 * u];
+#pragma unroll
+                for (int n = 0; n < N; ++n) sum[u][n] = fmaf(w, to_float(r.v[n]), sum[u][n]);
+            }
+    }
+    V *dst = reinterpret_cast<V *>(y + t * ldy);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (v0 + 32 * u < a.vecs) {
+            V r;
+#pragma unroll
+            for (int n = 0; n < N; ++n) r.v[n] = from_float<T>(sum[u][n]);
+            dst[v0 + 32 * u] = r;
+        }
+}
+
+// A block per token, K choices at a time: dy's row is read once for them
+// and their dot products summed over the block.
+template <typename T, int N, int K>
+__global__ void __launch_bounds__(kRowThreads)
+route_combine_backward_kernel(RowArgs a, const T *__restrict__ dy, int64_t lddy, const T *ys, int64_t ldys, T *dys,
+                              int64_t lddys, float *__restrict__ dw, int64_t lddw) {
+    using V = Vec<T, N>;
+    __shared__ float part[K][kRowThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t t = blockIdx.x;
+    const V *g = reinterpret_cast<const V *>(dy + t * lddy);
+    for (int j0 = 0; j0 < a.k; j0 += K) {
+        int32_t p[K];
+        float w[K], dot[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const bool in = j0 + j < a.k;
+            p[j] = in ? __ldg(a.slot + t * a.k + j0 + j) : 0;
+            w[j] = in && a.w ? __ldg(a.w + t * a.ldw + j0 + j) : 1.0f;
+            dot[j] = 0.0f;
+        }
+        for (int v = threadIdx.x; v < a.vecs; v += blockDim.x) {
+            const V gv = g[v];
+            V yv[K];
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (dw && j0 + j < a.k && p[j] >= 0) yv[j] = reinterpret_cast<const V *>(ys + (int64_t)p[j] * ldys)[v];
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                if (j0 + j >= a.k) continue;
+                V r;
+                if (p[j] < 0) {
+#pragma unroll
+                    for (int n = 0; n < N; ++n) r.v[n] = zero_of<T>();
+                } else {
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        const float gf = to_float(gv.v[n]);
+                        if (dw) dot[j] = fmaf(gf, to_float(yv[j].v[n]), dot[j]);
+                        r.v[n] = from_float<T>(w[j] * gf);
+                    }
+                }
+                reinterpret_cast<V *>(dys + (int64_t)(p[j] < 0 ? -1 - p[j] : p[j]) * lddys)[v] = r;
+            }
+        }
+        if (dw) {
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                float d = dot[j];
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
+                if (lane == 0) part[j][warp] = d;
+            }
+            __syncthreads();
+            if (threadIdx.x < K && j0 + threadIdx.x < a.k) {
+                float d = 0.0f;
+                for (int i = 0; i < warps; ++i) d += part[threadIdx.x][i];
+                dw[t * lddw + j0 + threadIdx.x] = d;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+RowArgs row_args(int32_t tokens, int32_t k, int32_t hidden, int n, int u, const int32_t *slot, const float *w,
+                 int64_t ldw) {
+    RowArgs a;
+    a.vecs = hidden / n;
+    a.spans = (a.vecs + 32 * u - 1) / (32 * u);
+    a.items = (int64_t)tokens * a.spans;
+    a.k = k;
+    a.slot = slot;
+    a.w = w;
+    a.ldw = ldw;
+    return a;
+}
+
+unsigned row_blocks(const RowArgs &a) { return (unsigned)((a.items + kRowThreads / 32 - 1) / (kRowThreads / 32)); }
+
+template <typename T, int N>
+cudaError_t launch_dispatch(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const void *x, int64_t ldx,
+                            void *xs, int64_t ldxs, cudaStream_t stream) {
+    constexpr int U = 4;
+    const RowArgs a = row_args(tokens, k, hidden, N, U, slot, nullptr, 0);
+    route_dispatch_kernel<T, N, U><<<row_blocks(a), kRowThreads, 0, stream>>>(a, static_cast<const T *>(x), ldx,
+                                                                              static_cast<T *>(xs), ldxs);
+    return cudaGetLastError();
+}
+
+template <typename T, int N>
+cudaError_t launch_combine(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const float *w, int64_t ldw,
+                           const void *ys, int64_t ldys, void *y, int64_t ldy, cudaStream_t stream) {
+    constexpr int U = 2;
+    const RowArgs a = row_args(tokens, k, hidden, N, U, slot, w, ldw);
+    route_combine_kernel<T, N, U><<<row_blocks(a), kRowThreads, 0, stream>>>(a, static_cast<const T *>(ys), ldys,
+                                                                             static_cast<T *>(y), ldy);
+    return cudaGetLastError();
+}
+
+template <typename T, int N>
+cudaError_t launch_combine_backward(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const float *w,
+                                    int64_t ldw, const void *dy, int64_t lddy, const void *ys, int64_t ldys, void *dys,
+                                    int64_t lddys, float *dw, int64_t lddw, cudaStream_t stream) {
+    const RowArgs a = row_args(tokens, k, hidden, N, 1, slot, w, ldw);
+    route_combine_backward_kernel<T, N, 4><<<(unsigned)tokens, kRowThreads, 0, stream>>>(
+        a, static_cast<const T *>(dy), lddy, static_cast<const T *>(ys), ldys, static_cast<T *>(dys), lddys, dw, lddw);
+    return cudaGetLastError();
+}
+
+// Rows whose addresses all fall on 16 bytes move in 16-byte vectors, others
+// element by element.
+bool rows_wide(int64_t hidden, int size, std::initializer_list<std::pair<const void *, int64_t>> rows) {
+    if (hidden * size % 16) return false;
+    for (const auto &r : rows)
+        if (!aligned_to(r.first, 16) || r.second * size % 16) return false;
+    return true;
+}
+
+// `size`-byte elements only (dispatch copies whatever they hold)
+#define ROUTE_BY_SIZE(size, wide, F, ...)                                                     \
+    ((size) == 4 ? ((wide) ? F<float, 4>(__VA_ARGS__) : F<float, 1>(__VA_ARGS__))             \
+                 : ((wide) ? F<__half, 8>(__VA_ARGS__) : F<__half, 1>(__VA_ARGS__)))
+#define ROUTE_BY_ELEM(elem, wide, F, ...)                                                                   \
+    ((elem) == SPMV_ELEM_F32    ? ((wide) ? F<float, 4>(__VA_ARGS__) : F<float, 1>(__VA_ARGS__))            \
+     : (elem) == SPMV_ELEM_BF16 ? ((wide) ? F<__nv_bfloat16, 8>(__VA_ARGS__) : F<__nv_bfloat16, 1>(__VA_ARGS__)) \
+                                : ((wide) ? F<__half, 8>(__VA_ARGS__) : F<__half, 1>(__VA_ARGS__)))
+
+// The checks the rows' passes share; null: they hold.
+const char *rows_bad(int32_t tokens, int32_t top_k, int32_t hidden, int elem) {
+    if (tokens < 0 || top_k < 0 || hidden < 0) return "negative size";
+    if ((int64_t)tokens * top_k >= (1LL << 31)) return "tokens * top_k must be < 2^31";
+    if (!elem_ok(elem)) return "unknown element type";
+    // the passes' grids: one block per token, or eight warps of 32 elements
+    if ((int64_t)tokens * ((hidden + 31) / 32) / 8 >= (1LL << 31) - 1) return "tokens * hidden is too large";
+    return nullptr;
+}
+
+}  // namespace
+
+}  // namespace lbcsr
+
+using namespace lbcsr;
+
+extern "C" {
+
+spmv_status_t spmv_route_workspace(int32_t tokens, int32_t top_k, int32_t experts, size_t *bytes) {
+    if (!bytes) return llm_bad("bytes is NULL");
+    *bytes = 0;
+    if (tokens < 0 || top_k < 0) return llm_bad("negative size");
+    if (experts < 1 || experts > kMaxExperts) return llm_bad("experts must be in [1, 2048]");
+    const int64_t n = (int64_t)tokens * top_k;
+    if (n >= (1LL << 31)) return llm_bad("tokens * top_k must be < 2^31");
+    const int tiles = build_tiles(n);
+    *bytes = tiles > 1 ? (size_t)tiles * (experts + 1) * 4 : 0;
+    return SPMV_OK;
+}
+
+spmv_status_t spmv_route_build(int32_t tokens, int32_t top_k, int32_t experts, const void *expert_ids,
+                               int32_t id_bytes, int64_t ld_ids, int32_t *expert_ptr, int32_t *entry, int32_t *slot,
+                               void *workspace, size_t workspace_bytes, spmv_stream_t stream_handle) {
+    size_t need = 0;
+    const spmv_status_t st = spmv_route_workspace(tokens, top_k, experts, &need);
+    if (st != SPMV_OK) return st;
+    const int64_t n = (int64_t)tokens * top_k;
+    if (id_bytes != 4 && id_bytes != 8) return llm_bad("id_bytes must be 4 or 8");
+    if (!expert_ptr) return llm_bad("expert_ptr is NULL");
+    if (n > 0 && (!expert_ids || !entry || !slot)) return llm_bad("expert_ids, entry or slot is NULL");
+    if (!aligned_to(expert_ids, id_bytes)) return llm_bad("expert_ids is not aligned to its type");
+    if (need && (!workspace || workspace_bytes < need || !aligned_to(workspace, 16)))
+        return llm_bad("workspace is NULL, too small or not 16-byte aligned");
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
+    int32_t *hist = static_cast<int32_t *>(workspace);
+    const cudaError_t e =
+        id_bytes == 8 ? launch_build(n, top_k, experts, static_cast<const int64_t *>(expert_ids), ld_ids, expert_ptr,
+                                     entry, slot, hist, stream)
+                      : launch_build(n, top_k, experts, static_cast<const int32_t *>(expert_ids), ld_ids, expert_ptr,
+                                     entry, slot, hist, stream);
+    return llm_launched("spmv_route_build launch", e);
+}
+
+spmv_status_t spmv_route_dispatch(int32_t tokens, int32_t top_k, int32_t hidden, spmv_elem_t elem,
+                                  const int32_t *slot, const void *x, int64_t ldx, void *xs, int64_t ldxs,
+                                  spmv_stream_t stream_handle) {
+    if (const char *bad = rows_bad(tokens, top_k, hidden, elem)) return llm_bad(bad);
+    if (tokens == 0 || top_k == 0 || hidden == 0) return SPMV_OK;
+    if (!slot || !x || !xs) return llm_bad("slot, x or xs is NULL");
+    if (ldxs < hidden) return llm_bad("ldxs is smaller than hidden");
+    const int size = elem_size(elem);
+    if (!aligned_to(x, size) || !aligned_to(xs, size)) return llm_bad("x or xs is not aligned to its type");
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
+    const bool wide = rows_wide(hidden, size, {{x, ldx}, {xs, ldxs}});
+    return llm_launched("spmv_route_dispatch launch",
+                        ROUTE_BY_SIZE(size, wide, launch_dispatch, tokens, top_k, hidden, slot, x, ldx, xs, ldxs, stream));
+}
+
+spmv_status_t spmv_route_combine(int32_t tokens, int32_t top_k, int32_t hidden, spmv_elem_t elem,
+                                 const int32_t *slot, const float *weights, int64_t ldw, const void *ys,
+                                 int64_t ldys, void *y, int64_t ldy, spmv_stream_t stream_handle) {
+    if (const char *bad = rows_bad(tokens, top_k, hidden, elem)) return llm_bad(bad);
+    if (tokens == 0 || hidden == 0) return SPMV_OK;
+    if (!y || (top_k > 0 && (!slot || !ys))) return llm_bad("slot, ys or y is NULL");
+    if (ldy < hidden) return llm_bad("ldy is smaller than hidden");
+    const int size = elem_size(elem);
+    if (!aligned_to(ys, size) || !aligned_to(y, size)) return llm_bad("ys or y is not aligned to its type");
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
+    const bool wide = rows_wide(hidden, size, {{ys, ldys}, {y, ldy}});
+    return llm_launched("spmv_route_combine launch", ROUTE_BY_ELEM(elem, wide, launch_combine, tokens, top_k, hidden, slot,
+                                                                   weights, ldw, ys, ldys, y, ldy, stream));
+}
+
+spmv_status_t spmv_route_combine_backward(int32_t tokens, int32_t top_k, int32_t hidden, spmv_elem_t elem,
+                                          const int32_t *slot, const float *weights, int64_t ldw, const void *dy,
+                                          int64_t lddy, const void *ys, int64_t ldys, void *dys, int64_t lddys,
+                                          float *dweights, int64_t lddw, spmv_stream_t stream_handle) {
+    if (const char *bad = rows_bad(tokens, top_k, hidden, elem)) return llm_bad(bad);
+    if (tokens == 0 || top_k == 0) return SPMV_OK;
+    if (!slot || (hidden > 0 && (!dy || !dys))) return llm_bad("slot, dy or dys is NULL");
+    if (dweights && hidden > 0 && !ys) return llm_bad("ys is NULL");
+    if (lddys < hidden) return llm_bad("lddys is smaller than hidden");
+    if (dweights && lddw < top_k) return llm_bad("lddw is smaller than top_k");
+    const int size = elem_size(elem);
+    if (!aligned_to(dy, size) || !aligned_to(ys, size) || !aligned_to(dys, size))
+        return llm_bad("dy, ys or dys is not aligned to its type");
+    if (ys && ys == dys && ldys != lddys) return llm_bad("dys may be ys only with the same row stride");
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
+    const bool wide = rows_wide(hidden, size, {{dy, lddy}, {ys, dweights ? ldys : 0}, {dys, lddys}});
+    return llm_launched("spmv_route_combine_backward launch",
+                        ROUTE_BY_ELEM(elem, wide, launch_combine_backward, tokens, top_k, hidden, slot, weights, ldw, dy,
+                                      lddy, ys, ldys, dys, lddys, dweights, lddw, stream));
+}
+
+}  // extern "C"
