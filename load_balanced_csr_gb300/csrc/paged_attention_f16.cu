@@ -1,0 +1,15 @@
+// Paged attention with f16 elements (the kernel is in paged_attention.cuh).
+#include "paged_attention.cuh"
+
+namespace lbcsr {
+
+size_t attention_workspace_f16(int dim, int group, int sms) {
+    return with_mma<__half>(dim, group, [&](auto tile) { return workspace_of<decltype(tile)>(sms); });
+}
+
+cudaError_t launch_attention_f16(const spmv_paged_attention_t &a, int sms, cudaStream_t stream) {
+    return with_mma<__half>(a.head_dim, a.q_heads / a.kv_heads,
+                                  [&](auto tile) { return launch_attention<decltype(tile)>(a, sms, stream); });
+}
+
+}  // namespace lbcsr
