@@ -657,9 +657,10 @@ typedef struct {
     const int32_t *lens;
     void *out;
     float *lse;            /* [batch * q_heads], or null */
-    void *workspace;       /* spmv_paged_attention_workspace bytes, 16-byte aligned; zeroed once by
-                              the caller, every call leaves it ready for the next; calls that may
-                              overlap on the GPU need workspaces of their own */
+    void *workspace;       /* spmv_paged_attention_workspace bytes, 16-byte aligned; the first 4096
+                              are zeroed once by the caller, every call leaves them ready for the
+                              next; calls that may overlap on the GPU need workspaces of their
+                              own */
     size_t workspace_bytes;
     int32_t *status;       /* device int32; flags are OR-ed in.  Bit 0: a page outside
                               [0, num_pages) (its positions are left out); bit 1: a length that is

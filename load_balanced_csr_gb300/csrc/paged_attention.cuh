@@ -8,12 +8,13 @@
 // are powers of two.
 //
 // The work is a sparse product's with very uneven rows: row (request, kv
-// head), one unit per chunk of positions.  Units in row order are cut into
-// equal shares, one per warp, whatever the lengths (the merge-path SpMV's
-// schedule).  Each warp is a pipeline of its own: it copies its next chunks
-// into its part of shared memory (cp.async, several chunks in flight) while
-// it works on the present one, across row ends, with no barrier in the loop.
-// A row inside one share is written out by its warp; the parts of a row cut
+// head), one unit per chunk of positions and kRowCost for the row itself.
+// Units in row order are cut into equal shares whatever the lengths (the
+// merge-path SpMV's schedule), one per block, and those among the block's
+// warps.  Each warp is a pipeline of its own: it copies its next chunks into
+// its part of shared memory (cp.async, several chunks in flight) while it
+// works on the present one, across row ends, with no barrier in the loop.  A
+// row inside one share is written out by its warp; the parts of a row cut
 // between warps are records (unnormalised sums, m and l per head) that the
 // block joins in shared memory; the blocks' parts of a row cut between blocks
 // are joined, in block order, by the last of them to arrive.  The order of
@@ -40,7 +41,10 @@ cudaError_t launch_attention_f16(const spmv_paged_attention_t &a, int sms, cudaS
 namespace {
 
 constexpr int kMaxDim = 256;
-constexpr int kMaxSlice = 2048;  // requests per launch: their prefix sums live in shared memory
+constexpr int kMaxSlice = 1024;  // requests per launch: their lengths and prefix sums live in shared memory
+constexpr uint32_t kRowCost = 2;      // units a row costs beside its chunks: its queries, its output
+constexpr uint32_t kBlockRow = 32;    // rows of so few chunks are not cut between blocks,
+constexpr uint32_t kWarpRow = 4;      // of so few not between warps: joining would take longer
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -54,9 +58,10 @@ struct AttendArgs {
     float scale2;    // |scale| / ln 2
     uint32_t flip;   // sign bits of a pair of 16-bit elements, set when scale < 0: q is negated
     uint32_t page_mul, page_shift;  // t / page_size = (mulhi(t, page_mul) + t) >> page_shift
+    int32_t q_pairs, out_pairs;     // pairs of elements of q, of out, are aligned
     int32_t *arrivals;   // [blocks], zero between calls
     float *warp_rec;     // [blocks * warps] records
-    float *block_rec;    // [blocks][2] records
+    float *block_rec;    // [blocks][2] records: of the row that began earlier and ends here, of the one that goes on
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -128,11 +133,14 @@ struct TileMma {
     static constexpr int QBYTES = 0;
     static constexpr int H = GT / 8;  // heads of a lane: lane / 4 and, with 16, lane / 4 + 8
 
-    uint32_t q[DP / 16][2 * H];
+    static constexpr bool AHEAD = GT * DP <= 1024;  // registers for the next row's queries too
+
+    uint32_t q[DP / 16][2 * H], next[AHEAD ? DP / 16 : 1][2 * H];
     float o[DP / 8][4];
     float m[H], l[H];  // l: this lane's part of the sum
 
-    __device__ __forceinline__ void begin(const AttendArgs &p, int b, int h0, int heads, char *, int lane) {
+    // the queries of a row, as the product's left operand
+    __device__ __forceinline__ static void load(const AttendArgs &p, uint32_t (*to)[2 * H], int b, int h0, int heads, int lane) {
         const T *base = static_cast<const T *>(p.a.q) + b * p.a.q_stride[0] + h0 * p.a.q_stride[1];
         const int g = lane >> 2, t = (lane & 3) * 2;
 #pragma unroll
@@ -143,9 +151,31 @@ struct TileMma {
                 for (int h = 0; h < H; ++h) {
                     const int head = g + h * 8, d = s * 16 + t + r * 8;
                     const T *at = base + head * p.a.q_stride[1] + d;
-                    const bool real = head < heads && d < p.a.head_dim;
-                    q[s][r * H + h] = real ? pack2(at[0], at[1]) ^ p.flip : 0u;
+                    uint32_t pair = 0;
+                    if (head < heads && d < p.a.head_dim)
+                        pair = p.q_pairs ? *reinterpret_cast<const uint32_t *>(at) : pack2(at[0], at[1]);
+                    to[s][r * H + h] = pair;
                 }
+    }
+    // starts to load the next row's queries
+    __device__ __forceinline__ void fetch(const AttendArgs &p, int b, int h0, int heads, int lane) {
+        if (AHEAD) load(p, next, b, h0, heads, lane);
+    }
+    __device__ __forceinline__ void begin(const AttendArgs &p, int b, int h0, int heads, char *, int lane, bool fetched) {
+        if (AHEAD && fetched) {
+#pragma unroll
+            for (int s = 0; s < DP / 16; ++s)
+#pragma unroll
+                for (int r = 0; r < 2 * H; ++r) q[s][r] = next[AHEAD ? s : 0][r];
+        } else {
+            load(p, q, b, h0, heads, lane);
+        }
+        if (p.flip) {  // a pair of zeros may become a pair of negative zeros: the products stay zeros
+#pragma unroll
+            for (int s = 0; s < DP / 16; ++s)
+#pragma unroll
+                for (int r = 0; r < 2 * H; ++r) q[s][r] ^= p.flip;
+        }
 #pragma unroll
         for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
 #pragma unroll
@@ -284,17 +314,28 @@ struct TileF32 {
     static constexpr int PITCH = DP * 4 + 16;
     static constexpr int QBYTES = GT * DP * 4;
 
+    static constexpr bool AHEAD = true;
+
     float2 o[GT][DP / 64];
     float m[GT], l[GT];
+    float next[GT][DP / 32];  // the next row's queries: elements lane, lane + 32, ...
 
-    __device__ __forceinline__ void begin(const AttendArgs &p, int b, int h0, int heads, char *qs, int lane) {
+    __device__ __forceinline__ void fetch(const AttendArgs &p, int b, int h0, int heads, int lane) {
         const float *base = static_cast<const float *>(p.a.q) + b * p.a.q_stride[0] + h0 * p.a.q_stride[1];
+#pragma unroll
+        for (int g = 0; g < GT; ++g)
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i)
+                next[g][i] = g < heads && lane + 32 * i < p.a.head_dim ? base[g * p.a.q_stride[1] + lane + 32 * i] : 0.0f;
+    }
+    __device__ __forceinline__ void begin(const AttendArgs &p, int b, int h0, int heads, char *qs, int lane, bool fetched) {
+        if (!fetched) fetch(p, b, h0, heads, lane);
         float *q = reinterpret_cast<float *>(qs);
         __syncwarp();
 #pragma unroll
         for (int g = 0; g < GT; ++g) {
-            for (int d = lane; d < DP; d += 32)
-                q[g * DP + d] = g < heads && d < p.a.head_dim ? (p.flip ? -1.0f : 1.0f) * base[g * p.a.q_stride[1] + d] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i) q[g * DP + lane + 32 * i] = p.flip ? -next[g][i] : next[g][i];
 #pragma unroll
             for (int i = 0; i < DP / 64; ++i) o[g][i] = make_float2(0.0f, 0.0f);
             m[g] = -INFINITY;
@@ -379,7 +420,8 @@ struct TileF32 {
     }
 };
 
-// A record: GT rows of sums, then m and l of each head.
+// A part of a row, when the row is cut: GT rows of sums, then m and l of
+// each head.
 template <class P>
 struct Record {
     static constexpr int ROW = P::DP + 8;  // the rows' first banks differ
@@ -388,102 +430,100 @@ struct Record {
     static constexpr int WARP = P::STAGES * STAGE + P::QBYTES;          // bytes of a warp's shared memory
     static_assert(2 * FLOATS * 4 <= P::STAGES * STAGE, "both records of a warp fit its stages");
     static_assert(FLOATS % 4 == 0 && ROW % 4 == 0 && P::PITCH % 16 == 0 && P::QBYTES % 16 == 0, "16-byte accesses");
-    static constexpr int PREFIX = (4 * (kMaxSlice + 1) + 15) / 16 * 16;
+    static constexpr int PREFIX = (4 * (2 * kMaxSlice + 1) + 15) / 16 * 16;
     static constexpr int SMEM = PREFIX + P::NW * WARP;
 };
 
-// Where a warp is in its share: chunk ch of nch of row vh of request b.
-struct Place {
-    int b, vh;
-    uint32_t ch, nch;
-    int len;
+// The rows: where each request's units begin.
+struct Rows {
+    const uint32_t *pre;   // [batch + 1]
+    const int32_t *lens;   // [batch], within their tables
+    int batch, rows;       // rows: per request
+
+    // the request of unit c
+    __device__ __forceinline__ int request(uint32_t c) const {
+        int lo = 0, hi = batch - 1;  // the first with pre[b + 1] > c
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid + 1] > c) hi = mid;
+            else lo = mid + 1;
+        }
+        return lo;
+    }
+    __device__ __forceinline__ uint32_t units(int b) const { return (pre[b + 1] - pre[b]) / rows; }
+    // a cut at unit c: one inside a short row, or before a row's first chunk, moves to the row's begin
+    __device__ __forceinline__ uint32_t cut(uint32_t c, uint32_t short_row) const {
+        if (c >= pre[batch]) return pre[batch];
+        const int b = request(c);
+        const uint32_t n = units(b), u = (c - pre[b]) % n;
+        return n - kRowCost <= short_row || u <= kRowCost ? c - u : c;
+    }
 };
 
-__device__ __forceinline__ int clamped_len(const AttendArgs &p, int b) {
-    const long long most = (long long)p.a.max_pages * p.a.page_size;
-    const int len = __ldg(p.a.lens + b);
-    return len < 0 ? 0 : (int)min((long long)len, most);
-}
+// A warp's place: chunk ch of nch of row vh of request b.
+struct Place {
+    int b, vh, len;
+    uint32_t ch, nch;
 
-// The next chunk (only called while there is one).
-__device__ __forceinline__ void next_row(const AttendArgs &p, const uint32_t *pre, Place &at) {
-    at.ch = 0;
-    if (++at.vh < p.rows) return;
-    at.vh = 0;
-    do ++at.b;
-    while (pre[at.b + 1] == pre[at.b]);
-    at.nch = (pre[at.b + 1] - pre[at.b]) / p.rows;
-    at.len = clamped_len(p, at.b);
-}
+    // the chunk that a share beginning at unit c begins with; returns its unit
+    __device__ __forceinline__ uint32_t find(const Rows &r, uint32_t c) {
+        b = r.request(c);
+        const uint32_t n = r.units(b), u = (c - r.pre[b]) % n;
+        vh = (int)((c - r.pre[b]) / n);
+        nch = n - kRowCost;
+        ch = u == 0 ? 0 : u - kRowCost;
+        len = r.lens[b];
+        return c - u + kRowCost + ch;
+    }
+    // the next row (only called while there is one)
+    __device__ __forceinline__ void next_row(const Rows &r) {
+        ch = 0;
+        if (++vh < r.rows) return;
+        vh = 0;
+        do ++b;
+        while (r.pre[b + 1] == r.pre[b]);
+        nch = r.units(b) - kRowCost;
+        len = r.lens[b];
+    }
+};
 
-// Sums of records joined: record i has weight exp2(m_i - m); f gives record
-// i's floats.  Writes head g's elements d .. d + 3 through out(g, d, values,
-// l, m).
-template <class P, typename Rec, typename Out>
-__device__ __forceinline__ void join(int count, int heads, Rec rec, Out out) {
-    for (int e = threadIdx.x; e < heads * (P::DP / 4); e += P::NW * 32) {
-        const int g = e / (P::DP / 4), d = e % (P::DP / 4) * 4;
-        float m = -INFINITY;
-        for (int i = 0; i < count; ++i) m = fmaxf(m, rec(i, P::GT * Record<P>::ROW + g));
-        const float base = base_of(m);
-        float l = 0.0f;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int i = 0; i < count; ++i) {
-            const float w = pow2(rec(i, P::GT * Record<P>::ROW + g) - base);
-            l = fmaf(w, rec(i, P::GT * Record<P>::ROW + P::GT + g), l);
-            const float4 v = rec.quad(i, g * Record<P>::ROW + d);
-            sum.x = fmaf(w, v.x, sum.x), sum.y = fmaf(w, v.y, sum.y);
-            sum.z = fmaf(w, v.z, sum.z), sum.w = fmaf(w, v.w, sum.w);
-        }
-        out(g, d, sum, l, m);
+template <class P>
+__device__ __forceinline__ void write_out(const AttendArgs &p, int b, int head, int d, float x, float y, float inv) {
+    using T = typename P::T;
+    if (d >= p.a.head_dim) return;
+    T *out = static_cast<T *>(p.a.out) + b * p.a.out_stride[0] + head * p.a.out_stride[1] + d;
+    if (p.out_pairs) {
+        Vec<T, 2> v;
+        v.v[0] = from_float<T>(x * inv), v.v[1] = from_float<T>(y * inv);
+        *reinterpret_cast<Vec<T, 2> *>(out) = v;
+    } else {
+        out[0] = from_float<T>(x * inv), out[1] = from_float<T>(y * inv);
     }
 }
-
-template <class P>
-__device__ __forceinline__ void write_final(const AttendArgs &p, int b, int head, int d, const float *v, int n, float l,
-                                            float m) {
-    using T = typename P::T;
-    T *out = static_cast<T *>(p.a.out) + b * p.a.out_stride[0] + head * p.a.out_stride[1] + d;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no weight at all: zeros (a NaN stays)
-    if (d < p.a.head_dim)
-        for (int i = 0; i < n; ++i) out[i] = from_float<T>(v[i] * inv);
-    if (d == 0 && p.a.lse) p.a.lse[(int64_t)b * p.a.q_heads + head] = (m + log2f(l)) * kLn2;
+// no weight at all: zeros (a NaN stays)
+__device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ void write_lse(const AttendArgs &p, int b, int head, float m, float l) {
+    if (p.a.lse) p.a.lse[(int64_t)b * p.a.q_heads + head] = (m + log2f(l)) * kLn2;
 }
 
-// Parts of a row that a block holds, in warps first .. last.
-struct Part {
-    int first, last;
-    bool before, ended;  // the row begins in an earlier block; it ends in this one
-    int b, vh;
-};
-
+// Prefix sums of the requests' chunks into shared memory, with their lengths.
 template <class P>
-__global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendArgs p) {
-    using R = Record<P>;
-    using T = typename P::T;
+__device__ __forceinline__ Rows load_rows(const AttendArgs &p, char *smem) {
     constexpr int NT = P::NW * 32;
-    extern __shared__ __align__(16) char smem[];
     __shared__ uint32_t warp_sum[P::NW];
-    __shared__ uint32_t masks[P::NW][P::STAGES];
-    __shared__ int has[P::NW];             // bit 0: a head record, 1: a tail record, 2: its row began in an earlier warp
-    __shared__ int rows_of[P::NW][4];      // head record's request and row, tail record's
-    __shared__ Part parts[P::NW + 1];
-    __shared__ int num_parts, last_arrived[2];
-    uint32_t *pre = reinterpret_cast<uint32_t *>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    char *mine = smem + R::PREFIX + warp * R::WARP;
-    char *qs = mine + P::STAGES * R::STAGE;
-
-    // ---- prefix sums of the requests' chunks
+    uint32_t *pre = reinterpret_cast<uint32_t *>(smem);
+    int32_t *lens = reinterpret_cast<int32_t *>(smem) + kMaxSlice + 1;
     uint32_t carry = 0;
     for (int b0 = 0; b0 < p.a.batch; b0 += NT) {
         const int b = b0 + threadIdx.x;
         uint32_t n = 0;
         if (b < p.a.batch) {
-            const int len = clamped_len(p, b);
-            n = (uint32_t)((len + P::CH - 1) / P::CH) * p.rows;
-            if (blockIdx.x == 0 && len != __ldg(p.a.lens + b)) atomicOr(p.a.status, kBadLength);
+            const int given = __ldg(p.a.lens + b);
+            const int len = given < 0 ? 0 : (int)min((long long)given, (long long)p.a.max_pages * p.a.page_size);
+            if (blockIdx.x == 0 && len != given) atomicOr(p.a.status, kBadLength);
+            n = len ? ((uint32_t)((len + P::CH - 1) / P::CH) + kRowCost) * p.rows : 0;
+            lens[b] = len;
         }
         uint32_t scan = n;
 #pragma unroll
@@ -504,256 +544,355 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
         __syncthreads();
     }
     if (threadIdx.x == 0) pre[p.a.batch] = carry;
-    if (p.a.head_dim < P::DP) {  // the copies never write a row's padding: K's has to be zero
-        for (int i = lane * 16; i < P::STAGES * R::STAGE; i += 512) *reinterpret_cast<uint4 *>(mine + i) = make_uint4(0, 0, 0, 0);
-    }
     __syncthreads();
+    return Rows{pre, lens, p.a.batch, p.rows};
+}
+
+// Parts of a row that a block holds, in warps first .. last.
+struct Part {
+    int first, last;
+    bool before, ended;  // the row begins in an earlier block; it ends in this one
+    int b, vh;
+};
+
+// Joins parts: part i has weight 2^(m_i - max m), and rec(i) is its record.
+// Gives head g's elements d .. d + 3 to out(g, d, sums, m, l).
+template <class P, typename Rec, typename Out>
+__device__ __forceinline__ void join(int count, int heads, Rec rec, Out out) {
+    constexpr int BATCH = 8;  // parts read at once
+    for (int e = threadIdx.x; e < heads * (P::DP / 4); e += P::NW * 32) {
+        const int g = e / (P::DP / 4), d = e % (P::DP / 4) * 4;
+        float m = -INFINITY, l = 0.0f;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int i0 = 0; i0 < count; i0 += BATCH) {
+            float mi[BATCH], li[BATCH], top = m;
+            float4 v[BATCH];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                const auto r = rec(min(i0 + u, count - 1));
+                mi[u] = i0 + u < count ? r.one(P::GT * Record<P>::ROW + g) : -INFINITY;
+                li[u] = r.one(P::GT * Record<P>::ROW + P::GT + g);
+                v[u] = r.four(g * Record<P>::ROW + d);
+            }
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) top = fmaxf(top, mi[u]);
+            const float base = base_of(top), keep = pow2(m - base);
+            m = top;
+            l *= keep, sum.x *= keep, sum.y *= keep, sum.z *= keep, sum.w *= keep;
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                if (i0 + u >= count) break;
+                const float w = pow2(mi[u] - base);
+                l = fmaf(w, li[u], l);
+                sum.x = fmaf(w, v[u].x, sum.x), sum.y = fmaf(w, v[u].y, sum.y);
+                sum.z = fmaf(w, v[u].z, sum.z), sum.w = fmaf(w, v[u].w, sum.w);
+            }
+        }
+        out(g, d, sum, m, l);
+    }
+}
+struct SharedRecord {
+    const float *at;
+    __device__ __forceinline__ float one(int f) const { return at[f]; }
+    __device__ __forceinline__ float4 four(int f) const { return *reinterpret_cast<const float4 *>(at + f); }
+};
+struct GlobalRecord {  // written by other blocks: read past L1
+    const float *at;
+    __device__ __forceinline__ float one(int f) const { return __ldcg(at + f); }
+    __device__ __forceinline__ float4 four(int f) const { return __ldcg(reinterpret_cast<const float4 *>(at + f)); }
+};
+
+template <class P>
+__global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendArgs p) {
+    using R = Record<P>;
+    using T = typename P::T;
+    constexpr int NT = P::NW * 32;
+    constexpr uint32_t FULL = (1u << P::CH) - 1u;
+    enum { kFresh = 1 << 16, kBefore = 1 << 17, kRowEnd = 1 << 18, kShareEnd = 1 << 19 };
+    extern __shared__ __align__(16) char smem[];
+    __shared__ int3 notes[P::NW][P::STAGES];  // a stage's request, row, and mask of positions with flags
+    __shared__ int has[P::NW];                // bit 0: a head record, 1: a tail record, 2: its row began in an earlier warp
+    __shared__ int rows_of[P::NW][4];         // head record's request and row, tail record's
+    __shared__ Part parts[P::NW + 1];
+    __shared__ int num_parts, last_arrived[2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    char *mine = smem + R::PREFIX + warp * R::WARP;
+    char *qs = mine + P::STAGES * R::STAGE;
+    const Rows rows = load_rows<P>(p, smem);
     for (int b = blockIdx.x; b < p.a.batch; b += gridDim.x) {
-        if (pre[b + 1] != pre[b]) continue;  // nothing to attend to: zeros
+        if (rows.pre[b + 1] != rows.pre[b]) continue;  // nothing to attend to: zeros
         T *out = static_cast<T *>(p.a.out) + b * p.a.out_stride[0];
         for (int e = threadIdx.x; e < p.a.q_heads * p.a.head_dim; e += NT)
             out[e / p.a.head_dim * p.a.out_stride[1] + e % p.a.head_dim] = zero_of<T>();
         for (int h = threadIdx.x; p.a.lse && h < p.a.q_heads; h += NT) p.a.lse[(int64_t)b * p.a.q_heads + h] = -INFINITY;
     }
-    const uint32_t total = carry;
-    const uint32_t share = (total + gridDim.x * P::NW - 1) / (gridDim.x * P::NW);
-    const uint32_t block_share = share * P::NW;
-    if (blockIdx.x * block_share >= total) return;  // the whole block
-    const uint32_t c0 = min(blockIdx.x * block_share + warp * share, total), c1 = min(c0 + share, total);
-    const int count = (int)(c1 - c0);
+    const uint32_t total = rows.pre[p.a.batch], share = (total + gridDim.x - 1) / gridDim.x;
+    const uint32_t block0 = rows.cut(min(blockIdx.x * share, total), kBlockRow);
+    const uint32_t block1 = rows.cut(min((blockIdx.x + 1) * share, total), kBlockRow);
+    if (block0 >= block1) return;  // the whole block
+    const uint32_t warp_share = (block1 - block0 + P::NW - 1) / P::NW;
+    auto warp_cut = [&](int w) {
+        const uint32_t c = block0 + w * warp_share;
+        return w == 0 ? block0 : c >= block1 ? block1 : rows.cut(c, kWarpRow);
+    };
+    const uint32_t begin = warp_cut(warp), end = warp_cut(warp + 1);
+    if (p.a.head_dim < P::DP) {  // the copies never write a row's padding: K's has to be zero
+        for (int i = lane * 16; i < P::STAGES * R::STAGE; i += 512) *reinterpret_cast<uint4 *>(mine + i) = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+    }
 
-    // ---- this warp's share
     P tile;
-    int flags = 0;
-    if (count > 0) {
-        Place load;
-        {
-            int lo = 0, hi = p.a.batch - 1;  // the first request with pre[b + 1] > c0
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (pre[mid + 1] > c0) hi = mid;
-                else lo = mid + 1;
-            }
-            load.b = lo;
-            load.nch = (pre[lo + 1] - pre[lo]) / p.rows;
-            load.vh = (int)((c0 - pre[lo]) / load.nch);
-            load.ch = (c0 - pre[lo]) % load.nch;
-            load.len = clamped_len(p, lo);
+
+    // ---- the chunks to copy.  Under load a read takes longer than a chunk's
+    // work, so what the next copies need is read well before: the pages in
+    // batches of 32 units (a unit is a chunk where every chunk lies in one
+    // page, else a position), the next request's first batch, and the next
+    // row's queries.
+    Place load;
+    uint32_t at = 0;            // the next chunk's unit
+    int32_t pages = 0, more_pages = 0, first_pages = 0, next_request_pages = 0;
+    int base = 0;               // the first unit of `pages`
+    int fetched_b = -1, fetched_vh = 0;  // the row whose queries are on their way
+    int64_t kv_head = 0;
+    bool live = begin < end, opened = true;
+    const int tok = lane % P::CH;
+    const bool one_page = p.a.page_size % P::CH == 0;
+    const int unit = one_page ? 1 : P::CH;  // units in a chunk
+    auto page_at = [&](int pos) { return (int)((__umulhi((uint32_t)pos, p.page_mul) + (uint32_t)pos) >> p.page_shift); };
+    // this lane's entry of the batch of request b that begins at unit u
+    auto read_pages = [&](int b, int len, int u) {
+        const int64_t pos = (int64_t)(u + lane) * (one_page ? P::CH : 1);
+        return pos < len ? __ldg(p.a.table + b * p.a.table_stride + page_at((int)pos)) : -1;
+    };
+    auto read_next_request = [&] {
+        int b = load.b + 1;
+        while (b < rows.batch && rows.pre[b + 1] == rows.pre[b]) ++b;
+        next_request_pages = b < rows.batch ? read_pages(b, rows.lens[b], 0) : -1;
+    };
+    auto enter_row = [&] {
+        kv_head = load.vh / p.tiles;
+        if (P::AHEAD && fetched_b < 0) {
+            const int t = load.vh % p.tiles;
+            tile.fetch(p, load.b, (int)kv_head * p.group + t * P::GT, min(P::GT, p.group - t * P::GT), lane);
+            fetched_b = load.b, fetched_vh = load.vh;
         }
-        Place work = load;
-        const int tok = lane % P::CH;
-        const bool one_page = p.a.page_size % P::CH == 0;  // every chunk lies in one page
-        auto page_at = [&](int pos) { return (int)((__umulhi((uint32_t)pos, p.page_mul) + (uint32_t)pos) >> p.page_shift); };
-        auto page_of = [&](const Place &at) {  // this lane's position's page, -1: none
-            const int pos = (int)at.ch * P::CH + tok;
-            return pos < at.len ? __ldg(p.a.table + at.b * p.a.table_stride + page_at(pos)) : -1;
-        };
-        int32_t page = page_of(load);
-        int64_t head = load.vh / p.tiles;  // of `load`
-        // copies chunk `load` into a stage and moves `load` on; `page` was loaded one chunk ahead
-        constexpr int PER = 16 / sizeof(T), VPR = P::DP / PER;  // elements in a copy, copies in a row
-        auto copy = [&](int stage, bool more) {
-            const int first = (int)load.ch * P::CH, pos = first + tok;
-            const bool in = pos < load.len, real = (uint32_t)page < (uint32_t)p.a.num_pages;
-            const uint32_t mask = __ballot_sync(0xffffffffu, real) & ((1u << P::CH) - 1u);
-            if (lane == 0) masks[warp][stage] = mask;
-            const int inside = pos - page_at(pos) * p.a.page_size;
-            const uint32_t dst = smem_addr(mine + stage * R::STAGE);
-            if (one_page && mask == (1u << P::CH) - 1u) {
-                // the whole chunk, in one page: row r is r strides after row 0
-                const int row0 = lane / VPR, col = lane % VPR;
-                const int64_t in0 = __shfl_sync(0xffffffffu, inside, 0) + row0;
-                const T *ks = static_cast<const T *>(p.a.k_cache) + page * p.a.k_stride[0] + in0 * p.a.k_stride[1] +
-                              head * p.a.k_stride[2] + col * PER;
-                const T *vs = static_cast<const T *>(p.a.v_cache) + page * p.a.v_stride[0] + in0 * p.a.v_stride[1] +
-                              head * p.a.v_stride[2] + col * PER;
-                if (32 % VPR == 0) {
-                    constexpr int STEP = 32 / VPR > 0 ? 32 / VPR : 1;  // rows a warp copies at once
-                    const int64_t kstep = STEP * p.a.k_stride[1], vstep = STEP * p.a.v_stride[1];
-                    const uint32_t to = dst + row0 * P::PITCH + col * 16;
-                    if (col * PER < p.a.head_dim) {
+    };
+    // copies chunk `at` into a stage and moves on
+    constexpr int PER = 16 / sizeof(T), VPR = P::DP / PER;  // elements in a copy, copies in a row
+    auto copy = [&](int stage) {
+        const int pos = (int)load.ch * P::CH + tok;
+        const int32_t page = __shfl_sync(0xffffffffu, pages, (int)load.ch * unit - base + (one_page ? 0 : tok));
+        const bool in = pos < load.len, real = in && (uint32_t)page < (uint32_t)p.a.num_pages;
+        const uint32_t mask = __ballot_sync(0xffffffffu, real) & FULL;
+        const bool row_end = load.ch + 1 == load.nch;
+        if (lane == 0)
+            notes[warp][stage] = make_int3(load.b, load.vh, (int)mask | (opened || load.ch == 0 ? kFresh : 0) |
+                                           (opened && load.ch != 0 ? kBefore : 0) | (row_end ? kRowEnd : 0) |
+                                           (at + 1 == end ? kShareEnd : 0));
+        opened = false;
+        const int inside = pos - page_at(pos) * p.a.page_size;
+        const uint32_t dst = smem_addr(mine + stage * R::STAGE);
+        if (one_page && mask == FULL) {
+            // the whole chunk, in one page: row r is r strides after row 0
+            const int row0 = lane / VPR, col = lane % VPR;
+            const int64_t in0 = __shfl_sync(0xffffffffu, inside, 0) + row0;
+            const T *ks = static_cast<const T *>(p.a.k_cache) + page * p.a.k_stride[0] + in0 * p.a.k_stride[1] +
+                          kv_head * p.a.k_stride[2] + col * PER;
+            const T *vs = static_cast<const T *>(p.a.v_cache) + page * p.a.v_stride[0] + in0 * p.a.v_stride[1] +
+                          kv_head * p.a.v_stride[2] + col * PER;
+            if (32 % VPR == 0) {
+                constexpr int STEP = 32 / VPR > 0 ? 32 / VPR : 1;  // rows a warp copies at once
+                const int64_t kstep = STEP * p.a.k_stride[1], vstep = STEP * p.a.v_stride[1];
+                const uint32_t to = dst + row0 * P::PITCH + col * 16;
+                if (col * PER < p.a.head_dim) {
 #pragma unroll
-                        for (int i = 0; i < P::CH / STEP; ++i) {
-                            copy16(to + i * STEP * P::PITCH, ks, true);
-                            copy16(to + (P::CH + i * STEP) * P::PITCH, vs, true);
-                            ks += kstep, vs += vstep;
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < P::CH * VPR / 32; ++i) {
-                        const int e = lane + 32 * i, row = e / VPR, c = e % VPR;
-                        if (c * PER < p.a.head_dim) {
-                            const uint32_t to = dst + row * P::PITCH + c * 16;
-                            copy16(to, ks + (row - row0) * p.a.k_stride[1] + (c - col) * PER, true);
-                            copy16(to + P::CH * P::PITCH, vs + (row - row0) * p.a.v_stride[1] + (c - col) * PER, true);
-                        }
+                    for (int i = 0; i < P::CH / STEP; ++i) {
+                        copy16(to + i * STEP * P::PITCH, ks, true);
+                        copy16(to + (P::CH + i * STEP) * P::PITCH, vs, true);
+                        ks += kstep, vs += vstep;
                     }
                 }
             } else {
-                if (in && !real && lane < P::CH) atomicOr(p.a.status, kBadPage);
-                const int64_t pg = real ? page : 0;
-                const int64_t ko = pg * p.a.k_stride[0] + inside * p.a.k_stride[1] + head * p.a.k_stride[2];
-                const int64_t vo = pg * p.a.v_stride[0] + inside * p.a.v_stride[1] + head * p.a.v_stride[2];
 #pragma unroll
                 for (int i = 0; i < P::CH * VPR / 32; ++i) {
-                    const int e = lane + 32 * i, row = e / VPR, col = e % VPR;
-                    const int64_t kr = __shfl_sync(0xffffffffu, ko, row), vr = __shfl_sync(0xffffffffu, vo, row);
-                    const bool live = (mask >> row) & 1;
-                    if (col * PER < p.a.head_dim) {
-                        const uint32_t to = dst + row * P::PITCH + col * 16;
-                        copy16(to, static_cast<const T *>(p.a.k_cache) + (live ? kr + col * PER : 0), live);
-                        copy16(to + P::CH * P::PITCH, static_cast<const T *>(p.a.v_cache) + (live ? vr + col * PER : 0), live);
+                    const int e = lane + 32 * i, row = e / VPR, c = e % VPR;
+                    if (c * PER < p.a.head_dim) {
+                        const uint32_t to = dst + row * P::PITCH + c * 16;
+                        copy16(to, ks + (row - row0) * p.a.k_stride[1] + (c - col) * PER, true);
+                        copy16(to + P::CH * P::PITCH, vs + (row - row0) * p.a.v_stride[1] + (c - col) * PER, true);
                     }
                 }
             }
-            if (more) {
-                if (++load.ch == load.nch) {
-                    next_row(p, pre, load);
-                    head = load.vh / p.tiles;
+        } else {
+            if (in && !real && lane < P::CH) atomicOr(p.a.status, kBadPage);
+            const int64_t pg = real ? page : 0;
+            const int64_t ko = pg * p.a.k_stride[0] + inside * p.a.k_stride[1] + kv_head * p.a.k_stride[2];
+            const int64_t vo = pg * p.a.v_stride[0] + inside * p.a.v_stride[1] + kv_head * p.a.v_stride[2];
+#pragma unroll
+            for (int i = 0; i < P::CH * VPR / 32; ++i) {
+                const int e = lane + 32 * i, row = e / VPR, col = e % VPR;
+                const int64_t kr = __shfl_sync(0xffffffffu, ko, row), vr = __shfl_sync(0xffffffffu, vo, row);
+                const bool there = (mask >> row) & 1;
+                if (col * PER < p.a.head_dim) {
+                    const uint32_t to = dst + row * P::PITCH + col * 16;
+                    copy16(to, static_cast<const T *>(p.a.k_cache) + (there ? kr + col * PER : 0), there);
+                    copy16(to + P::CH * P::PITCH, static_cast<const T *>(p.a.v_cache) + (there ? vr + col * PER : 0), there);
                 }
-                page = page_of(load);
             }
-        };
-        auto begin_row = [&] {
-            const int c = work.vh / p.tiles, t = work.vh % p.tiles;
-            tile.begin(p, work.b, c * p.group + t * P::GT, min(P::GT, p.group - t * P::GT), qs, lane);
-        };
-        auto write_record = [&](float *rec) {
-            tile.sums();
-            tile.each(lane, [&](int g, int d, float x, float y, float) {
-                *reinterpret_cast<float2 *>(rec + g * R::ROW + d) = make_float2(x, y);
+        }
+        if (++at >= end) {
+            live = false;
+        } else if (row_end) {
+            at += kRowCost;
+            const int b = load.b;
+            load.next_row(rows);
+            if (load.b != b) {
+                first_pages = next_request_pages;
+                read_next_request();
+            }
+            base = 0, pages = first_pages;
+            more_pages = read_pages(load.b, load.len, 32);
+            enter_row();
+        } else {
+            ++load.ch;
+            if ((int)load.ch * unit - base == 32) {
+                base += 32, pages = more_pages;
+                more_pages = read_pages(load.b, load.len, base + 32);
+            }
+        }
+    };
+    if (live) {
+        at = load.find(rows, begin);
+        base = (int)load.ch * unit & ~31;
+        pages = read_pages(load.b, load.len, base);
+        more_pages = read_pages(load.b, load.len, base + 32);
+        first_pages = base == 0 ? pages : read_pages(load.b, load.len, 0);
+        read_next_request();
+        enter_row();
+    }
+
+    // ---- the chunks copied
+    auto write_record = [&](float *rec, int heads) {
+        tile.each(lane, [&](int g, int d, float x, float y, float) {
+            if (g < heads) *reinterpret_cast<float2 *>(rec + g * R::ROW + d) = make_float2(x, y);
+        });
+        tile.each_head(lane, [&](int g, float m, float l) {
+            rec[P::GT * R::ROW + g] = m;
+            rec[P::GT * R::ROW + P::GT + g] = l;
+        });
+    };
+    float *head_rec = p.warp_rec + (int64_t)(blockIdx.x * P::NW + warp) * R::FLOATS;
+    float *recs = reinterpret_cast<float *>(mine);  // both records, in the stages when these hold nothing any more
+    int copied = 0, flags = 0;
+#pragma unroll
+    for (int s = 0; s < P::STAGES - 1; ++s) {
+        if (live) copy(s), ++copied;
+        copy_commit();
+    }
+    bool before = false;  // the present row began in an earlier warp
+    int stage = 0;
+    for (int done = 0; done < copied; ++done) {
+        if (live) copy(stage == 0 ? P::STAGES - 1 : stage - 1), ++copied;
+        copy_commit();
+        copy_wait<P::STAGES - 1>();
+        __syncwarp();
+        const int3 note = notes[warp][stage];
+        const int c = note.y / p.tiles, t = note.y - c * p.tiles;
+        const int heads = min(P::GT, p.group - t * P::GT), h0 = c * p.group + t * P::GT;
+        if (note.z & kFresh) {
+            tile.begin(p, note.x, h0, heads, qs, lane, note.x == fetched_b && note.y == fetched_vh);
+            fetched_b = -1;
+            before = note.z & kBefore;
+        }
+        tile.chunk(p, mine + stage * R::STAGE, qs, note.z & FULL, lane);
+        __syncwarp();
+        stage = stage + 1 == P::STAGES ? 0 : stage + 1;
+        if (!(note.z & (kRowEnd | kShareEnd))) continue;
+        tile.sums();
+        if (!(note.z & kRowEnd)) {  // the last chunk
+            flags |= before ? 6 : 2;
+            if (lane == 0) rows_of[warp][2] = note.x, rows_of[warp][3] = note.y;
+            write_record(recs + R::FLOATS, heads);
+        } else if (before) {
+            flags |= 1;
+            if (lane == 0) rows_of[warp][0] = note.x, rows_of[warp][1] = note.y;
+            write_record(head_rec, heads);
+        } else {
+            tile.each(lane, [&](int g, int d, float x, float y, float l) {
+                if (g < heads) write_out<P>(p, note.x, h0 + g, d, x, y, inverse(l));
             });
             tile.each_head(lane, [&](int g, float m, float l) {
-                rec[P::GT * R::ROW + g] = m;
-                rec[P::GT * R::ROW + P::GT + g] = l;
+                if (g < heads) write_lse(p, note.x, h0 + g, m, l);
             });
-        };
-        float *head_rec = p.warp_rec + (int64_t)(blockIdx.x * P::NW + warp) * R::FLOATS;
-#pragma unroll
-        for (int s = 0; s < P::STAGES - 1; ++s) {
-            if (s < count) copy(s, s + 1 < count);
-            copy_commit();
         }
-        bool before = work.ch != 0;  // the present row began in an earlier warp
-        begin_row();
-        int stage = 0;
-        for (int i = 0; i < count; ++i) {
-            const int ahead = i + P::STAGES - 1;
-            if (ahead < count) copy(stage == 0 ? P::STAGES - 1 : stage - 1, ahead + 1 < count);
-            copy_commit();
-            copy_wait<P::STAGES - 1>();
-            __syncwarp();
-            tile.chunk(p, mine + stage * R::STAGE, qs, masks[warp][stage], lane);
-            __syncwarp();
-            stage = stage + 1 == P::STAGES ? 0 : stage + 1;
-            if (++work.ch < work.nch) continue;
-            // the row ends here
-            if (before) {
-                write_record(head_rec);
-                flags |= 1;
-                if (lane == 0) rows_of[warp][0] = work.b, rows_of[warp][1] = work.vh;
-                before = false;
-            } else {
-                const int c = work.vh / p.tiles, t = work.vh % p.tiles, h0 = c * p.group + t * P::GT;
-                const int heads = min(P::GT, p.group - t * P::GT);
-                tile.sums();
-                tile.each(lane, [&](int g, int d, float x, float y, float l) {
-                    const float v[2] = {x, y};
-                    if (g < heads && d != 0) write_final<P>(p, work.b, h0 + g, d, v, 2, l, 0.0f);
-                    else if (g < heads) {
-                        T *out = static_cast<T *>(p.a.out) + work.b * p.a.out_stride[0] + (h0 + g) * p.a.out_stride[1];
-                        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                        out[0] = from_float<T>(x * inv), out[1] = from_float<T>(y * inv);
-                    }
-                });
-                if (p.a.lse)
-                    tile.each_head(lane, [&](int g, float m, float l) {
-                        if (g < heads) p.a.lse[(int64_t)work.b * p.a.q_heads + h0 + g] = (m + log2f(l)) * kLn2;
-                    });
-            }
-            if (i + 1 < count) {
-                next_row(p, pre, work);
-                begin_row();
-            }
-        }
-        copy_wait<0>();
+    }
+    copy_wait<0>();
+    if (flags & 1) {
         __syncwarp();
-        // both records into this warp's stages, which hold nothing any more
-        float *recs = reinterpret_cast<float *>(mine);
-        if (work.ch < work.nch) {
-            flags |= before ? 6 : 2;
-            write_record(recs + R::FLOATS);
-            if (lane == 0) rows_of[warp][2] = work.b, rows_of[warp][3] = work.vh;
-        }
-        if (flags & 1) {
-            __syncwarp();
 #pragma unroll 8
-            for (int e = lane; e < R::FLOATS / 4; e += 32)
-                reinterpret_cast<float4 *>(recs)[e] = reinterpret_cast<const float4 *>(head_rec)[e];
-        }
+        for (int e = lane; e < R::FLOATS / 4; e += 32)
+            reinterpret_cast<float4 *>(recs)[e] = reinterpret_cast<const float4 *>(head_rec)[e];
     }
     if (lane == 0) has[warp] = flags;
     __syncthreads();
 
     // ---- the rows cut between this block's warps, and between blocks
     if (threadIdx.x == 0) {
-        int n = 0, open = has[0] & 5 ? 0 : -1;
-        bool before = open == 0;
+        int n = 0, open = -1, tail = 0;
+        bool from_before = false;
         for (int w = 0; w < P::NW; ++w) {
+            if (open < 0 && (has[w] & 5)) open = w, from_before = true;  // only the first warp with any chunk
             if (open >= 0 && (has[w] & 1)) {
-                parts[n++] = Part{open, w, before, true, rows_of[w][0], rows_of[w][1]};
-                open = -1, before = false;
+                parts[n++] = Part{open, w, from_before, true, rows_of[w][0], rows_of[w][1]};
+                open = -1, from_before = false;
             }
             if ((has[w] & 6) == 2) open = w;
+            if (has[w] & 2) tail = w;
         }
-        if (open >= 0) parts[n++] = Part{open, P::NW - 1, before, false, rows_of[P::NW - 1][2], rows_of[P::NW - 1][3]};
+        if (open >= 0) parts[n++] = Part{open, tail, from_before, false, rows_of[tail][2], rows_of[tail][3]};
         num_parts = n;
         last_arrived[0] = last_arrived[1] = -1;
     }
     __syncthreads();
-    struct SharedRec {
-        const char *base;
-        Part part;
-        __device__ __forceinline__ const float *at(int i) const {
-            const int w = part.first + i;
-            return reinterpret_cast<const float *>(base + w * R::WARP) + (w == part.last && part.ended ? 0 : R::FLOATS);
-        }
-        __device__ __forceinline__ float operator()(int i, int f) const { return at(i)[f]; }
-        __device__ __forceinline__ float4 quad(int i, int f) const { return *reinterpret_cast<const float4 *>(at(i) + f); }
-    };
     for (int n = 0; n < num_parts; ++n) {
         const Part part = parts[n];
         const int c = part.vh / p.tiles, t = part.vh % p.tiles, h0 = c * p.group + t * P::GT;
-        const int heads = min(P::GT, p.group - t * P::GT);
-        const SharedRec rec{smem + R::PREFIX, part};
+        const char *first = smem + R::PREFIX + part.first * R::WARP;
         float *to = p.block_rec + ((int64_t)blockIdx.x * 2 + (part.ended ? 0 : 1)) * R::FLOATS;
-        join<P>(part.last - part.first + 1, heads, rec, [&](int g, int d, float4 v, float l, float m) {
-            if (part.ended && !part.before) {
-                const float x[4] = {v.x, v.y, v.z, v.w};
-                write_final<P>(p, part.b, h0 + g, d, x, 4, l, m);
-            } else {
-                *reinterpret_cast<float4 *>(to + g * R::ROW + d) = v;
-                if (d == 0) to[P::GT * R::ROW + g] = m, to[P::GT * R::ROW + P::GT + g] = l;
-            }
-        });
+        join<P>(part.last - part.first + 1, min(P::GT, p.group - t * P::GT),
+                [&](int i) {
+                    return SharedRecord{reinterpret_cast<const float *>(first + i * R::WARP) +
+                                        (part.ended && part.first + i == part.last ? 0 : R::FLOATS)};
+                },
+                [&](int g, int d, float4 v, float m, float l) {
+                    if (part.ended && !part.before) {
+                        const float inv = inverse(l);
+                        write_out<P>(p, part.b, h0 + g, d, v.x, v.y, inv);
+                        write_out<P>(p, part.b, h0 + g, d + 2, v.z, v.w, inv);
+                        if (d == 0) write_lse(p, part.b, h0 + g, m, l);
+                    } else {
+                        *reinterpret_cast<float4 *>(to + g * R::ROW + d) = v;
+                        if (d == 0) to[P::GT * R::ROW + g] = m, to[P::GT * R::ROW + P::GT + g] = l;
+                    }
+                });
     }
     if (num_parts == 0) return;
     const bool cut_before = parts[0].before, cut_after = !parts[num_parts - 1].ended;
     if (!cut_before && !cut_after) return;
     __threadfence();
     __syncthreads();
-    auto row_blocks = [&](const Part &part, int &first, int &last) {
-        const uint32_t nch = (pre[part.b + 1] - pre[part.b]) / p.rows, start = pre[part.b] + part.vh * nch;
-        first = (int)(start / block_share);
-        last = (int)((start + nch - 1) / block_share);
+    // the blocks that hold a row's first and last chunk: cuts up to its first chunk move to its begin
+    auto blocks_of = [&](const Part &part, int &first, int &last) {
+        const uint32_t n = rows.units(part.b), start = rows.pre[part.b] + part.vh * n;
+        first = (int)((start + kRowCost) / share);
+        last = (int)((start + n - 1) / share);
     };
     if (threadIdx.x == 0) {
         for (int side = 0; side < 2; ++side) {
             const Part &part = parts[side ? num_parts - 1 : 0];
             if (side ? !cut_after || (cut_before && num_parts == 1) : !cut_before) continue;
             int first, last;
-            row_blocks(part, first, last);
+            blocks_of(part, first, last);
             if (atomicAdd(p.arrivals + first, 1) == last - first) {
                 p.arrivals[first] = 0;  // for the next call
                 last_arrived[side] = side ? num_parts - 1 : 0;
@@ -762,28 +901,20 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
         __threadfence();
     }
     __syncthreads();
-    struct GlobalRec {
-        const float *base;
-        int first, last;
-        __device__ __forceinline__ const float *at(int i) const {
-            return base + ((int64_t)(first + i) * 2 + (first + i == last ? 0 : 1)) * R::FLOATS;
-        }
-        __device__ __forceinline__ float operator()(int i, int f) const { return __ldcg(at(i) + f); }
-        __device__ __forceinline__ float4 quad(int i, int f) const {
-            return __ldcg(reinterpret_cast<const float4 *>(at(i) + f));
-        }
-    };
     for (int side = 0; side < 2; ++side) {
         if (last_arrived[side] < 0) continue;
         const Part part = parts[last_arrived[side]];
-        GlobalRec rec;
-        rec.base = p.block_rec;
-        row_blocks(part, rec.first, rec.last);
+        int first, last;
+        blocks_of(part, first, last);
         const int c = part.vh / p.tiles, t = part.vh % p.tiles, h0 = c * p.group + t * P::GT;
-        join<P>(rec.last - rec.first + 1, min(P::GT, p.group - t * P::GT), rec, [&](int g, int d, float4 v, float l, float m) {
-            const float x[4] = {v.x, v.y, v.z, v.w};
-            write_final<P>(p, part.b, h0 + g, d, x, 4, l, m);
-        });
+        join<P>(last - first + 1, min(P::GT, p.group - t * P::GT),
+                [&](int i) { return GlobalRecord{p.block_rec + ((int64_t)(first + i) * 2 + (first + i == last ? 0 : 1)) * R::FLOATS}; },
+                [&](int g, int d, float4 v, float m, float l) {
+                    const float inv = inverse(l);
+                    write_out<P>(p, part.b, h0 + g, d, v.x, v.y, inv);
+                    write_out<P>(p, part.b, h0 + g, d + 2, v.z, v.w, inv);
+                    if (d == 0) write_lse(p, part.b, h0 + g, m, l);
+                });
     }
 }
 
@@ -798,6 +929,7 @@ size_t workspace_of(int blocks) {
 template <class P>
 cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStream_t stream) {
     using R = Record<P>;
+    using T = typename P::T;
     AttendArgs p;
     p.a = a;
     p.group = a.q_heads / a.kv_heads;
@@ -805,6 +937,12 @@ cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStrea
     p.rows = a.kv_heads * p.tiles;
     p.scale2 = std::fabs(a.scale) * kLog2e;
     p.flip = a.scale < 0.0f ? 0x80008000u : 0u;
+    const int size = sizeof(T);
+    auto pairs = [&](const void *at, const int64_t *strides) {  // pairs of elements are aligned
+        return aligned_to(at, 2 * size) && strides[0] % 2 == 0 && strides[1] % 2 == 0;
+    };
+    p.q_pairs = pairs(a.q, a.q_stride);
+    p.out_pairs = pairs(a.out, a.out_stride);
     // Division by a constant d < 2^31 of t < 2^31 ("Division by Invariant Integers using Multiplication", Granlund and
     // Montgomery, 1994, section 4): with 2^s >= d > 2^(s-1) and m = floor(2^32 (2^s - d) / d) + 1,
     // t / d = (mulhi(m, t) + t) >> s; the sum stays below 2^32.
@@ -816,10 +954,9 @@ cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStrea
     p.warp_rec = reinterpret_cast<float *>(w + align16(4 * (size_t)sms));
     p.block_rec = p.warp_rec + (int64_t)sms * P::NW * R::FLOATS;
     cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::SMEM);
-    // a launch's chunks are counted in 32 bits
-    const int64_t most = ((int64_t)a.max_pages * a.page_size + P::CH - 1) / P::CH * p.rows;
+    // a launch's units are counted in 32 bits
+    const int64_t most = (((int64_t)a.max_pages * a.page_size + P::CH - 1) / P::CH + kRowCost) * p.rows;
     const int slice = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxSlice, ((1LL << 31) - 1) / std::max<int64_t>(1, most)));
-    const int size = sizeof(typename P::T);
     for (int b = 0; b < a.batch && e == cudaSuccess; b += slice) {
         p.a.batch = std::min(slice, a.batch - b);
         p.a.q = static_cast<const char *>(a.q) + (int64_t)b * a.q_stride[0] * size;
@@ -827,7 +964,7 @@ cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStrea
         p.a.lse = a.lse ? a.lse + (int64_t)b * a.q_heads : nullptr;
         p.a.table = a.table + b * a.table_stride;
         p.a.lens = a.lens + b;
-        const int64_t blocks = std::min<int64_t>(sms, std::max<int64_t>(1, (most * p.a.batch + P::NW - 1) / P::NW));
+        const int64_t blocks = std::min<int64_t>(sms, most * p.a.batch);
         paged_attention_kernel<P><<<(unsigned)blocks, P::NW * 32, R::SMEM, stream>>>(p);
         e = cudaGetLastError();
     }

@@ -142,7 +142,8 @@ class PagedAttention:
         with torch.cuda.device(self.device):
             check(self._L.spmv_paged_attention_workspace(self.max_batch, self.q_heads, self.kv_heads, self.head_dim,
                                                          a.elem, ctypes.byref(size)), "spmv_paged_attention_workspace")
-        self._workspace = torch.zeros(size.value, dtype=torch.uint8, device=self.device)
+        self._workspace = torch.empty(size.value, dtype=torch.uint8, device=self.device)
+        self._workspace[:4096].zero_()
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
         a.workspace, a.workspace_bytes, a.status = (self._workspace.data_ptr() or None, size.value,
                                                     self._status.data_ptr())
