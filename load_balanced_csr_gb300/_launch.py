@@ -33,15 +33,18 @@ def empty(stream, device, shape, dtype):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+_current_device = torch._C._cuda_getDevice
+
+
 def call(fn, what, device, *args) -> None:
     """One library call with ``device`` current; raises SpmvError."""
-    from . import check
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         status = fn(*args)
     else:
         with torch.cuda.device(device):
             status = fn(*args)
     if status:
+        from . import check
         check(status, what)
 
 
@@ -71,4 +74,4 @@ def vector(name, t, n, dtype, device):
         raise TypeError(f"{name} must be a {dtype} tensor on {device}, got {t.dtype} on {t.device}")
     if t.dim() != 1 or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of at least {n} entries")
-    return t.data_ptr() or None
+    return t.data_ptr()

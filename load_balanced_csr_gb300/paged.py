@@ -17,7 +17,7 @@ import ctypes
 
 import torch
 
-from . import _launch
+from . import _launch, check, lib
 
 __all__ = ["PageTable", "PagedAttention", "paged_store"]
 
@@ -30,13 +30,13 @@ class PageTable:
     ``positions`` (max_tokens), ``taken`` (1) and ``status`` (1)."""
 
     def __init__(self, table, page_size: int, num_pages: int, max_tokens: int):
-        from . import check, lib
         if table.dtype != torch.int32 or not table.is_cuda or table.dim() != 2:
             raise TypeError("table must be a two-dimensional CUDA int32 tensor")
         self._L, self.table, self.device = lib(), table, table.device
         self.page_size, self.num_pages, self.max_tokens = int(page_size), int(num_pages), int(max_tokens)
         self.max_requests, self.max_pages = table.shape
         self._ld = _launch.rows("table", table, table.shape, torch.int32, self.device)
+        self._table_ptr = table.data_ptr()
         size = ctypes.c_size_t()
         check(self._L.spmv_pages_workspace(self.max_requests, ctypes.byref(size)), "spmv_pages_workspace")
         int32 = dict(dtype=torch.int32, device=self.device)
@@ -45,9 +45,9 @@ class PageTable:
         self.slots, self.positions = (torch.empty(self.max_tokens, **int32) for _ in range(2))
         self.taken, self.status = torch.zeros(1, **int32), torch.zeros(1, **int32)
         self._workspace = torch.empty(size.value, dtype=torch.uint8, device=self.device)
-        self._outputs = (self._token_ptr.data_ptr(), self._lens.data_ptr() or None, self.slots.data_ptr() or None,
-                         self.positions.data_ptr() or None, self.taken.data_ptr(), self.status.data_ptr(),
-                         self._workspace.data_ptr() or None, size.value)
+        self._outputs = (self._token_ptr.data_ptr(), self._lens.data_ptr(), self.slots.data_ptr(),
+                         self.positions.data_ptr(), self.taken.data_ptr(), self.status.data_ptr(),
+                         self._workspace.data_ptr(), size.value)
         self.token_ptr = self.lens = None
         self._requests = None
 
@@ -55,18 +55,17 @@ class PageTable:
         """Add ``fresh[r]`` tokens to request r, which holds ``past[r]``
         (both int32, one entry per request of the step, in the table's row
         order); new pages come from ``free_pages`` (int32) in its order."""
-        d, n = self.device, past.numel()
+        d, n, free = self.device, past.numel(), free_pages.numel()
         if n > self.max_requests:
             raise ValueError(f"{n} requests, but the table has {self.max_requests} rows")
         if fresh.numel() != n:
             raise ValueError("past and fresh differ in length")
         past_ptr = _launch.vector("past", past, n, torch.int32, d)
         fresh_ptr = _launch.vector("fresh", fresh, n, torch.int32, d)
-        free = free_pages.numel()
         free_ptr = _launch.vector("free_pages", free_pages, free, torch.int32, d)
         _launch.call(self._L.spmv_pages_append, "spmv_pages_append", d, n, past_ptr, fresh_ptr, self.page_size,
-                     self.num_pages, free_ptr, free, self.table.data_ptr() or None, self._ld, self.max_pages,
-                     self.max_tokens, *self._outputs, _launch.handle(stream, d))
+                     self.num_pages, free_ptr, free, self._table_ptr, self._ld, self.max_pages, self.max_tokens,
+                     *self._outputs, _launch.handle(stream, d))
         if n != self._requests:
             self.token_ptr, self.lens, self._requests = self._token_ptr[:n + 1], self._lens[:n], n
         return self
@@ -83,11 +82,12 @@ def _cache_strides(name, cache, heads, dim, dtype, device):
     return strides
 
 
-def paged_store(k, v, k_cache, v_cache, slots, stream=None) -> None:
-    """Write token i's keys and values (k, v: (tokens, kv_heads, head_dim),
-    contiguous in the last dimension) into slot ``slots[i]`` (int32) of the
-    caches; slots outside the caches (-1: padding) are skipped."""
-    from . import lib
+_I64x2, _I64x3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
+
+_store_seen = {}  # the layouts that were checked last, and what the checks gave
+
+
+def _check_store(k, v, k_cache, v_cache):
     d, dtype = k.device, k.dtype
     if not k.is_cuda:
         raise TypeError("k must be a CUDA tensor")
@@ -103,15 +103,25 @@ def paged_store(k, v, k_cache, v_cache, slots, stream=None) -> None:
     vc = _cache_strides("v_cache", v_cache, heads, dim, dtype, d)
     if k_cache.shape != v_cache.shape:
         raise ValueError("k_cache and v_cache differ in shape")
-    pages, page_size = k_cache.shape[:2]
-    slots_ptr = _launch.vector("slots", slots, tokens, torch.int32, d)
-    _launch.call(lib().spmv_paged_store, "spmv_paged_store", d, tokens, heads, dim, _launch.elem(dtype), slots_ptr,
-                 pages, page_size, k.data_ptr() or None, _I64x2(*ks[:2]), v.data_ptr() or None, _I64x2(*vs[:2]),
-                 k_cache.data_ptr() or None, _I64x3(*kc[:3]), v_cache.data_ptr() or None, _I64x3(*vc[:3]),
-                 _launch.handle(stream, d))
+    return (d, (tokens, heads, dim, _launch.elem(dtype)), tuple(k_cache.shape[:2]),
+            _I64x2(*ks[:2]), _I64x2(*vs[:2]), _I64x3(*kc[:3]), _I64x3(*vc[:3]))
 
 
-_I64x2, _I64x3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
+def paged_store(k, v, k_cache, v_cache, slots, stream=None) -> None:
+    """Write token i's keys and values (k, v: (tokens, kv_heads, head_dim),
+    contiguous in the last dimension) into slot ``slots[i]`` (int32) of the
+    caches; slots outside the caches (-1: padding) are skipped."""
+    like = (k.shape, k.stride(), k.dtype, k.device, v.shape, v.stride(), v.dtype, v.device,
+            k_cache.shape, k_cache.stride(), k_cache.dtype, k_cache.device,
+            v_cache.shape, v_cache.stride(), v_cache.dtype, v_cache.device)
+    known = _store_seen.get("last")
+    if known is None or known[0] != like:
+        known = like, _check_store(k, v, k_cache, v_cache)
+        _store_seen["last"] = known
+    d, sizes, pages, ks, vs, kc, vc = known[1]
+    at = _launch.vector("slots", slots, sizes[0], torch.int32, d)
+    _launch.call(lib().spmv_paged_store, "spmv_paged_store", d, *sizes, at, *pages, k.data_ptr(), ks, v.data_ptr(), vs,
+                 k_cache.data_ptr(), kc, v_cache.data_ptr(), vc, _launch.handle(stream, d))
 
 
 class PagedAttentionArgs(ctypes.Structure):
@@ -131,7 +141,6 @@ class PagedAttention:
     overlap on the GPU (two streams) need objects of their own."""
 
     def __init__(self, max_batch: int, q_heads: int, kv_heads: int, head_dim: int, dtype, device="cuda"):
-        from . import check, lib
         self._L, self.device, self.dtype = lib(), _launch.cuda_device(device), dtype
         self._args = a = PagedAttentionArgs()
         a.elem = _launch.elem(dtype)
@@ -145,21 +154,50 @@ class PagedAttention:
         self._workspace = torch.empty(size.value, dtype=torch.uint8, device=self.device)
         self._workspace[:4096].zero_()
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
-        a.workspace, a.workspace_bytes, a.status = (self._workspace.data_ptr() or None, size.value,
+        self._like, self._scale, self._args_ref = None, self.head_dim ** -0.5, ctypes.byref(a)
+        a.workspace, a.workspace_bytes, a.status = (self._workspace.data_ptr(), size.value,
                                                     self._status.data_ptr())
 
     def __call__(self, q, k_cache, v_cache, table, lens, scale=None, out=None, lse=None, stream=None):
         """(out, lse) of q (batch, q_heads, head_dim) over the first
         ``lens[b]`` (int32) positions of each request, whose pages are row b
         of ``table`` (int32).  ``scale``: head_dim ** -0.5 if None."""
-        d, dtype, dim, hq = self.device, self.dtype, self.head_dim, self.q_heads
-        batch = q.shape[0]
-        shape = (batch, hq, dim)
+        d, a = self.device, self._args
+        like = (q.shape, q.stride(), q.dtype, q.device, k_cache.shape, k_cache.stride(), k_cache.dtype, k_cache.device,
+                v_cache.shape, v_cache.stride(), v_cache.dtype, v_cache.device, table.shape, table.stride(), table.dtype,
+                table.device, lens.shape, lens.stride(), lens.dtype, lens.device)
+        if like != self._like:
+            self._like = None
+            self._check(q, k_cache, v_cache, table, lens)
+            self._like = like
+        shape = q.shape
+        if out is None:
+            out = _launch.empty(stream, d, shape, self.dtype)
+            a.out_stride[0], a.out_stride[1] = shape[1] * shape[2], shape[2]
+        else:
+            if out.dtype != self.dtype or out.device != d or out.shape != shape or out.stride(2) != 1:
+                raise ValueError(f"out must be a {self.dtype} tensor of shape {tuple(shape)} on {d}, contiguous in its last "
+                                 "dimension")
+            a.out_stride[:] = out.stride()[:2]
+        if lse is None:
+            lse = _launch.empty(stream, d, shape[:2], torch.float32)
+        elif lse.dtype != torch.float32 or lse.device != d or lse.shape != shape[:2] or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 tensor of shape {tuple(shape[:2])} on {d}")
+        a.scale = self._scale if scale is None else scale
+        a.q, a.k_cache, a.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+        a.table, a.lens, a.out, a.lse = table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr()
+        _launch.call(self._L.spmv_paged_attention, "spmv_paged_attention", d, self._args_ref,
+                     _launch.handle(stream, d))
+        return out, lse
+
+    def _check(self, q, k_cache, v_cache, table, lens):
+        """Checks the inputs' layouts and puts them into the arguments."""
+        d, dtype, dim, hq, a = self.device, self.dtype, self.head_dim, self.q_heads, self._args
         if q.dtype != dtype or q.device != d:
             raise TypeError(f"q must be a {dtype} tensor on {d}, got {q.dtype} on {q.device}")
-        if q.shape != shape or batch > self.max_batch:
+        if q.dim() != 3 or q.shape[1:] != (hq, dim) or q.shape[0] > self.max_batch:
             raise ValueError(f"q must be (batch <= {self.max_batch}, {hq}, {dim}), got {tuple(q.shape)}")
-        qs = q.stride()
+        batch, qs = q.shape[0], q.stride()
         if qs[2] != 1:
             raise ValueError("q must have a contiguous last dimension")
         ks = _cache_strides("k_cache", k_cache, self.kv_heads, dim, dtype, d)
@@ -168,27 +206,12 @@ class PagedAttention:
             raise ValueError("k_cache and v_cache differ in shape")
         if table.dim() != 2 or table.shape[0] < batch:
             raise ValueError("table must have a row for each request")
-        a = self._args
         a.table_stride = _launch.rows("table", table, table.shape, torch.int32, d)
-        a.lens = _launch.vector("lens", lens, batch, torch.int32, d)
-        if out is None:
-            out = _launch.empty(stream, d, shape, dtype)
-        elif out.dtype != dtype or out.device != d or out.shape != shape or out.stride(2) != 1:
-            raise ValueError(f"out must be a {dtype} tensor of shape {shape} on {d}, contiguous in its last dimension")
-        if lse is None:
-            lse = _launch.empty(stream, d, shape[:2], torch.float32)
-        elif lse.dtype != torch.float32 or lse.device != d or lse.shape != shape[:2] or not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous float32 tensor of shape {shape[:2]} on {d}")
-        os = out.stride()
-        a.batch, a.scale = batch, dim ** -0.5 if scale is None else scale
+        _launch.vector("lens", lens, batch, torch.int32, d)
+        a.batch = batch
         a.num_pages, a.page_size = k_cache.shape[:2]
         a.max_pages = table.shape[1]
-        a.q_stride[:], a.k_stride[:], a.v_stride[:], a.out_stride[:] = qs[:2], ks[:3], vs[:3], os[:2]
-        a.q, a.k_cache, a.v_cache = q.data_ptr() or None, k_cache.data_ptr() or None, v_cache.data_ptr() or None
-        a.table, a.out, a.lse = table.data_ptr() or None, out.data_ptr() or None, lse.data_ptr() or None
-        _launch.call(self._L.spmv_paged_attention, "spmv_paged_attention", d, ctypes.byref(a),
-                     _launch.handle(stream, d))
-        return out, lse
+        a.q_stride[:], a.k_stride[:], a.v_stride[:] = qs[:2], ks[:3], vs[:3]
 
     def device_status(self) -> int:
         """Flags of the calls so far (0 = none); waits for the device.  Bit 0:

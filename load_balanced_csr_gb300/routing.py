@@ -42,27 +42,33 @@ class ExpertRoute:
         self._entry, self._slot = torch.empty(n, **int32), torch.empty(n, **int32)
         # fewer tokens never need more workspace
         self._workspace = torch.empty(size.value, dtype=torch.uint8, device=self.device)
-        self._pointers = (self.expert_ptr.data_ptr(), self._entry.data_ptr() or None, self._slot.data_ptr() or None,
-                          self._workspace.data_ptr() or None, size.value)
+        self._pointers = (self.expert_ptr.data_ptr(), self._entry.data_ptr(), self._slot.data_ptr(),
+                          self._workspace.data_ptr(), size.value)
         self.tokens = None
         self.entry = self.slot = None
+        # the layouts of each method's tensors that were checked last, and what the checks gave
+        self._seen = {}
 
     def build(self, expert_ids, stream=None) -> "ExpertRoute":
         """Sort the entries of ``expert_ids`` (tokens, top_k) by expert; ids
         outside [0, experts) are dropped."""
-        ids = expert_ids
-        if ids.dtype not in (torch.int32, torch.int64) or ids.device != self.device:
-            raise TypeError(f"expert_ids must be an int32 or int64 tensor on {self.device}")
-        if ids.dim() != 2 or ids.shape[1] != self.top_k or ids.shape[0] > self.max_tokens:
-            raise ValueError(f"expert_ids must be (tokens <= {self.max_tokens}, {self.top_k}), got {tuple(ids.shape)}")
-        tokens, k = ids.shape
-        ld = _launch.rows("expert_ids", ids, ids.shape, ids.dtype, self.device)
-        ptr, entry, slot, work, size = self._pointers
-        _launch.call(self._L.spmv_route_build, "spmv_route_build", self.device, tokens, k, self.experts,
-                     ids.data_ptr() or None, ids.element_size(), ld, ptr, entry, slot, work, size,
-                     _launch.handle(stream, self.device))
+        ids, d = expert_ids, self.device
+        like = (ids.shape, ids.stride(), ids.dtype, ids.device)
+        known = self._seen.get("build")
+        if known is None or known[0] != like:
+            if ids.dtype not in (torch.int32, torch.int64) or ids.device != d:
+                raise TypeError(f"expert_ids must be an int32 or int64 tensor on {d}")
+            if ids.dim() != 2 or ids.shape[1] != self.top_k or ids.shape[0] > self.max_tokens:
+                raise ValueError(f"expert_ids must be (tokens <= {self.max_tokens}, {self.top_k}), got {tuple(ids.shape)}")
+            known = like, ids.shape[0], ids.element_size(), _launch.rows("expert_ids", ids, ids.shape, ids.dtype, d)
+            self._seen["build"] = known
+        _, tokens, size, ld = known
+        ptr, entry, slot, work, room = self._pointers
+        _launch.call(self._L.spmv_route_build, "spmv_route_build", d, tokens, self.top_k, self.experts,
+                     ids.data_ptr(), size, ld, ptr, entry, slot, work, room, _launch.handle(stream, d))
         if tokens != self.tokens:
-            self.entry, self.slot = self._entry[:tokens * k], self._slot[:tokens * k].view(tokens, k)
+            n = tokens * self.top_k
+            self.entry, self.slot = self._entry[:n], self._slot[:n].view(tokens, self.top_k)
             self.tokens = tokens
         return self
 
@@ -71,35 +77,50 @@ class ExpertRoute:
             raise RuntimeError("the route has not been built")
         return self.tokens
 
+    def _rows(self, what, t, **given):
+        """The element type, hidden size and row strides of a call's tensors
+        (name=(tensor, rows), the first of which sets the type and hidden
+        size; None: to be made)."""
+        like = (t, *[(x.shape, x.stride(), x.dtype, x.device) for x, _ in given.values() if x is not None])
+        known = self._seen.get(what)
+        if known is None or known[0] != like or known[1] != len(given):
+            first, _ = next(iter(given.values()))
+            hidden = first.shape[-1] if first.dim() else 0
+            found = [_launch.elem(first.dtype), hidden]
+            for name, (x, rows) in given.items():
+                found.append(hidden if x is None else _launch.rows(name, x, (rows, hidden), first.dtype, self.device))
+            known = self._seen[what] = (like, len(given), found)
+        return known[2]
+
     def _weights(self, weights):
         if weights is None:
-            return None, 0
-        ld = _launch.rows("weights", weights, (self.tokens, self.top_k), torch.float32, self.device)
-        return weights.data_ptr() or None, ld
+            return 0, 0
+        like = (self.tokens, weights.shape, weights.stride(), weights.dtype, weights.device)
+        known = self._seen.get("weights")
+        if known is None or known[0] != like:
+            ld = _launch.rows("weights", weights, (self.tokens, self.top_k), torch.float32, self.device)
+            known = self._seen["weights"] = (like, ld)
+        return weights.data_ptr(), known[1]
 
     def dispatch(self, x, out=None, stream=None):
         """xs[p] = x[entry[p] // top_k]; rows of dropped entries are zero."""
         t, k, d = self._built(), self.top_k, self.device
-        e, hidden = _launch.elem(x.dtype), x.shape[-1]
-        ldx = _launch.rows("x", x, (t, hidden), x.dtype, d)
+        e, hidden, ldx, ldo = self._rows("dispatch" if out is None else "dispatch to", t, x=(x, t), out=(out, t * k))
         if out is None:
             out = _launch.empty(stream, d, (t * k, hidden), x.dtype)
-        ldo = _launch.rows("out", out, (t * k, hidden), x.dtype, d)
         _launch.call(self._L.spmv_route_dispatch, "spmv_route_dispatch", d, t, k, hidden, e, self._pointers[2],
-                     x.data_ptr() or None, ldx, out.data_ptr() or None, ldo, _launch.handle(stream, d))
+                     x.data_ptr(), ldx, out.data_ptr(), ldo, _launch.handle(stream, d))
         return out
 
     def combine(self, ys, weights=None, out=None, stream=None):
         """y[t] = sum over j of weights[t, j] * ys[slot[t, j]] (weights float32; None: 1)."""
         t, k, d = self._built(), self.top_k, self.device
-        e, hidden = _launch.elem(ys.dtype), ys.shape[-1]
-        ldys = _launch.rows("ys", ys, (t * k, hidden), ys.dtype, d)
+        e, hidden, ldys, ldo = self._rows("combine" if out is None else "combine to", t, ys=(ys, t * k), out=(out, t))
         w, ldw = self._weights(weights)
         if out is None:
             out = _launch.empty(stream, d, (t, hidden), ys.dtype)
-        ldo = _launch.rows("out", out, (t, hidden), ys.dtype, d)
         _launch.call(self._L.spmv_route_combine, "spmv_route_combine", d, t, k, hidden, e, self._pointers[2], w, ldw,
-                     ys.data_ptr() or None, ldys, out.data_ptr() or None, ldo, _launch.handle(stream, d))
+                     ys.data_ptr(), ldys, out.data_ptr(), ldo, _launch.handle(stream, d))
         return out
 
     def dispatch_backward(self, dxs, out=None, stream=None):
@@ -109,17 +130,15 @@ class ExpertRoute:
     def combine_backward(self, dy, ys, weights=None, out=None, dweights=None, stream=None):
         """The gradient of combine: (dys, dweights).  ``out`` may be ``ys``."""
         t, k, d = self._built(), self.top_k, self.device
-        e, hidden = _launch.elem(dy.dtype), dy.shape[-1]
-        lddy = _launch.rows("dy", dy, (t, hidden), dy.dtype, d)
-        ldys = _launch.rows("ys", ys, (t * k, hidden), dy.dtype, d)
+        e, hidden, lddy, ldys, ldo = self._rows("combine_backward" if out is None else "combine_backward to", t,
+                                                dy=(dy, t), ys=(ys, t * k), out=(out, t * k))
         w, ldw = self._weights(weights)
         if out is None:
             out = _launch.empty(stream, d, (t * k, hidden), dy.dtype)
         if dweights is None:
             dweights = _launch.empty(stream, d, (t, k), torch.float32)
-        ldo = _launch.rows("out", out, (t * k, hidden), dy.dtype, d)
         lddw = _launch.rows("dweights", dweights, (t, k), torch.float32, d)
         _launch.call(self._L.spmv_route_combine_backward, "spmv_route_combine_backward", d, t, k, hidden, e,
-                     self._pointers[2], w, ldw, dy.data_ptr() or None, lddy, ys.data_ptr() or None, ldys,
-                     out.data_ptr() or None, ldo, dweights.data_ptr() or None, lddw, _launch.handle(stream, d))
+                     self._pointers[2], w, ldw, dy.data_ptr(), lddy, ys.data_ptr(), ldys, out.data_ptr(), ldo,
+                     dweights.data_ptr(), lddw, _launch.handle(stream, d))
         return out, dweights
