@@ -583,7 +583,7 @@ spmv_status_t spmv_pages_workspace(int32_t requests, size_t *bytes);
  *   positions[max_tokens]    each new token's position in its request;
  *   slots[max_tokens]        page * page_size + position % page_size;
  *   taken[1]                 how many of free_pages are used up (a prefix);
- *   status[1]                0, or the flags below.
+ *   status[1]                the flags below, OR-ed into what it holds.
  * Entries of slots and positions past the last new token are set to -1.  A
  * request that does not fit whole (the free list ends, the row would be
  * longer than max_pages, or its new tokens end past max_tokens) is not

@@ -182,7 +182,7 @@ struct TileMma {
         for (int h = 0; h < H; ++h) m[h] = -INFINITY, l[h] = 0.0f;
     }
 
-    __device__ __forceinline__ void chunk(const AttendArgs &p, const char *stage, const char *, uint32_t mask, int lane) {
+    __device__ __forceinline__ void chunk(const AttendArgs &p, const char *stage, char *, uint32_t mask, int lane) {
         const uint32_t ks = smem_addr(stage), vs = ks + CH * PITCH;
         const int r8 = lane & 7, mat = lane >> 3;
         // scores of positions 0-7 and 8-15, each in two sums that do not wait for one another
@@ -312,13 +312,16 @@ struct TileF32 {
     using T = float;
     static constexpr int DP = DP_, NW = NW_, STAGES = STAGES_, GT = GT_, CH = 8;
     static constexpr int PITCH = DP * 4 + 16;
-    static constexpr int QBYTES = GT * DP * 4;
-
+    static constexpr int WEIGHTS = GT * DP * 4;                // offset of the weights of a chunk behind the queries
+    static constexpr int QBYTES = WEIGHTS + GT * CH * 4;
     static constexpr bool AHEAD = true;
+    static constexpr int PAIRS = (DP + 63) / 64;               // pairs of elements of a lane; the last may not exist
 
-    float2 o[GT][DP / 64];
-    float m[GT], l[GT];
+    float2 o[GT][PAIRS];
+    float m[GT], l[GT];       // l: this lane's part of the sum
     float next[GT][DP / 32];  // the next row's queries: elements lane, lane + 32, ...
+
+    __device__ __forceinline__ static bool has_pair(int lane, int i) { return DP % 64 == 0 || 2 * (lane + 32 * i) < DP; }
 
     __device__ __forceinline__ void fetch(const AttendArgs &p, int b, int h0, int heads, int lane) {
         const float *base = static_cast<const float *>(p.a.q) + b * p.a.q_stride[0] + h0 * p.a.q_stride[1];
@@ -337,65 +340,84 @@ struct TileF32 {
 #pragma unroll
             for (int i = 0; i < DP / 32; ++i) q[g * DP + lane + 32 * i] = p.flip ? -next[g][i] : next[g][i];
 #pragma unroll
-            for (int i = 0; i < DP / 64; ++i) o[g][i] = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < PAIRS; ++i) o[g][i] = make_float2(0.0f, 0.0f);
             m[g] = -INFINITY;
             l[g] = 0.0f;
         }
         __syncwarp();
     }
 
-    __device__ __forceinline__ void chunk(const AttendArgs &p, const char *stage, const char *qs, uint32_t mask, int lane) {
+    __device__ __forceinline__ void chunk(const AttendArgs &p, const char *stage, char *qs, uint32_t mask, int lane) {
         const int pos = lane & 7, quarter = lane >> 3;
         const float4 *k = reinterpret_cast<const float4 *>(stage + pos * PITCH) + quarter * (DP / 16);
         const float4 *q = reinterpret_cast<const float4 *>(qs) + quarter * (DP / 16);
-        float s[GT];
+        float s[GT], s2[GT], top[GT];
 #pragma unroll
-        for (int g = 0; g < GT; ++g) s[g] = 0.0f;
+        for (int g = 0; g < GT; ++g) s[g] = s2[g] = 0.0f;
 #pragma unroll
         for (int i = 0; i < DP / 16; ++i) {
             const float4 kv = k[i];
 #pragma unroll
             for (int g = 0; g < GT; ++g) {
                 const float4 qv = q[g * (DP / 4) + i];
-                s[g] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[g]))));
+                s[g] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, s[g]));
+                s2[g] = fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s2[g]));
             }
         }
-        float pr[GT];
+        const bool live = (mask >> pos) & 1;
+#pragma unroll
+        for (int g = 0; g < GT; ++g) s[g] += s2[g];
+#pragma unroll
+        for (int d = 8; d < 32; d <<= 1)
+#pragma unroll
+            for (int g = 0; g < GT; ++g) s[g] += __shfl_xor_sync(0xffffffffu, s[g], d);
+#pragma unroll
+        for (int g = 0; g < GT; ++g) top[g] = live ? s[g] : -INFINITY;
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+            for (int g = 0; g < GT; ++g) top[g] = fmaxf(top[g], __shfl_xor_sync(0xffffffffu, top[g], d));
+        bool higher = false;  // the same on every lane
 #pragma unroll
         for (int g = 0; g < GT; ++g) {
-            s[g] += __shfl_xor_sync(0xffffffffu, s[g], 8);
-            s[g] += __shfl_xor_sync(0xffffffffu, s[g], 16);
-            const bool live = (mask >> pos) & 1;
-            float top = live ? s[g] : -INFINITY;
+            top[g] = fmaxf(m[g], top[g] * p.scale2);
+            higher |= top[g] > m[g];
+        }
+        if (higher) {
 #pragma unroll
-            for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            top = fmaxf(m[g], top * p.scale2);
-            const float base = base_of(top);
-            if (top > m[g]) {  // the same on every lane
-                const float keep = pow2(m[g] - base);
+            for (int g = 0; g < GT; ++g) {
+                const float keep = pow2(m[g] - base_of(top[g]));
                 l[g] *= keep;
 #pragma unroll
-                for (int i = 0; i < DP / 64; ++i) o[g][i].x *= keep, o[g][i].y *= keep;
-                m[g] = top;
+                for (int i = 0; i < PAIRS; ++i) o[g][i].x *= keep, o[g][i].y *= keep;
+                m[g] = top[g];
             }
-            pr[g] = live ? pow2(fmaf(s[g], p.scale2, -base)) : 0.0f;
-            if (quarter == 0) l[g] += pr[g];
         }
+        float *weights = reinterpret_cast<float *>(qs + WEIGHTS);  // [position][head]
+        float own = 0.0f;
+#pragma unroll
+        for (int g = 0; g < GT; ++g) {
+            const float w = live ? pow2(fmaf(s[g], p.scale2, -base_of(m[g]))) : 0.0f;
+            if (quarter == 0) l[g] += w;
+            if (quarter == g) own = w;
+        }
+        if (quarter < GT) weights[pos * GT + quarter] = own;
+        __syncwarp();
         const char *v = stage + CH * PITCH;
 #pragma unroll
         for (int t = 0; t < CH; ++t) {
-            float2 vv[DP / 64];
+            float2 vv[PAIRS];
 #pragma unroll
-            for (int i = 0; i < DP / 64; ++i) vv[i] = reinterpret_cast<const float2 *>(v + t * PITCH)[lane + 32 * i];
+            for (int i = 0; i < PAIRS; ++i)
+                vv[i] = has_pair(lane, i) ? reinterpret_cast<const float2 *>(v + t * PITCH)[lane + 32 * i] : make_float2(0.0f, 0.0f);
+            const Vec<float, GT> w = *reinterpret_cast<const Vec<float, GT> *>(weights + t * GT);
 #pragma unroll
-            for (int g = 0; g < GT; ++g) {
-                const float w = __shfl_sync(0xffffffffu, pr[g], t);
+            for (int g = 0; g < GT; ++g)
 #pragma unroll
-                for (int i = 0; i < DP / 64; ++i) {
-                    o[g][i].x = fmaf(w, vv[i].x, o[g][i].x);
-                    o[g][i].y = fmaf(w, vv[i].y, o[g][i].y);
+                for (int i = 0; i < PAIRS; ++i) {
+                    o[g][i].x = fmaf(w.v[g], vv[i].x, o[g][i].x);
+                    o[g][i].y = fmaf(w.v[g], vv[i].y, o[g][i].y);
                 }
-            }
         }
     }
 
@@ -410,7 +432,8 @@ struct TileF32 {
 #pragma unroll
         for (int g = 0; g < GT; ++g)
 #pragma unroll
-            for (int i = 0; i < DP / 64; ++i) f(g, 64 * i + 2 * lane, o[g][i].x, o[g][i].y, l[g]);
+            for (int i = 0; i < PAIRS; ++i)
+                if (has_pair(lane, i)) f(g, 64 * i + 2 * lane, o[g][i].x, o[g][i].y, l[g]);
     }
     template <typename F>
     __device__ __forceinline__ void each_head(int lane, F f) const {

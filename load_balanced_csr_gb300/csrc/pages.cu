@@ -2,14 +2,17 @@
 //
 // spmv_pages_append: with held_r = ceil(past_r / P), a prefix sum over the
 // requests of (fresh_r, pages needed) gives each new token's place and each
-// new page's place in the free list; then one thread per new token finds its
-// request by binary search in the prefix sums (as a merge-path tile finds its
-// first row), computes its slot from the table or, for a page not held
-// before, from the free list, and the token that opens a page writes the
-// table's entry.
+// new page's place in the free list; then each token finds its request by
+// binary search in the prefix sums (as a merge-path tile finds its first
+// row), computes its slot from the table or, for a page not held before, from
+// the free list, and the token that opens a page writes the table's entry.
+// It is bound by latency: up to kBlockRequests requests every block makes the
+// prefix sums for itself in shared memory, and there is one launch; beyond,
+// one block makes them in global memory first.
 #include <algorithm>
 #include <climits>
 
+#include "internal.cuh"
 #include "llm.cuh"
 
 namespace lbcsr {
@@ -17,10 +20,17 @@ namespace lbcsr {
 namespace {
 
 // ---------------------------------------------------------------- append
-constexpr int kScanThreads = 1024;
-constexpr int kExpandThreads = 256;
+constexpr int kAppendThreads = 512;
+constexpr int kTokensPerThread = 4;    // consecutive, so that they are stored together
+constexpr int kBlockRequests = 4096;
 
 enum { kFreeEnded = 1, kRowShort = 2, kTooManyTokens = 4, kBadLength = 8, kBadPage = 16 };
+
+// What the prefix sums leave of a request: where its new tokens begin, what it
+// held, the place of its first new page in the free list (-1: not served).
+struct Request {
+    int32_t token, past, first;
+};
 
 struct AppendArgs {
     int32_t requests, page, num_pages, num_free, max_pages, max_tokens;
@@ -28,17 +38,22 @@ struct AppendArgs {
     int32_t *table;
     int64_t ld_table;
     int32_t *token_ptr, *lens, *slots, *positions, *taken, *status;
-    int32_t *first;  // workspace [requests]: place of the request's first new page in the free list,
-                     // -1: not served
+    Request *made;  // workspace [requests], more than kBlockRequests only
 };
 
-__global__ void __launch_bounds__(kScanThreads) pages_scan_kernel(AppendArgs a) {
-    __shared__ long long warp_sum[kScanThreads / 32];
+__device__ __forceinline__ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Fills req[0 .. requests] (the last one's token: the number of new tokens);
+// the block that `writes` also gives the outputs per request.
+__device__ __forceinline__ void scan_requests(const AppendArgs &a, Request *req, bool writes) {
+    __shared__ long long warp_sum[kAppendThreads / 32];
+    __shared__ int32_t all_used;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long carry = 0;  // pages << 32 | tokens
     int32_t flags = 0, used = 0;
-    for (int r0 = 0; r0 < a.requests; r0 += kScanThreads) {
-        const int r = r0 + threadIdx.x;
+    if (threadIdx.x == 0) all_used = 0;
+    for (int64_t r0 = 0; r0 < a.requests; r0 += kAppendThreads) {
+        const int64_t r = r0 + threadIdx.x;
         int32_t past = 0, fresh = 0, need = 0;
         bool fits = true;
         if (r < a.requests) {
@@ -61,7 +76,7 @@ __global__ void __launch_bounds__(kScanThreads) pages_scan_kernel(AppendArgs a) 
         __syncthreads();
         long long start = carry + scan - mine;
 #pragma unroll
-        for (int w = 0; w < kScanThreads / 32; ++w) {
+        for (int w = 0; w < kAppendThreads / 32; ++w) {
             const long long s = warp_sum[w];
             if (w < warp) start += s;
             carry += s;
@@ -72,53 +87,78 @@ __global__ void __launch_bounds__(kScanThreads) pages_scan_kernel(AppendArgs a) 
             if (need > 0 && (long long)first + need > a.num_free) served = false, flags |= kFreeEnded;
             if (fresh > 0 && (long long)tokens + fresh > a.max_tokens) served = false, flags |= kTooManyTokens;
             if (served && need > 0) used = max(used, first + need);
-            a.token_ptr[r] = tokens;
-            a.lens[r] = served ? past + fresh : past;
-            a.first[r] = served ? first : -1;
+            req[r] = Request{tokens, past, served ? first : -1};
+            if (writes) a.token_ptr[r] = tokens, a.lens[r] = served ? past + fresh : past;
         }
         __syncthreads();
     }
-    __shared__ int32_t all_flags, all_used;
-    if (threadIdx.x == 0) all_flags = 0, all_used = 0, a.token_ptr[a.requests] = (int32_t)carry;
+    if (threadIdx.x == 0) req[a.requests].token = (int32_t)carry;
     __syncthreads();
-    if (flags) atomicOr(&all_flags, flags);
-    if (used) atomicMax(&all_used, used);
-    __syncthreads();
-    if (threadIdx.x == 0) *a.status = all_flags, *a.taken = all_used;
+    if (writes) {
+        if (flags) atomicOr(a.status, flags);
+        if (used) atomicMax(&all_used, used);
+        __syncthreads();
+        if (threadIdx.x == 0) a.token_ptr[a.requests] = (int32_t)carry, *a.taken = all_used;
+    }
 }
 
-__global__ void __launch_bounds__(kExpandThreads) pages_expand_kernel(AppendArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * kExpandThreads + threadIdx.x;
-    if (i >= a.max_tokens) return;
-    if (i >= a.token_ptr[a.requests]) {
-        a.slots[i] = -1, a.positions[i] = -1;
-        return;
+__global__ void __launch_bounds__(kAppendThreads) pages_scan_kernel(AppendArgs a) { scan_requests(a, a.made, true); }
+
+// SCAN: the block makes the prefix sums itself.
+template <bool SCAN>
+__global__ void __launch_bounds__(kAppendThreads) pages_append_kernel(AppendArgs a) {
+    extern __shared__ __align__(16) char smem[];
+    const Request *req = a.made;
+    if (SCAN) {
+        scan_requests(a, reinterpret_cast<Request *>(smem), blockIdx.x == 0);
+        req = reinterpret_cast<const Request *>(smem);
     }
-    int lo = 0, hi = a.requests - 1;  // the last request with token_ptr[r] <= i: the one that holds i
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.token_ptr[mid] <= i) lo = mid;
-        else hi = mid - 1;
+    const int32_t tokens = min(req[a.requests].token, a.max_tokens);
+    const bool whole = aligned16(a.slots) && aligned16(a.positions);
+    for (int64_t i0 = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) * kTokensPerThread; i0 < a.max_tokens;
+         i0 += (int64_t)gridDim.x * kAppendThreads * kTokensPerThread) {
+        int r = 0;
+        if (i0 < tokens) {
+            int hi = a.requests - 1;  // the last request with token <= i0: the one that holds i0
+            while (r < hi) {
+                const int mid = (r + hi + 1) >> 1;
+                if (req[mid].token <= i0) r = mid;
+                else hi = mid - 1;
+            }
+        }
+        int32_t slot[kTokensPerThread], position[kTokensPerThread];
+#pragma unroll
+        for (int u = 0; u < kTokensPerThread; ++u) {
+            const int64_t i = i0 + u;
+            slot[u] = position[u] = -1;
+            if (i >= tokens) continue;
+            while (r + 1 < a.requests && req[r + 1].token <= i) ++r;
+            const Request now = req[r];
+            const int32_t at = now.past + (int32_t)(i - now.token), page = at / a.page, inside = at - page * a.page;
+            position[u] = at;
+            if (now.first < 0 || at < 0 || page >= a.max_pages) continue;  // the last two only if sums passed 32 bits
+            const int32_t held = (int32_t)(((long long)now.past + a.page - 1) / a.page);
+            const int64_t place = (int64_t)now.first + page - held;
+            int32_t *entry = a.table + r * a.ld_table + page;
+            int32_t id = -1;
+            if (page < held) {
+                id = *entry;
+            } else if (place < a.num_free) {
+                id = __ldg(a.free_pages + place);
+                if (inside == 0) *entry = id;
+            }
+            if ((uint32_t)id < (uint32_t)a.num_pages) slot[u] = id * a.page + inside;
+            else atomicOr(a.status, kBadPage);
+        }
+        if (whole && i0 + kTokensPerThread <= a.max_tokens) {
+            *reinterpret_cast<int4 *>(a.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4 *>(a.positions + i0) = make_int4(position[0], position[1], position[2], position[3]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kTokensPerThread; ++u)
+                if (i0 + u < a.max_tokens) a.slots[i0 + u] = slot[u], a.positions[i0 + u] = position[u];
+        }
     }
-    const int32_t past = max(a.past[lo], 0), at = past + (int32_t)(i - a.token_ptr[lo]);
-    const int32_t first = a.first[lo], page = at / a.page, inside = at - page * a.page;
-    a.positions[i] = at;
-    if (first < 0 || i - a.token_ptr[lo] >= a.fresh[lo]) {  // the latter only if the sums passed 32 bits
-        a.slots[i] = -1;
-        return;
-    }
-    const int32_t held = (int32_t)(((long long)past + a.page - 1) / a.page);
-    int32_t *entry = a.table + lo * a.ld_table + page;
-    int32_t id;
-    if (page < held) {
-        id = *entry;
-    } else {
-        id = a.free_pages[first + page - held];
-        if (inside == 0) *entry = id;
-    }
-    const bool good = id >= 0 && id < a.num_pages;
-    if (!good) atomicOr(a.status, kBadPage);
-    a.slots[i] = good ? id * a.page + inside : -1;
 }
 
 // ---------------------------------------------------------------- store
@@ -179,7 +219,7 @@ spmv_status_t spmv_pages_workspace(int32_t requests, size_t *bytes) {
     if (!bytes) return llm_bad("bytes is NULL");
     *bytes = 0;
     if (requests < 0) return llm_bad("negative size");
-    *bytes = 4 * (size_t)requests;
+    *bytes = requests > kBlockRequests ? sizeof(Request) * ((size_t)requests + 1) : 0;
     return SPMV_OK;
 }
 
@@ -209,14 +249,26 @@ spmv_status_t spmv_pages_append(int32_t requests, const int32_t *past, const int
     a.table = table, a.ld_table = ld_table;
     a.token_ptr = token_ptr, a.lens = lens, a.slots = slots, a.positions = positions, a.taken = taken;
     a.status = status;
-    a.first = static_cast<int32_t *>(workspace);
+    a.made = static_cast<Request *>(workspace);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
-    pages_scan_kernel<<<1, kScanThreads, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && max_tokens > 0) {
-        pages_expand_kernel<<<(unsigned)(((int64_t)max_tokens + kExpandThreads - 1) / kExpandThreads), kExpandThreads, 0,
-                              stream>>>(a);
+    const int64_t per_block = (int64_t)kAppendThreads * kTokensPerThread;
+    const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>((max_tokens + per_block - 1) / per_block, 2 * device_sm_count()));
+    cudaError_t e = cudaSuccess;
+    if (requests <= kBlockRequests) {
+        const size_t smem = sizeof(Request) * ((size_t)requests + 1);
+        if (smem > 47 * 1024)
+            e = cudaFuncSetAttribute(pages_append_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess) {
+            pages_append_kernel<true><<<blocks, kAppendThreads, smem, stream>>>(a);
+            e = cudaGetLastError();
+        }
+    } else {
+        pages_scan_kernel<<<1, kAppendThreads, 0, stream>>>(a);
         e = cudaGetLastError();
+        if (e == cudaSuccess && max_tokens > 0) {
+            pages_append_kernel<false><<<blocks, kAppendThreads, 0, stream>>>(a);
+            e = cudaGetLastError();
+        }
     }
     return llm_launched("spmv_pages_append launch", e);
 }

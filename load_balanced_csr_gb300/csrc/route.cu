@@ -15,22 +15,36 @@
 // rows pass.
 #include <algorithm>
 
+#include <cooperative_groups.h>
+
 #include "llm.cuh"
 
 namespace lbcsr {
 
+namespace cg = cooperative_groups;
+
 namespace {
 
 // ---------------------------------------------------------------- build
-constexpr int kBuildThreads = 512;
+// Bound by latency: the ids are read once into registers, up to eight per
+// thread, and ranked twice from there (counts per warp and expert, then
+// positions).  Up to 131,072 entries are sorted by one launch of one cluster
+// of up to 16 blocks, which read one another's counts in shared memory; more by two
+// launches, the first of which counts.
+constexpr int kBuildThreads = 1024;
 constexpr int kBuildWarps = kBuildThreads / 32;
+constexpr int kBuildKeys = 8;                               // ids of a thread at a time
+constexpr int kBuildTile = kBuildThreads * kBuildKeys;      // entries of a block at a time
+constexpr int kBuildCluster = 16;
 constexpr int kMaxExperts = 2048;
-constexpr int kMaxTiles = 152;      // one tile per SM at most
-constexpr int kMinTile = 4096;      // entries
+constexpr int kMaxTiles = 152;                              // one tile per SM at most
 
+bool build_clustered(int64_t n) { return n <= (int64_t)kBuildCluster * kBuildTile; }
+// Entries of a block: in a cluster, spread over as many blocks as there are whole warps' loads for; else whole
+// rounds of kBuildTile.
 int64_t build_tile(int64_t n) {
-    const int64_t t = std::max<int64_t>((n + kMaxTiles - 1) / kMaxTiles, kMinTile);
-    return (t + kBuildThreads - 1) / kBuildThreads * kBuildThreads;
+    const int64_t blocks = build_clustered(n) ? kBuildCluster : kMaxTiles, step = build_clustered(n) ? kBuildThreads : kBuildTile;
+    return std::max<int64_t>(step, (n + blocks * step - 1) / (blocks * step) * step);
 }
 int build_tiles(int64_t n) { return (int)std::max<int64_t>(1, (n + build_tile(n) - 1) / build_tile(n)); }
 
@@ -38,6 +52,23 @@ template <typename I>
 __device__ __forceinline__ int key_of(const I *__restrict__ ids, int64_t ld, int k, int experts, int64_t i) {
     const I id = ld == k ? ids[i] : ids[(i / k) * ld + i % k];
     return id >= 0 && id < (I)experts ? (int)id : experts;  // the last bin: dropped
+}
+
+// The lanes whose key is this lane's, from one vote per bit of the keys
+// (measured on 8,192 entries a block and 129 bins: the warp's match
+// instruction takes about 210 clocks, more with more distinct keys; eight
+// votes about 60).
+__device__ __forceinline__ unsigned same_key(int key, int bits) {
+    unsigned peers = 0xffffffffu;
+    for (int b = 0; b < bits; b += 4) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const bool one = (key >> (b + u)) & 1;
+            const unsigned vote = __ballot_sync(0xffffffffu, one);
+            peers &= one ? vote : ~vote;
+        }
+    }
+    return peers;
 }
 
 // hist[tile * (experts + 1) + bin]: entries of the tile in each bin
@@ -50,96 +81,142 @@ route_hist_kernel(const I *__restrict__ ids, int64_t ld, int k, int64_t n, int e
     for (int b = threadIdx.x; b < bins; b += kBuildThreads) h[b] = 0;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * tile, t1 = min(t0 + tile, n);
+#pragma unroll 4
     for (int64_t i = t0 + threadIdx.x; i < t1; i += kBuildThreads) atomicAdd(&h[key_of(ids, ld, k, experts, i)], 1);
     __syncthreads();
     for (int b = threadIdx.x; b < bins; b += kBuildThreads) hist[(int64_t)blockIdx.x * bins + b] = h[b];
 }
 
-// Ranks of one tile.  Each warp owns a run of consecutive entries; base[w][b]
-// becomes the position of warp w's first entry in bin b: the bin's start,
-// plus the earlier tiles' counts, plus the earlier warps'.
+// Positions of one tile.  Each warp owns a run of consecutive entries.
+// counts[w][b]: the entries of bin b in warp w's run, then in the earlier
+// warps' runs (a round has at most kBuildTile entries: 16 bits); base[b]: the
+// position of the block's first entry in bin b, that is the bin's begin plus
+// the earlier blocks' entries.  hist is null in a cluster.
 template <typename I>
 __global__ void __launch_bounds__(kBuildThreads)
 route_rank_kernel(const I *__restrict__ ids, int64_t ld, int k, int64_t n, int experts, int64_t tile, int tiles,
                   const int32_t *__restrict__ hist, int32_t *__restrict__ expert_ptr, int32_t *__restrict__ entry,
                   int32_t *__restrict__ slot) {
-    extern __shared__ int32_t base[];  // [warps][bins]
+    extern __shared__ int32_t smem[];
     __shared__ int32_t warp_sum[kBuildWarps];
-    const int bins = experts + 1;
+    const int bins = experts + 1, bits = 32 - __clz(bins);  // keys, and `bins` for no entry
+    int32_t *base = smem, *total = smem + bins, *sum = smem + 2 * bins;
+    uint16_t *counts = reinterpret_cast<uint16_t *>(smem + 3 * bins);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t0 = (int64_t)blockIdx.x * tile;
-    const int64_t run = ((tile + kBuildWarps - 1) / kBuildWarps + 31) / 32 * 32;
-    const int64_t w0 = t0 + warp * run, w1 = min(min(w0 + run, t0 + tile), n);
-    int32_t *mine = base + warp * bins;
-    for (int b = lane; b < bins; b += 32) mine[b] = 0;
-    __syncwarp();
-    for (int64_t i0 = w0; i0 < w1; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int key = i < w1 ? key_of(ids, ld, k, experts, i) : bins;
-        const unsigned peers = __match_any_sync(0xffffffffu, key);
-        if (i < w1 && lane == __ffs(peers) - 1) mine[key] += __popc(peers);
-        __syncwarp();
-    }
-    __syncthreads();
-    // bins in blocks of one per thread; carry: the entries of earlier blocks
-    int32_t carry = 0;
-    for (int b0 = 0; b0 < bins; b0 += kBuildThreads) {
-        const int b = b0 + threadIdx.x;
-        int32_t total = 0, before = 0;
-        if (b < bins) {
-            if (tiles == 1) {
-                for (int w = 0; w < kBuildWarps; ++w) total += base[w * bins + b];
-            } else {
-#pragma unroll 8
-                for (int t = 0; t < tiles; ++t) {
-                    const int32_t c = __ldg(hist + (int64_t)t * bins + b);
-                    total += c;
-                    if (t < blockIdx.x) before += c;
-                }
-            }
-        }
-        // exclusive prefix sum of the totals over the block's threads
-        int32_t scan = total;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int32_t up = __shfl_up_sync(0xffffffffu, scan, d);
-            if (lane >= d) scan += up;
-        }
-        if (lane == 31) warp_sum[warp] = scan;
-        __syncthreads();
-        int32_t start = carry + scan - total, all = 0;
-#pragma unroll
-        for (int w = 0; w < kBuildWarps; ++w) {
-            const int32_t s = warp_sum[w];
-            if (w < warp) start += s;
-            all += s;
-        }
-        carry += all;
-        if (b < bins) {
-            if (blockIdx.x == 0) expert_ptr[b] = start;  // bin `experts` starts where the experts end
-            int32_t at = start + before;
-            for (int w = 0; w < kBuildWarps; ++w) {
-                const int32_t c = base[w * bins + b];
-                base[w * bins + b] = at;
-                at += c;
-            }
-        }
-        __syncthreads();
-    }
     const unsigned lt = (1u << lane) - 1u;
-    for (int64_t i0 = w0; i0 < w1; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int key = i < w1 ? key_of(ids, ld, k, experts, i) : bins;
-        const unsigned peers = __match_any_sync(0xffffffffu, key);
-        if (i < w1) {
-            const int32_t p = mine[key] + __popc(peers & lt);
-            entry[p] = (int32_t)i;
-            slot[i] = key < experts ? p : -1 - p;
+    const int64_t t0 = (int64_t)blockIdx.x * tile, t1 = min(t0 + tile, n);
+    uint16_t *mine = counts + warp * bins;
+    bool first = true;
+    for (int64_t r0 = t0; first || r0 < t1; r0 += kBuildTile) {
+        const int64_t r1 = min(r0 + kBuildTile, t1);
+        // runs of whole multiples of 32, as short as the round allows
+        const int run = (int)((max(r1 - r0, (int64_t)1) + kBuildThreads - 1) / kBuildThreads) * 32;
+        const int64_t w0 = r0 + (int64_t)warp * run, w1 = min(w0 + run, r1);
+        int key[kBuildKeys];
+        unsigned peers[kBuildKeys];
+#pragma unroll
+        for (int j = 0; j < kBuildKeys; ++j) {
+            const int64_t i = w0 + j * 32 + lane;
+            key[j] = i < w1 ? key_of(ids, ld, k, experts, i) : bins;
         }
+        for (int b = lane; b < bins; b += 32) mine[b] = 0;
         __syncwarp();
-        if (i < w1 && lane == __ffs(peers) - 1) mine[key] += __popc(peers);
-        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kBuildKeys; ++j) {
+            if (w0 + j * 32 >= w1) break;
+            peers[j] = same_key(key[j], bits);
+            if (key[j] < bins && lane == __ffs(peers[j]) - 1) mine[key[j]] += __popc(peers[j]);
+            __syncwarp();
+        }
+        __syncthreads();
+        for (int b = threadIdx.x; b < bins; b += kBuildThreads) {
+            int32_t before = 0;
+#pragma unroll 16
+            for (int w = 0; w < kBuildWarps; ++w) {
+                const int32_t c = counts[w * bins + b];
+                counts[w * bins + b] = (uint16_t)before;
+                before += c;
+            }
+            total[b] = before;
+            if (first) base[b] = 0, sum[b] = 0;
+        }
+        if (first) {
+            // base: the earlier blocks' entries of each bin; sum: all blocks'
+            __syncthreads();
+            if (hist) {
+                for (int t = warp; t < tiles; t += kBuildWarps)
+                    for (int b = lane; b < bins; b += 32) {
+                        const int32_t c = __ldg(hist + (int64_t)t * bins + b);
+                        atomicAdd(sum + b, c);
+                        if (t < blockIdx.x) atomicAdd(base + b, c);
+                    }
+                __syncthreads();
+            } else {
+                cg::cluster_group cluster = cg::this_cluster();
+                cluster.sync();
+                for (int b = threadIdx.x; b < bins; b += kBuildThreads) {
+                    int32_t all = 0, before = 0;
+#pragma unroll
+                    for (int t = 0; t < kBuildCluster; ++t) {
+                        const int32_t c = t < tiles ? *cluster.map_shared_rank(total + b, t) : 0;
+                        all += c;
+                        if (t < blockIdx.x) before += c;
+                    }
+                    sum[b] = all, base[b] = before;
+                }
+                __syncthreads();
+            }
+            // plus each bin's begin: an exclusive prefix sum of `sum`, bins in blocks of one per thread
+            int32_t carry = 0;
+            for (int b0 = 0; b0 < bins; b0 += kBuildThreads) {
+                const int b = b0 + threadIdx.x;
+                const int32_t own = b < bins ? sum[b] : 0;
+                int32_t scan = own;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int32_t up = __shfl_up_sync(0xffffffffu, scan, d);
+                    if (lane >= d) scan += up;
+                }
+                if (lane == 31) warp_sum[warp] = scan;
+                __syncthreads();
+                int32_t before = lane < warp ? warp_sum[lane] : 0, all = warp_sum[lane];
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) {
+                    before += __shfl_xor_sync(0xffffffffu, before, d);
+                    all += __shfl_xor_sync(0xffffffffu, all, d);
+                }
+                const int32_t begin = carry + before + scan - own;
+                carry += all;
+                if (b < bins) {
+                    base[b] += begin;
+                    if (blockIdx.x == 0) expert_ptr[b] = begin;  // bin `experts` begins where the experts end
+                }
+                __syncthreads();
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kBuildKeys; ++j) {
+            if (w0 + j * 32 >= w1) break;
+            if (key[j] < bins) {
+                const int32_t p = base[key[j]] + mine[key[j]] + __popc(peers[j] & lt);
+                const int64_t i = w0 + j * 32 + lane;
+                entry[p] = (int32_t)i;
+                slot[i] = key[j] < experts ? p : -1 - p;
+            }
+            __syncwarp();
+            if (key[j] < bins && lane == __ffs(peers[j]) - 1) mine[key[j]] += __popc(peers[j]);
+            __syncwarp();
+        }
+        if (r0 + kBuildTile < t1) {  // the next round goes on behind this one
+            __syncthreads();
+            for (int b = threadIdx.x; b < bins; b += kBuildThreads) base[b] += total[b];
+            __syncthreads();
+        }
+        first = false;
     }
+    // a block's counts stay until the others have read them
+    if (!hist) cg::this_cluster().sync();
 }
 
 template <typename I>
@@ -147,21 +224,41 @@ cudaError_t launch_build(int64_t n, int k, int experts, const I *ids, int64_t ld
                          int32_t *slot, int32_t *hist, cudaStream_t stream) {
     const int64_t tile = build_tile(n);
     const int tiles = build_tiles(n);
-    const size_t bins = (size_t)experts + 1, smem = bins * kBuildWarps * 4;
-    if (smem > 48 * 1024) {
+    const size_t bins = (size_t)experts + 1, smem = bins * (3 * 4 + kBuildWarps * 2);
+    if (smem > 47 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(route_rank_kernel<I>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)smem);
         if (e != cudaSuccess) return e;
     }
-    if (tiles > 1)
+    const bool clustered = build_clustered(n);
+    if (tiles > 8 && clustered) {  // more blocks than every device's clusters may have
+        const cudaError_t e = cudaFuncSetAttribute(route_rank_kernel<I>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    if (!clustered) {
         route_hist_kernel<I><<<tiles, kBuildThreads, bins * 4, stream>>>(ids, ld, k, n, experts, tile, hist);
-    route_rank_kernel<I><<<tiles, kBuildThreads, smem, stream>>>(ids, ld, k, n, experts, tile, tiles, hist, expert_ptr,
-                                                                 entry, slot);
-    return cudaGetLastError();
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)tiles;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3((unsigned)tiles);
+    config.blockDim = dim3(kBuildThreads);
+    config.dynamicSmemBytes = smem;
+    config.stream = stream;
+    config.attrs = &attr;
+    config.numAttrs = clustered ? 1 : 0;
+    const int32_t *counted = clustered ? nullptr : hist;
+    return cudaLaunchKernelEx(&config, route_rank_kernel<I>, ids, ld, k, n, experts, tile, tiles, counted, expert_ptr,
+                              entry, slot);
 }
 
 // ---------------------------------------------------------------- rows
 constexpr int kRowThreads = 256;
+constexpr int kBackThreads = 128;
 
 // One warp per (token, span of 32 * U vectors of its row).
 struct RowArgs {
@@ -213,19 +310,43 @@ route_combine_kernel(RowArgs a, const T *__restrict__ ys, int64_t ldys, T *__res
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int n = 0; n < N; ++n) sum[u][n] = 0.0f;
-#pragma unroll 4
-    for (int j = 0; j < a.k; ++j) {
-        const int32_t p = __ldg(a.slot + t * a.k + j);
-        if (p < 0) continue;
-        const float w = a.w ? __ldg(a.w + t * a.ldw + j) : 1.0f;
-        const V *src = reinterpret_cast<const V *>(ys + (int64_t)p * ldys);
+    if constexpr (U == 1) {
+        // few rows: what counts is that the choices' rows are on their way together
+        constexpr int BATCH = 4;
+        for (int j0 = 0; j0 < a.k; j0 += BATCH) {
+            int32_t p[BATCH];
+            float w[BATCH];
+            V r[BATCH];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v0 + 32 * u < a.vecs) {
-                const V r = src[v0 + 32 * u];
-#pragma unroll
-                for (int n = 0; n < N; ++n) sum[u][n] = fmaf(w, to_float(r.v[n]), sum[u][n]);
+            for (int j = 0; j < BATCH; ++j) {
+                const bool in = j0 + j < a.k;
+                p[j] = in ? __ldg(a.slot + t * a.k + j0 + j) : -1;
+                w[j] = in && a.w ? __ldg(a.w + t * a.ldw + j0 + j) : 1.0f;
             }
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j)
+                if (p[j] >= 0 && v0 < a.vecs) r[j] = reinterpret_cast<const V *>(ys + (int64_t)p[j] * ldys)[v0];
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j)
+                if (p[j] >= 0 && v0 < a.vecs)
+#pragma unroll
+                    for (int n = 0; n < N; ++n) sum[0][n] = fmaf(w[j], to_float(r[j].v[n]), sum[0][n]);
+        }
+    } else {
+#pragma unroll 4
+        for (int j = 0; j < a.k; ++j) {
+            const int32_t p = __ldg(a.slot + t * a.k + j);
+            if (p < 0) continue;
+            const float w = a.w ? __ldg(a.w + t * a.ldw + j) : 1.0f;
+            const V *src = reinterpret_cast<const V *>(ys + (int64_t)p * ldys);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v0 + 32 * u < a.vecs) {
+                    const V r = src[v0 + 32 * u];
+#pragma unroll
+                    for (int n = 0; n < N; ++n) sum[u][n] = fmaf(w, to_float(r.v[n]), sum[u][n]);
+                }
+        }
     }
     V *dst = reinterpret_cast<V *>(y + t * ldy);
 #pragma unroll
@@ -238,15 +359,17 @@ route_combine_kernel(RowArgs a, const T *__restrict__ ys, int64_t ldys, T *__res
         }
 }
 
-// A block per token, K choices at a time: dy's row is read once for them
-// and their dot products summed over the block.
-template <typename T, int N, int K>
-__global__ void __launch_bounds__(kRowThreads)
+// A block per token.  The choices go K at a time, and for them U vectors of
+// the row per thread: dy's and all K expert rows' are on their way together.
+// dy's row is read once per K choices, and the dot products are summed over
+// the block in a fixed order.
+template <typename T, int N, int K, int U>
+__global__ void __launch_bounds__(kBackThreads)
 route_combine_backward_kernel(RowArgs a, const T *__restrict__ dy, int64_t lddy, const T *ys, int64_t ldys, T *dys,
                               int64_t lddys, float *__restrict__ dw, int64_t lddw) {
     using V = Vec<T, N>;
-    __shared__ float part[K][kRowThreads / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    __shared__ float part[K][kBackThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = blockIdx.x;
     const V *g = reinterpret_cast<const V *>(dy + t * lddy);
     for (int j0 = 0; j0 < a.k; j0 += K) {
@@ -259,28 +382,34 @@ route_combine_backward_kernel(RowArgs a, const T *__restrict__ dy, int64_t lddy,
             w[j] = in && a.w ? __ldg(a.w + t * a.ldw + j0 + j) : 1.0f;
             dot[j] = 0.0f;
         }
-        for (int v = threadIdx.x; v < a.vecs; v += blockDim.x) {
-            const V gv = g[v];
-            V yv[K];
+        for (int v0 = threadIdx.x; v0 < a.vecs; v0 += kBackThreads * U) {
+            V gv[U], yv[K][U];
 #pragma unroll
-            for (int j = 0; j < K; ++j)
-                if (dw && j0 + j < a.k && p[j] >= 0) yv[j] = reinterpret_cast<const V *>(ys + (int64_t)p[j] * ldys)[v];
+            for (int u = 0; u < U; ++u) {
+                const int v = v0 + u * kBackThreads;
+                if (v < a.vecs) gv[u] = g[v];
+#pragma unroll
+                for (int j = 0; j < K; ++j)
+                    if (dw && v < a.vecs && j0 + j < a.k && p[j] >= 0)
+                        yv[j][u] = reinterpret_cast<const V *>(ys + (int64_t)p[j] * ldys)[v];
+            }
 #pragma unroll
             for (int j = 0; j < K; ++j) {
-                if (j0 + j >= a.k) continue;
-                V r;
-                if (p[j] < 0) {
+                if (j0 + j >= a.k) break;
+                V *to = reinterpret_cast<V *>(dys + (int64_t)(p[j] < 0 ? -1 - p[j] : p[j]) * lddys);
 #pragma unroll
-                    for (int n = 0; n < N; ++n) r.v[n] = zero_of<T>();
-                } else {
+                for (int u = 0; u < U; ++u) {
+                    const int v = v0 + u * kBackThreads;
+                    if (v >= a.vecs) break;
+                    V r;
 #pragma unroll
                     for (int n = 0; n < N; ++n) {
-                        const float gf = to_float(gv.v[n]);
-                        if (dw) dot[j] = fmaf(gf, to_float(yv[j].v[n]), dot[j]);
-                        r.v[n] = from_float<T>(w[j] * gf);
+                        const float gf = to_float(gv[u].v[n]);
+                        if (dw && p[j] >= 0) dot[j] = fmaf(gf, to_float(yv[j][u].v[n]), dot[j]);
+                        r.v[n] = p[j] < 0 ? zero_of<T>() : from_float<T>(w[j] * gf);
                     }
+                    to[v] = r;
                 }
-                reinterpret_cast<V *>(dys + (int64_t)(p[j] < 0 ? -1 - p[j] : p[j]) * lddys)[v] = r;
             }
         }
         if (dw) {
@@ -294,7 +423,8 @@ route_combine_backward_kernel(RowArgs a, const T *__restrict__ dy, int64_t lddy,
             __syncthreads();
             if (threadIdx.x < K && j0 + threadIdx.x < a.k) {
                 float d = 0.0f;
-                for (int i = 0; i < warps; ++i) d += part[threadIdx.x][i];
+#pragma unroll
+                for (int i = 0; i < kBackThreads / 32; ++i) d += part[threadIdx.x][i];
                 dw[t * lddw + j0 + threadIdx.x] = d;
             }
             __syncthreads();
@@ -317,34 +447,56 @@ RowArgs row_args(int32_t tokens, int32_t k, int32_t hidden, int n, int u, const 
 
 unsigned row_blocks(const RowArgs &a) { return (unsigned)((a.items + kRowThreads / 32 - 1) / (kRowThreads / 32)); }
 
-template <typename T, int N>
-cudaError_t launch_dispatch(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const void *x, int64_t ldx,
-                            void *xs, int64_t ldxs, cudaStream_t stream) {
-    constexpr int U = 4;
+// A warp's span: with many rows, enough vectors per lane to keep the memory
+// busy; with few, one, so that the rows spread over the SMs.
+bool few_rows(int32_t tokens, int32_t hidden, int n) { return (int64_t)tokens * (hidden / n) < 152 * 64 * 32; }
+
+template <typename T, int N, int U>
+cudaError_t launch_dispatch_u(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const void *x, int64_t ldx,
+                              void *xs, int64_t ldxs, cudaStream_t stream) {
     const RowArgs a = row_args(tokens, k, hidden, N, U, slot, nullptr, 0);
     route_dispatch_kernel<T, N, U><<<row_blocks(a), kRowThreads, 0, stream>>>(a, static_cast<const T *>(x), ldx,
                                                                               static_cast<T *>(xs), ldxs);
     return cudaGetLastError();
 }
-
 template <typename T, int N>
-cudaError_t launch_combine(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const float *w, int64_t ldw,
-                           const void *ys, int64_t ldys, void *y, int64_t ldy, cudaStream_t stream) {
-    constexpr int U = 2;
+cudaError_t launch_dispatch(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const void *x, int64_t ldx,
+                            void *xs, int64_t ldxs, cudaStream_t stream) {
+    return few_rows(tokens, hidden, N) ? launch_dispatch_u<T, N, 1>(tokens, k, hidden, slot, x, ldx, xs, ldxs, stream)
+                                       : launch_dispatch_u<T, N, (N == 1 ? 8 : 4)>(tokens, k, hidden, slot, x, ldx, xs, ldxs, stream);
+}
+
+template <typename T, int N, int U>
+cudaError_t launch_combine_u(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const float *w, int64_t ldw,
+                             const void *ys, int64_t ldys, void *y, int64_t ldy, cudaStream_t stream) {
     const RowArgs a = row_args(tokens, k, hidden, N, U, slot, w, ldw);
     route_combine_kernel<T, N, U><<<row_blocks(a), kRowThreads, 0, stream>>>(a, static_cast<const T *>(ys), ldys,
                                                                              static_cast<T *>(y), ldy);
     return cudaGetLastError();
 }
+template <typename T, int N>
+cudaError_t launch_combine(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const float *w, int64_t ldw,
+                           const void *ys, int64_t ldys, void *y, int64_t ldy, cudaStream_t stream) {
+    return few_rows(tokens, hidden, N) ? launch_combine_u<T, N, 1>(tokens, k, hidden, slot, w, ldw, ys, ldys, y, ldy, stream)
+                                       : launch_combine_u<T, N, (N == 1 ? 4 : 2)>(tokens, k, hidden, slot, w, ldw, ys, ldys, y, ldy, stream);
+}
 
+template <typename T, int N, int K, int U>
+cudaError_t launch_combine_backward_k(const RowArgs &a, int32_t tokens, const void *dy, int64_t lddy, const void *ys,
+                                      int64_t ldys, void *dys, int64_t lddys, float *dw, int64_t lddw, cudaStream_t stream) {
+    route_combine_backward_kernel<T, N, K, U><<<(unsigned)tokens, kBackThreads, 0, stream>>>(
+        a, static_cast<const T *>(dy), lddy, static_cast<const T *>(ys), ldys, static_cast<T *>(dys), lddys, dw, lddw);
+    return cudaGetLastError();
+}
 template <typename T, int N>
 cudaError_t launch_combine_backward(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const float *w,
                                     int64_t ldw, const void *dy, int64_t lddy, const void *ys, int64_t ldys, void *dys,
                                     int64_t lddys, float *dw, int64_t lddw, cudaStream_t stream) {
     const RowArgs a = row_args(tokens, k, hidden, N, 1, slot, w, ldw);
-    route_combine_backward_kernel<T, N, 4><<<(unsigned)tokens, kRowThreads, 0, stream>>>(
-        a, static_cast<const T *>(dy), lddy, static_cast<const T *>(ys), ldys, static_cast<T *>(dys), lddys, dw, lddw);
-    return cudaGetLastError();
+    // about a dozen loads of a thread on their way
+    if (k <= 2) return launch_combine_backward_k<T, N, 2, 4>(a, tokens, dy, lddy, ys, ldys, dys, lddys, dw, lddw, stream);
+    if (k <= 4) return launch_combine_backward_k<T, N, 4, 2>(a, tokens, dy, lddy, ys, ldys, dys, lddys, dw, lddw, stream);
+    return launch_combine_backward_k<T, N, 8, (N == 1 ? 4 : 1)>(a, tokens, dy, lddy, ys, ldys, dys, lddys, dw, lddw, stream);
 }
 
 // Rows whose addresses all fall on 16 bytes move in 16-byte vectors, others
@@ -390,8 +542,7 @@ spmv_status_t spmv_route_workspace(int32_t tokens, int32_t top_k, int32_t expert
     if (experts < 1 || experts > kMaxExperts) return llm_bad("experts must be in [1, 2048]");
     const int64_t n = (int64_t)tokens * top_k;
     if (n >= (1LL << 31)) return llm_bad("tokens * top_k must be < 2^31");
-    const int tiles = build_tiles(n);
-    *bytes = tiles > 1 ? (size_t)tiles * (experts + 1) * 4 : 0;
+    *bytes = build_clustered(n) ? 0 : (size_t)build_tiles(n) * (experts + 1) * 4;
     return SPMV_OK;
 }
 

@@ -27,7 +27,8 @@ class PageTable:
     tokens.  ``table`` (max_requests, max_pages), int32, is the caller's and
     is extended in place.  ``append`` fills, for the requests of one step,
     ``token_ptr`` (requests + 1), ``lens`` (requests), ``slots`` and
-    ``positions`` (max_tokens), ``taken`` (1) and ``status`` (1)."""
+    ``positions`` (max_tokens) and ``taken`` (1), and adds its flags to
+    ``status`` (1)."""
 
     def __init__(self, table, page_size: int, num_pages: int, max_tokens: int):
         if table.dtype != torch.int32 or not table.is_cuda or table.dim() != 2:

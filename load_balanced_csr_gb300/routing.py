@@ -77,20 +77,16 @@ class ExpertRoute:
             raise RuntimeError("the route has not been built")
         return self.tokens
 
-    def _rows(self, what, t, **given):
+    def _rows(self, what, like, *given):
         """The element type, hidden size and row strides of a call's tensors
-        (name=(tensor, rows), the first of which sets the type and hidden
-        size; None: to be made)."""
-        like = (t, *[(x.shape, x.stride(), x.dtype, x.device) for x, _ in given.values() if x is not None])
-        known = self._seen.get(what)
-        if known is None or known[0] != like or known[1] != len(given):
-            first, _ = next(iter(given.values()))
-            hidden = first.shape[-1] if first.dim() else 0
-            found = [_launch.elem(first.dtype), hidden]
-            for name, (x, rows) in given.items():
-                found.append(hidden if x is None else _launch.rows(name, x, (rows, hidden), first.dtype, self.device))
-            known = self._seen[what] = (like, len(given), found)
-        return known[2]
+        (name, tensor or None, rows), the first of which sets the type and
+        the hidden size; `like` is what they depend on."""
+        (_, first, _), found = given[0], []
+        hidden = first.shape[-1] if first.dim() else 0
+        for name, x, rows in given:
+            found.append(hidden if x is None else _launch.rows(name, x, (rows, hidden), first.dtype, self.device))
+        known = self._seen[what] = (like, _launch.elem(first.dtype), hidden, *found)
+        return known
 
     def _weights(self, weights):
         if weights is None:
@@ -105,7 +101,12 @@ class ExpertRoute:
     def dispatch(self, x, out=None, stream=None):
         """xs[p] = x[entry[p] // top_k]; rows of dropped entries are zero."""
         t, k, d = self._built(), self.top_k, self.device
-        e, hidden, ldx, ldo = self._rows("dispatch" if out is None else "dispatch to", t, x=(x, t), out=(out, t * k))
+        like = (t, x.shape, x.stride(), x.dtype, x.device,
+                None if out is None else (out.shape, out.stride(), out.dtype, out.device))
+        known = self._seen.get("dispatch")
+        if known is None or known[0] != like:
+            known = self._rows("dispatch", like, ("x", x, t), ("out", out, t * k))
+        _, e, hidden, ldx, ldo = known
         if out is None:
             out = _launch.empty(stream, d, (t * k, hidden), x.dtype)
         _launch.call(self._L.spmv_route_dispatch, "spmv_route_dispatch", d, t, k, hidden, e, self._pointers[2],
@@ -115,7 +116,12 @@ class ExpertRoute:
     def combine(self, ys, weights=None, out=None, stream=None):
         """y[t] = sum over j of weights[t, j] * ys[slot[t, j]] (weights float32; None: 1)."""
         t, k, d = self._built(), self.top_k, self.device
-        e, hidden, ldys, ldo = self._rows("combine" if out is None else "combine to", t, ys=(ys, t * k), out=(out, t))
+        like = (t, ys.shape, ys.stride(), ys.dtype, ys.device,
+                None if out is None else (out.shape, out.stride(), out.dtype, out.device))
+        known = self._seen.get("combine")
+        if known is None or known[0] != like:
+            known = self._rows("combine", like, ("ys", ys, t * k), ("out", out, t))
+        _, e, hidden, ldys, ldo = known
         w, ldw = self._weights(weights)
         if out is None:
             out = _launch.empty(stream, d, (t, hidden), ys.dtype)
@@ -130,8 +136,12 @@ class ExpertRoute:
     def combine_backward(self, dy, ys, weights=None, out=None, dweights=None, stream=None):
         """The gradient of combine: (dys, dweights).  ``out`` may be ``ys``."""
         t, k, d = self._built(), self.top_k, self.device
-        e, hidden, lddy, ldys, ldo = self._rows("combine_backward" if out is None else "combine_backward to", t,
-                                                dy=(dy, t), ys=(ys, t * k), out=(out, t * k))
+        like = (t, dy.shape, dy.stride(), dy.dtype, dy.device, ys.shape, ys.stride(), ys.dtype, ys.device,
+                None if out is None else (out.shape, out.stride(), out.dtype, out.device))
+        known = self._seen.get("combine_backward")
+        if known is None or known[0] != like:
+            known = self._rows("combine_backward", like, ("dy", dy, t), ("ys", ys, t * k), ("out", out, t * k))
+        _, e, hidden, lddy, ldys, ldo = known
         w, ldw = self._weights(weights)
         if out is None:
             out = _launch.empty(stream, d, (t * k, hidden), dy.dtype)
