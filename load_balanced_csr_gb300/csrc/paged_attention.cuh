@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
     // batches of 32 units (a unit is a chunk where every chunk lies in one
     // page, else a position), the next request's first batch, and the next
     // row's queries.
-    Place load;
+    Place load{};
     uint32_t at = 0;            // the next chunk's unit
     int32_t pages = 0, more_pages = 0, first_pages = 0, next_request_pages = 0;
     int base = 0;               // the first unit of `pages`
@@ -715,53 +715,42 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
         opened = false;
         const int inside = pos - page_at(pos) * p.a.page_size;
         const uint32_t dst = smem_addr(mine + stage * R::STAGE);
-        if (one_page && mask == FULL) {
-            // the whole chunk, in one page: row r is r strides after row 0
+        if (32 % VPR == 0 && one_page && mask == FULL) {
+            // the whole chunk, in one page: row r is r strides after row 0, and neighbouring lanes copy neighbours
             const int row0 = lane / VPR, col = lane % VPR;
             const int64_t in0 = __shfl_sync(0xffffffffu, inside, 0) + row0;
             const T *ks = static_cast<const T *>(p.a.k_cache) + page * p.a.k_stride[0] + in0 * p.a.k_stride[1] +
                           kv_head * p.a.k_stride[2] + col * PER;
             const T *vs = static_cast<const T *>(p.a.v_cache) + page * p.a.v_stride[0] + in0 * p.a.v_stride[1] +
                           kv_head * p.a.v_stride[2] + col * PER;
-            if (32 % VPR == 0) {
-                constexpr int STEP = 32 / VPR > 0 ? 32 / VPR : 1;  // rows a warp copies at once
-                const int64_t kstep = STEP * p.a.k_stride[1], vstep = STEP * p.a.v_stride[1];
-                const uint32_t to = dst + row0 * P::PITCH + col * 16;
-                if (col * PER < p.a.head_dim) {
+            constexpr int STEP = 32 / VPR > 0 ? 32 / VPR : 1;  // rows a warp copies at once
+            const int64_t kstep = STEP * p.a.k_stride[1], vstep = STEP * p.a.v_stride[1];
+            const uint32_t to = dst + row0 * P::PITCH + col * 16;
+            if (col * PER < p.a.head_dim) {
 #pragma unroll
-                    for (int i = 0; i < P::CH / STEP; ++i) {
-                        copy16(to + i * STEP * P::PITCH, ks, true);
-                        copy16(to + (P::CH + i * STEP) * P::PITCH, vs, true);
-                        ks += kstep, vs += vstep;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < P::CH * VPR / 32; ++i) {
-                    const int e = lane + 32 * i, row = e / VPR, c = e % VPR;
-                    if (c * PER < p.a.head_dim) {
-                        const uint32_t to = dst + row * P::PITCH + c * 16;
-                        copy16(to, ks + (row - row0) * p.a.k_stride[1] + (c - col) * PER, true);
-                        copy16(to + P::CH * P::PITCH, vs + (row - row0) * p.a.v_stride[1] + (c - col) * PER, true);
-                    }
+                for (int i = 0; i < P::CH / STEP; ++i) {
+                    copy16(to + i * STEP * P::PITCH, ks, true);
+                    copy16(to + (P::CH + i * STEP) * P::PITCH, vs, true);
+                    ks += kstep, vs += vstep;
                 }
             }
         } else {
+            // each lane copies a share of its own position's row
             if (in && !real && lane < P::CH) atomicOr(p.a.status, kBadPage);
-            const int64_t pg = real ? page : 0;
-            const int64_t ko = pg * p.a.k_stride[0] + inside * p.a.k_stride[1] + kv_head * p.a.k_stride[2];
-            const int64_t vo = pg * p.a.v_stride[0] + inside * p.a.v_stride[1] + kv_head * p.a.v_stride[2];
+            constexpr int PARTS = 32 / P::CH;
+            const int part = lane / P::CH;
+            const int64_t pg = real ? page : 0, in0 = real ? inside : 0;
+            const T *ks = static_cast<const T *>(p.a.k_cache) + pg * p.a.k_stride[0] + in0 * p.a.k_stride[1] +
+                          kv_head * p.a.k_stride[2] + part * PER;
+            const T *vs = static_cast<const T *>(p.a.v_cache) + pg * p.a.v_stride[0] + in0 * p.a.v_stride[1] +
+                          kv_head * p.a.v_stride[2] + part * PER;
+            const uint32_t to = dst + tok * P::PITCH + part * 16;
 #pragma unroll
-            for (int i = 0; i < P::CH * VPR / 32; ++i) {
-                const int e = lane + 32 * i, row = e / VPR, col = e % VPR;
-                const int64_t kr = __shfl_sync(0xffffffffu, ko, row), vr = __shfl_sync(0xffffffffu, vo, row);
-                const bool there = (mask >> row) & 1;
-                if (col * PER < p.a.head_dim) {
-                    const uint32_t to = dst + row * P::PITCH + col * 16;
-                    copy16(to, static_cast<const T *>(p.a.k_cache) + (there ? kr + col * PER : 0), there);
-                    copy16(to + P::CH * P::PITCH, static_cast<const T *>(p.a.v_cache) + (there ? vr + col * PER : 0), there);
+            for (int i = 0; i < VPR / PARTS; ++i)
+                if ((part + i * PARTS) * PER < p.a.head_dim) {
+                    copy16(to + i * PARTS * 16, ks + i * PARTS * PER, real);
+                    copy16(to + P::CH * P::PITCH + i * PARTS * 16, vs + i * PARTS * PER, real);
                 }
-            }
         }
         if (++at >= end) {
             live = false;
@@ -806,7 +795,11 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
     };
     float *head_rec = p.warp_rec + (int64_t)(blockIdx.x * P::NW + warp) * R::FLOATS;
     float *recs = reinterpret_cast<float *>(mine);  // both records, in the stages when these hold nothing any more
-    int copied = 0, flags = 0;
+    int copied = 0, flags = 0, h0 = 0, heads = 0;  // of the present row
+    auto heads_of = [&](int vh) {
+        const int c = vh / p.tiles, t = vh - c * p.tiles;
+        h0 = c * p.group + t * P::GT, heads = min(P::GT, p.group - t * P::GT);
+    };
 #pragma unroll
     for (int s = 0; s < P::STAGES - 1; ++s) {
         if (live) copy(s), ++copied;
@@ -820,9 +813,8 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
         copy_wait<P::STAGES - 1>();
         __syncwarp();
         const int3 note = notes[warp][stage];
-        const int c = note.y / p.tiles, t = note.y - c * p.tiles;
-        const int heads = min(P::GT, p.group - t * P::GT), h0 = c * p.group + t * P::GT;
         if (note.z & kFresh) {
+            heads_of(note.y);
             tile.begin(p, note.x, h0, heads, qs, lane, note.x == fetched_b && note.y == fetched_vh);
             fetched_b = -1;
             before = note.z & kBefore;
