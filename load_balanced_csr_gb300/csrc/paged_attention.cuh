@@ -112,23 +112,30 @@ __device__ __forceinline__ float pow2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// the mask of a whole chunk
+template <int CH>
+constexpr uint32_t FULL_MASK = 0xffffffffu >> (32 - CH);
+
 // what scores are taken relative to; the running maximum m is -infinity
 // until a score has come, and nothing has weight then
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // ------------------------------------------------------------ 16-bit elements
-// A chunk is 16 positions; a tile is 8 or 16 query heads of one kv head.  The
-// scores are one 16 x 16 product per chunk (heads by positions) and the
+// A chunk is 16 positions, or 32 of small heads, so that a chunk's fixed work
+// is not most of it; a tile is 8 or 16 query heads of one kv head.  The
+// scores are one 16 x CH product per chunk (heads by positions) and the
 // output one 16 x DP product, on the warp's matrix instructions with 32-bit
 // sums.  The weights go into the second product as hi + lo, two elements of
 // the caches' type (p - hi is exact in 32 bits), so they carry 16 (bf16) or
 // 22 (f16) bits: with hi alone the output's error against 64 bits is 1.4
 // times that of one rounding.  A tile of 8 heads has hi in the product's
 // first 8 rows and lo in its last 8, and so costs no more than hi alone.
-template <typename T_, int GT_, int DP_, int NW_, int STAGES_>
+template <typename T_, int GT_, int DP_, int CH_, int NW_, int STAGES_>
 struct TileMma {
     using T = T_;
-    static constexpr int DP = DP_, NW = NW_, STAGES = STAGES_, GT = GT_, CH = 16;
+    static constexpr int DP = DP_, NW = NW_, STAGES = STAGES_, GT = GT_, CH = CH_;
+    static constexpr int PAGE_UNIT = 16;   // positions that lie in one page when page_size is a multiple
+    static constexpr int NT = CH / 8;      // the scores' product in columns of 8 positions
     static constexpr int PITCH = DP * 2 + 16;  // bytes: rows 16 bytes apart modulo 128, so ldmatrix has no conflicts
     static constexpr int QBYTES = 0;
     static constexpr int H = GT / 8;  // heads of a lane: lane / 4 and, with 16, lane / 4 + 8
@@ -185,31 +192,36 @@ struct TileMma {
     __device__ __forceinline__ void chunk(const AttendArgs &p, const char *stage, char *, uint32_t mask, int lane) {
         const uint32_t ks = smem_addr(stage), vs = ks + CH * PITCH;
         const int r8 = lane & 7, mat = lane >> 3;
-        // scores of positions 0-7 and 8-15, each in two sums that do not wait for one another
-        float sums[2][2][4] = {};
+        // with 16 positions, each score in two sums that do not wait for one another
+        constexpr int SPLIT = CH == 16 ? 2 : 1;
+        float sums[SPLIT][NT][4] = {};
         {
             const uint32_t at = ks + (r8 + (mat >> 1) * 8) * PITCH + (mat & 1) * 16;
 #pragma unroll
             for (int i = 0; i < DP / 16; ++i) {
-                uint32_t kb[4];
-                ldmatrix4(at + i * 32, kb);
                 const uint32_t qa[4] = {q[i][0], H == 2 ? q[i][H - 1] : 0u, q[i][H], H == 2 ? q[i][2 * H - 1] : 0u};
-                mma16816<T>(sums[i & 1][0], qa, kb[0], kb[1]);
-                mma16816<T>(sums[i & 1][1], qa, kb[2], kb[3]);
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    uint32_t kb[4];
+                    ldmatrix4(at + n * 8 * PITCH + i * 32, kb);
+                    mma16816<T>(sums[i % SPLIT][n], qa, kb[0], kb[1]);
+                    mma16816<T>(sums[i % SPLIT][n + 1], qa, kb[2], kb[3]);
+                }
             }
         }
-        const bool whole = mask == 0xffffu;
-        uint32_t hi[2 * H], lo[2 * H];  // [positions 0-7, 8-15][head]
-        float s[2][H][2], top[H];
+        const bool whole = mask == FULL_MASK<CH>;
+        uint32_t hi[NT * H], lo[NT * H];  // [8 positions][head]
+        float s[NT][H][2], top[H];
         bool higher = false;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             float raw = -INFINITY;
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    s[n][h][c] = sums[0][n][2 * h + c] + sums[1][n][2 * h + c];
+                    s[n][h][c] = sums[0][n][2 * h + c];
+                    if (SPLIT == 2) s[n][h][c] += sums[SPLIT - 1][n][2 * h + c];
                     if (!whole && !((mask >> (n * 8 + (lane & 3) * 2 + c)) & 1)) s[n][h][c] = -INFINITY;
                     raw = fmaxf(raw, s[n][h][c]);
                 }
@@ -235,7 +247,7 @@ struct TileMma {
         for (int h = 0; h < H; ++h) {
             const float base = base_of(m[h]);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < NT; ++n) {
                 float w[2];
                 T high[2];
 #pragma unroll
@@ -250,25 +262,21 @@ struct TileMma {
             }
         }
         const uint32_t at = vs + (r8 + (mat & 1) * 8) * PITCH + (mat >> 1) * 16;
-        if (H == 1) {
-            const uint32_t pa[4] = {hi[0], lo[0], hi[1], lo[1]};
+#pragma unroll
+        for (int k = 0; k < CH / 16; ++k) {
+            const uint32_t *kh = hi + 2 * k * H, *kl = lo + 2 * k * H;
+            const uint32_t pa[4] = {kh[0], H == 1 ? kl[0] : kh[H - 1], kh[H], H == 1 ? kl[1] : kh[2 * H - 1]};
+            const uint32_t pl[4] = {kl[0], kl[H - 1], kl[H], kl[2 * H - 1]};
 #pragma unroll
             for (int i = 0; i < DP / 16; ++i) {
                 uint32_t vb[4];
-                ldmatrix4_t(at + i * 32, vb);
+                ldmatrix4_t(at + k * 16 * PITCH + i * 32, vb);
                 mma16816<T>(o[2 * i], pa, vb[0], vb[1]);
                 mma16816<T>(o[2 * i + 1], pa, vb[2], vb[3]);
-            }
-        } else {
-            const uint32_t ph[4] = {hi[0], hi[H - 1], hi[H], hi[2 * H - 1]}, pl[4] = {lo[0], lo[H - 1], lo[H], lo[2 * H - 1]};
-#pragma unroll
-            for (int i = 0; i < DP / 16; ++i) {
-                uint32_t vb[4];
-                ldmatrix4_t(at + i * 32, vb);
-                mma16816<T>(o[2 * i], ph, vb[0], vb[1]);
-                mma16816<T>(o[2 * i + 1], ph, vb[2], vb[3]);
-                mma16816<T>(o[2 * i], pl, vb[0], vb[1]);
-                mma16816<T>(o[2 * i + 1], pl, vb[2], vb[3]);
+                if (H == 2) {
+                    mma16816<T>(o[2 * i], pl, vb[0], vb[1]);
+                    mma16816<T>(o[2 * i + 1], pl, vb[2], vb[3]);
+                }
             }
         }
     }
@@ -310,7 +318,7 @@ struct TileMma {
 template <int DP_, int GT_, int NW_, int STAGES_>
 struct TileF32 {
     using T = float;
-    static constexpr int DP = DP_, NW = NW_, STAGES = STAGES_, GT = GT_, CH = 8;
+    static constexpr int DP = DP_, NW = NW_, STAGES = STAGES_, GT = GT_, CH = 8, PAGE_UNIT = 8;
     static constexpr int PITCH = DP * 4 + 16;
     static constexpr int WEIGHTS = GT * DP * 4;                // offset of the weights of a chunk behind the queries
     static constexpr int QBYTES = WEIGHTS + GT * CH * 4;
@@ -630,10 +638,10 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
     using R = Record<P>;
     using T = typename P::T;
     constexpr int NT = P::NW * 32;
-    constexpr uint32_t FULL = (1u << P::CH) - 1u;
-    enum { kFresh = 1 << 16, kBefore = 1 << 17, kRowEnd = 1 << 18, kShareEnd = 1 << 19 };
+    constexpr uint32_t FULL = FULL_MASK<P::CH>;
+    enum { kFresh = 1, kBefore = 2, kRowEnd = 4, kShareEnd = 8 };
     extern __shared__ __align__(16) char smem[];
-    __shared__ int3 notes[P::NW][P::STAGES];  // a stage's request, row, and mask of positions with flags
+    __shared__ int4 notes[P::NW][P::STAGES];  // a stage's request, row, mask of positions, flags
     __shared__ int has[P::NW];                // bit 0: a head record, 1: a tail record, 2: its row began in an earlier warp
     __shared__ int rows_of[P::NW][4];         // head record's request and row, tail record's
     __shared__ Part parts[P::NW + 1];
@@ -668,8 +676,8 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
 
     // ---- the chunks to copy.  Under load a read takes longer than a chunk's
     // work, so what the next copies need is read well before: the pages in
-    // batches of 32 units (a unit is a chunk where every chunk lies in one
-    // page, else a position), the next request's first batch, and the next
+    // batches of 32 units (a unit is PAGE_UNIT positions where these lie in one
+    // page, else one), the next request's first batch, and the next
     // row's queries.
     Place load{};
     uint32_t at = 0;            // the next chunk's unit
@@ -679,12 +687,12 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
     int64_t kv_head = 0;
     bool live = begin < end, opened = true;
     const int tok = lane % P::CH;
-    const bool one_page = p.a.page_size % P::CH == 0;
-    const int unit = one_page ? 1 : P::CH;  // units in a chunk
+    const bool one_page = p.a.page_size % P::PAGE_UNIT == 0;
+    const int unit = one_page ? P::CH / P::PAGE_UNIT : P::CH;  // units in a chunk
     auto page_at = [&](int pos) { return (int)((__umulhi((uint32_t)pos, p.page_mul) + (uint32_t)pos) >> p.page_shift); };
     // this lane's entry of the batch of request b that begins at unit u
     auto read_pages = [&](int b, int len, int u) {
-        const int64_t pos = (int64_t)(u + lane) * (one_page ? P::CH : 1);
+        const int64_t pos = (int64_t)(u + lane) * (one_page ? P::PAGE_UNIT : 1);
         return pos < len ? __ldg(p.a.table + b * p.a.table_stride + page_at((int)pos)) : -1;
     };
     auto read_next_request = [&] {
@@ -704,34 +712,38 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
     constexpr int PER = 16 / sizeof(T), VPR = P::DP / PER;  // elements in a copy, copies in a row
     auto copy = [&](int stage) {
         const int pos = (int)load.ch * P::CH + tok;
-        const int32_t page = __shfl_sync(0xffffffffu, pages, (int)load.ch * unit - base + (one_page ? 0 : tok));
+        const int32_t page = __shfl_sync(0xffffffffu, pages, (int)load.ch * unit - base + (one_page ? tok / P::PAGE_UNIT : tok));
         const bool in = pos < load.len, real = in && (uint32_t)page < (uint32_t)p.a.num_pages;
         const uint32_t mask = __ballot_sync(0xffffffffu, real) & FULL;
         const bool row_end = load.ch + 1 == load.nch;
         if (lane == 0)
-            notes[warp][stage] = make_int3(load.b, load.vh, (int)mask | (opened || load.ch == 0 ? kFresh : 0) |
-                                           (opened && load.ch != 0 ? kBefore : 0) | (row_end ? kRowEnd : 0) |
-                                           (at + 1 == end ? kShareEnd : 0));
+            notes[warp][stage] = make_int4(load.b, load.vh, (int)mask,
+                                           (opened || load.ch == 0 ? kFresh : 0) | (opened && load.ch != 0 ? kBefore : 0) |
+                                               (row_end ? kRowEnd : 0) | (at + 1 == end ? kShareEnd : 0));
         opened = false;
         const int inside = pos - page_at(pos) * p.a.page_size;
         const uint32_t dst = smem_addr(mine + stage * R::STAGE);
         if (32 % VPR == 0 && one_page && mask == FULL) {
-            // the whole chunk, in one page: row r is r strides after row 0, and neighbouring lanes copy neighbours
-            const int row0 = lane / VPR, col = lane % VPR;
-            const int64_t in0 = __shfl_sync(0xffffffffu, inside, 0) + row0;
-            const T *ks = static_cast<const T *>(p.a.k_cache) + page * p.a.k_stride[0] + in0 * p.a.k_stride[1] +
-                          kv_head * p.a.k_stride[2] + col * PER;
-            const T *vs = static_cast<const T *>(p.a.v_cache) + page * p.a.v_stride[0] + in0 * p.a.v_stride[1] +
-                          kv_head * p.a.v_stride[2] + col * PER;
+            // a whole chunk: in a unit row r is r strides after row 0, and neighbouring lanes copy neighbours
             constexpr int STEP = 32 / VPR > 0 ? 32 / VPR : 1;  // rows a warp copies at once
+            const int row0 = lane / VPR, col = lane % VPR;
             const int64_t kstep = STEP * p.a.k_stride[1], vstep = STEP * p.a.v_stride[1];
-            const uint32_t to = dst + row0 * P::PITCH + col * 16;
-            if (col * PER < p.a.head_dim) {
 #pragma unroll
-                for (int i = 0; i < P::CH / STEP; ++i) {
-                    copy16(to + i * STEP * P::PITCH, ks, true);
-                    copy16(to + (P::CH + i * STEP) * P::PITCH, vs, true);
-                    ks += kstep, vs += vstep;
+            for (int h = 0; h < P::CH / P::PAGE_UNIT; ++h) {
+                const int64_t page_h = __shfl_sync(0xffffffffu, page, h * P::PAGE_UNIT);
+                const int64_t in0 = __shfl_sync(0xffffffffu, inside, h * P::PAGE_UNIT) + row0;
+                const T *ks = static_cast<const T *>(p.a.k_cache) + page_h * p.a.k_stride[0] + in0 * p.a.k_stride[1] +
+                              kv_head * p.a.k_stride[2] + col * PER;
+                const T *vs = static_cast<const T *>(p.a.v_cache) + page_h * p.a.v_stride[0] + in0 * p.a.v_stride[1] +
+                              kv_head * p.a.v_stride[2] + col * PER;
+                const uint32_t to = dst + (h * P::PAGE_UNIT + row0) * P::PITCH + col * 16;
+                if (col * PER < p.a.head_dim) {
+#pragma unroll
+                    for (int i = 0; i < P::PAGE_UNIT / STEP; ++i) {
+                        copy16(to + i * STEP * P::PITCH, ks, true);
+                        copy16(to + (P::CH + i * STEP) * P::PITCH, vs, true);
+                        ks += kstep, vs += vstep;
+                    }
                 }
             }
         } else {
@@ -812,19 +824,19 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
         copy_commit();
         copy_wait<P::STAGES - 1>();
         __syncwarp();
-        const int3 note = notes[warp][stage];
-        if (note.z & kFresh) {
+        const int4 note = notes[warp][stage];
+        if (note.w & kFresh) {
             heads_of(note.y);
             tile.begin(p, note.x, h0, heads, qs, lane, note.x == fetched_b && note.y == fetched_vh);
             fetched_b = -1;
-            before = note.z & kBefore;
+            before = note.w & kBefore;
         }
-        tile.chunk(p, mine + stage * R::STAGE, qs, note.z & FULL, lane);
+        tile.chunk(p, mine + stage * R::STAGE, qs, (uint32_t)note.z, lane);
         __syncwarp();
         stage = stage + 1 == P::STAGES ? 0 : stage + 1;
-        if (!(note.z & (kRowEnd | kShareEnd))) continue;
+        if (!(note.w & (kRowEnd | kShareEnd))) continue;
         tile.sums();
-        if (!(note.z & kRowEnd)) {  // the last chunk
+        if (!(note.w & kRowEnd)) {  // the last chunk
             flags |= before ? 6 : 2;
             if (lane == 0) rows_of[warp][2] = note.x, rows_of[warp][3] = note.y;
             write_record(recs + R::FLOATS, heads);
@@ -989,11 +1001,11 @@ cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStrea
 // Calls f with the tile of 16-bit elements T for the head size and group.
 template <typename T, int GT, typename F>
 auto with_mma(int dim, F f) {
-    if (dim <= 64) return f(TileMma<T, GT, 64, 8, 5>());
-    if (dim <= 96) return f(TileMma<T, GT, 96, 8, 4>());
-    if (dim <= 128) return f(TileMma<T, GT, 128, 8, 3>());
-    if (dim <= 192) return f(TileMma<T, GT, 192, 4, 4>());
-    return f(TileMma<T, GT, 256, 4, 3>());
+    if (dim <= 64) return f(TileMma<T, GT, 64, 32, 8, 3>());
+    if (dim <= 96) return f(TileMma<T, GT, 96, 16, 8, 4>());
+    if (dim <= 128) return f(TileMma<T, GT, 128, 16, 8, 3>());
+    if (dim <= 192) return f(TileMma<T, GT, 192, 16, 4, 4>());
+    return f(TileMma<T, GT, 256, 16, 4, 3>());
 }
 
 template <typename T, typename F>

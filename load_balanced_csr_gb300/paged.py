@@ -155,7 +155,10 @@ class PagedAttention:
         self._workspace = torch.empty(size.value, dtype=torch.uint8, device=self.device)
         self._workspace[:4096].zero_()
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
-        self._like, self._scale, self._args_ref = None, self.head_dim ** -0.5, ctypes.byref(a)
+        # the inputs' layouts that were checked last, and the outputs' shapes for them; whether the arguments have
+        # the strides of a new output
+        self._like = self._shape = None
+        self._dense, self._scale, self._args_ref = False, self.head_dim ** -0.5, ctypes.byref(a)
         a.workspace, a.workspace_bytes, a.status = (self._workspace.data_ptr(), size.value,
                                                     self._status.data_ptr())
 
@@ -170,20 +173,23 @@ class PagedAttention:
         if like != self._like:
             self._like = None
             self._check(q, k_cache, v_cache, table, lens)
-            self._like = like
-        shape = q.shape
-        if out is None:
-            out = _launch.empty(stream, d, shape, self.dtype)
-            a.out_stride[0], a.out_stride[1] = shape[1] * shape[2], shape[2]
-        else:
+            self._like, self._shape, self._dense = like, (q.shape, q.shape[:2]), False
+        shape, heads = self._shape
+        if out is not None:
             if out.dtype != self.dtype or out.device != d or out.shape != shape or out.stride(2) != 1:
                 raise ValueError(f"out must be a {self.dtype} tensor of shape {tuple(shape)} on {d}, contiguous in its last "
                                  "dimension")
             a.out_stride[:] = out.stride()[:2]
+            self._dense = False
+        else:
+            out = _launch.empty(stream, d, shape, self.dtype)
+            if not self._dense:
+                a.out_stride[:] = out.stride()[:2]
+                self._dense = True
         if lse is None:
-            lse = _launch.empty(stream, d, shape[:2], torch.float32)
-        elif lse.dtype != torch.float32 or lse.device != d or lse.shape != shape[:2] or not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous float32 tensor of shape {tuple(shape[:2])} on {d}")
+            lse = _launch.empty(stream, d, heads, torch.float32)
+        elif lse.dtype != torch.float32 or lse.device != d or lse.shape != heads or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 tensor of shape {tuple(heads)} on {d}")
         a.scale = self._scale if scale is None else scale
         a.q, a.k_cache, a.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
         a.table, a.lens, a.out, a.lse = table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr()
