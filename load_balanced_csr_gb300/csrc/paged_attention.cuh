@@ -586,52 +586,73 @@ struct Part {
     int b, vh;
 };
 
-// Joins parts: part i has weight 2^(m_i - max m), and rec(i) is its record.
-// Gives head g's elements d .. d + 3 to out(g, d, sums, m, l).
-template <class P, typename Rec, typename Out>
-__device__ __forceinline__ void join(int count, int heads, Rec rec, Out out) {
-    constexpr int BATCH = 8;  // parts read at once
-    for (int e = threadIdx.x; e < heads * (P::DP / 4); e += P::NW * 32) {
-        const int g = e / (P::DP / 4), d = e % (P::DP / 4) * 4;
-        float m = -INFINITY, l = 0.0f;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int i0 = 0; i0 < count; i0 += BATCH) {
-            float mi[BATCH], li[BATCH], top = m;
-            float4 v[BATCH];
+// One warp joins `count` parts of a row for head g of its tile: part i has
+// weight 2^(m_i - max m), and its record is at from + i * step + FLOATS, the
+// last one's, if the row ends there, at from + i * step.  Writes the head's
+// output, or the parts' sum to `to`.  GLOBAL: other blocks wrote the records,
+// so they are read past L1.
+template <class P, bool GLOBAL>
+__device__ __forceinline__ void join(const AttendArgs &p, const float *from, int64_t step, const Part &part, int count, bool ended,
+                                     int g, int lane, float *to) {
+    using R = Record<P>;
+    const int c = part.vh / p.tiles, t = part.vh - c * p.tiles, head = c * p.group + t * P::GT + g;
+    if (g >= min(P::GT, p.group - t * P::GT)) return;
+    auto record = [&](int i) { return from + i * step + (ended && i == count - 1 ? 0 : R::FLOATS); };
+    auto one = [&](const float *at) { return GLOBAL ? __ldcg(at) : *at; };
+    auto four = [&](const float *at) {
+        return GLOBAL ? __ldcg(reinterpret_cast<const float4 *>(at)) : *reinterpret_cast<const float4 *>(at);
+    };
+    float m = -INFINITY, l = 0.0f;
+    for (int i = lane; i < count; i += 32) m = fmaxf(m, one(record(i) + P::GT * R::ROW + g));
 #pragma unroll
-            for (int u = 0; u < BATCH; ++u) {
-                const auto r = rec(min(i0 + u, count - 1));
-                mi[u] = i0 + u < count ? r.one(P::GT * Record<P>::ROW + g) : -INFINITY;
-                li[u] = r.one(P::GT * Record<P>::ROW + P::GT + g);
-                v[u] = r.four(g * Record<P>::ROW + d);
-            }
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float base = base_of(m);
+    constexpr int QUADS = P::DP / 4, PER = (QUADS + 31) / 32;  // quads of elements, of a lane
+    float4 sum[PER];
 #pragma unroll
-            for (int u = 0; u < BATCH; ++u) top = fmaxf(top, mi[u]);
-            const float base = base_of(top), keep = pow2(m - base);
-            m = top;
-            l *= keep, sum.x *= keep, sum.y *= keep, sum.z *= keep, sum.w *= keep;
+    for (int j = 0; j < PER; ++j) sum[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = 0; i0 < count; i0 += 32) {
+        float w = 0.0f;
+        if (i0 + lane < count) {
+            const float *rec = record(i0 + lane) + P::GT * R::ROW + g;
+            w = pow2(one(rec) - base);
+            l = fmaf(w, one(rec + P::GT), l);
+        }
+        const int n = min(32, count - i0);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            const float *rec = record(i0 + i) + g * R::ROW;
 #pragma unroll
-            for (int u = 0; u < BATCH; ++u) {
-                if (i0 + u >= count) break;
-                const float w = pow2(mi[u] - base);
-                l = fmaf(w, li[u], l);
-                sum.x = fmaf(w, v[u].x, sum.x), sum.y = fmaf(w, v[u].y, sum.y);
-                sum.z = fmaf(w, v[u].z, sum.z), sum.w = fmaf(w, v[u].w, sum.w);
+            for (int j = 0; j < PER; ++j) {
+                const int quad = lane + 32 * j;
+                if (QUADS % 32 == 0 || quad < QUADS) {
+                    const float4 v = four(rec + 4 * quad);
+                    sum[j].x = fmaf(wi, v.x, sum[j].x), sum[j].y = fmaf(wi, v.y, sum[j].y);
+                    sum[j].z = fmaf(wi, v.z, sum[j].z), sum[j].w = fmaf(wi, v.w, sum[j].w);
+                }
             }
         }
-        out(g, d, sum, m, l);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    const float inv = inverse(l);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int d = 4 * (lane + 32 * j);
+        if (QUADS % 32 != 0 && d >= P::DP) break;
+        if (to) {
+            *reinterpret_cast<float4 *>(to + g * R::ROW + d) = sum[j];
+        } else {
+            write_out<P>(p, part.b, head, d, sum[j].x, sum[j].y, inv);
+            write_out<P>(p, part.b, head, d + 2, sum[j].z, sum[j].w, inv);
+        }
+    }
+    if (lane == 0) {
+        if (to) to[P::GT * R::ROW + g] = m, to[P::GT * R::ROW + P::GT + g] = l;
+        else write_lse(p, part.b, head, m, l);
     }
 }
-struct SharedRecord {
-    const float *at;
-    __device__ __forceinline__ float one(int f) const { return at[f]; }
-    __device__ __forceinline__ float4 four(int f) const { return *reinterpret_cast<const float4 *>(at + f); }
-};
-struct GlobalRecord {  // written by other blocks: read past L1
-    const float *at;
-    __device__ __forceinline__ float one(int f) const { return __ldcg(at + f); }
-    __device__ __forceinline__ float4 four(int f) const { return __ldcg(reinterpret_cast<const float4 *>(at + f)); }
-};
 
 template <class P>
 __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendArgs p) {
@@ -881,27 +902,12 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
         last_arrived[0] = last_arrived[1] = -1;
     }
     __syncthreads();
-    for (int n = 0; n < num_parts; ++n) {
-        const Part part = parts[n];
-        const int c = part.vh / p.tiles, t = part.vh % p.tiles, h0 = c * p.group + t * P::GT;
-        const char *first = smem + R::PREFIX + part.first * R::WARP;
-        float *to = p.block_rec + ((int64_t)blockIdx.x * 2 + (part.ended ? 0 : 1)) * R::FLOATS;
-        join<P>(part.last - part.first + 1, min(P::GT, p.group - t * P::GT),
-                [&](int i) {
-                    return SharedRecord{reinterpret_cast<const float *>(first + i * R::WARP) +
-                                        (part.ended && part.first + i == part.last ? 0 : R::FLOATS)};
-                },
-                [&](int g, int d, float4 v, float m, float l) {
-                    if (part.ended && !part.before) {
-                        const float inv = inverse(l);
-                        write_out<P>(p, part.b, h0 + g, d, v.x, v.y, inv);
-                        write_out<P>(p, part.b, h0 + g, d + 2, v.z, v.w, inv);
-                        if (d == 0) write_lse(p, part.b, h0 + g, m, l);
-                    } else {
-                        *reinterpret_cast<float4 *>(to + g * R::ROW + d) = v;
-                        if (d == 0) to[P::GT * R::ROW + g] = m, to[P::GT * R::ROW + P::GT + g] = l;
-                    }
-                });
+    const int most_heads = min(P::GT, p.group);
+    for (int i = warp; i < num_parts * most_heads; i += P::NW) {
+        const Part part = parts[i / most_heads];
+        const float *from = reinterpret_cast<const float *>(smem + R::PREFIX + part.first * R::WARP);
+        float *to = part.ended && !part.before ? nullptr : p.block_rec + ((int64_t)blockIdx.x * 2 + (part.ended ? 0 : 1)) * R::FLOATS;
+        join<P, false>(p, from, R::WARP / 4, part, part.last - part.first + 1, part.ended, i % most_heads, lane, to);
     }
     if (num_parts == 0) return;
     const bool cut_before = parts[0].before, cut_after = !parts[num_parts - 1].ended;
@@ -933,15 +939,8 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
         const Part part = parts[last_arrived[side]];
         int first, last;
         blocks_of(part, first, last);
-        const int c = part.vh / p.tiles, t = part.vh % p.tiles, h0 = c * p.group + t * P::GT;
-        join<P>(last - first + 1, min(P::GT, p.group - t * P::GT),
-                [&](int i) { return GlobalRecord{p.block_rec + ((int64_t)(first + i) * 2 + (first + i == last ? 0 : 1)) * R::FLOATS}; },
-                [&](int g, int d, float4 v, float m, float l) {
-                    const float inv = inverse(l);
-                    write_out<P>(p, part.b, h0 + g, d, v.x, v.y, inv);
-                    write_out<P>(p, part.b, h0 + g, d + 2, v.z, v.w, inv);
-                    if (d == 0) write_lse(p, part.b, h0 + g, m, l);
-                });
+        for (int g = warp; g < most_heads; g += P::NW)
+            join<P, true>(p, p.block_rec + (int64_t)first * 2 * R::FLOATS, 2 * R::FLOATS, part, last - first + 1, true, g, lane, nullptr);
     }
 }
 
