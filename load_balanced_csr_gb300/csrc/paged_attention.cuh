@@ -59,6 +59,7 @@ struct AttendArgs {
     uint32_t flip;   // sign bits of a pair of 16-bit elements, set when scale < 0: q is negated
     uint32_t page_mul, page_shift;  // t / page_size = (mulhi(t, page_mul) + t) >> page_shift
     int32_t q_pairs, out_pairs;     // pairs of elements of q, of out, are aligned
+    int32_t same_strides;           // of the two caches
     int32_t *arrivals;   // [blocks], zero between calls
     float *warp_rec;     // [blocks * warps] records
     float *block_rec;    // [blocks][2] records: of the row that began earlier and ends here, of the one that goes on
@@ -768,22 +769,27 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
                 }
             }
         } else {
-            // each lane copies a share of its own position's row
+            // row by row, each position's offsets from its lane; neighbouring lanes copy neighbours here too (each
+            // lane copying a share of its own position's row took 313 us instead of 268 with 64-element heads
+            // and 7 positions a page, 130 instead of 82 with one)
             if (in && !real && lane < P::CH) atomicOr(p.a.status, kBadPage);
-            constexpr int PARTS = 32 / P::CH;
-            const int part = lane / P::CH;
             const int64_t pg = real ? page : 0, in0 = real ? inside : 0;
-            const T *ks = static_cast<const T *>(p.a.k_cache) + pg * p.a.k_stride[0] + in0 * p.a.k_stride[1] +
-                          kv_head * p.a.k_stride[2] + part * PER;
-            const T *vs = static_cast<const T *>(p.a.v_cache) + pg * p.a.v_stride[0] + in0 * p.a.v_stride[1] +
-                          kv_head * p.a.v_stride[2] + part * PER;
-            const uint32_t to = dst + tok * P::PITCH + part * 16;
+            const int64_t ko = pg * p.a.k_stride[0] + in0 * p.a.k_stride[1] + kv_head * p.a.k_stride[2];
+            const int64_t vo = pg * p.a.v_stride[0] + in0 * p.a.v_stride[1] + kv_head * p.a.v_stride[2];
+            const T *kc = static_cast<const T *>(p.a.k_cache), *vc = static_cast<const T *>(p.a.v_cache);
 #pragma unroll
-            for (int i = 0; i < VPR / PARTS; ++i)
-                if ((part + i * PARTS) * PER < p.a.head_dim) {
-                    copy16(to + i * PARTS * 16, ks + i * PARTS * PER, real);
-                    copy16(to + P::CH * P::PITCH + i * PARTS * 16, vs + i * PARTS * PER, real);
+            for (int i = 0; i < P::CH * VPR / 32; ++i) {
+                const int e = lane + 32 * i, row = e / VPR, col = e % VPR;
+                const int64_t kr = __shfl_sync(0xffffffffu, ko, row);
+                int64_t vr = kr;
+                if (!p.same_strides) vr = __shfl_sync(0xffffffffu, vo, row);
+                const bool there = (mask >> row) & 1;
+                const uint32_t to = dst + row * P::PITCH + col * 16;
+                if (col * PER < p.a.head_dim) {
+                    copy16(to, kc + kr + col * PER, there);
+                    copy16(to + P::CH * P::PITCH, vc + vr + col * PER, there);
                 }
+            }
         }
         if (++at >= end) {
             live = false;
@@ -969,6 +975,7 @@ cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStrea
     };
     p.q_pairs = pairs(a.q, a.q_stride);
     p.out_pairs = pairs(a.out, a.out_stride);
+    p.same_strides = std::equal(a.k_stride, a.k_stride + 3, a.v_stride);
     // Division by a constant d < 2^31 of t < 2^31 ("Division by Invariant Integers using Multiplication", Granlund and
     // Montgomery, 1994, section 4): with 2^s >= d > 2^(s-1) and m = floor(2^32 (2^s - d) / d) + 1,
     // t / d = (mulhi(m, t) + t) >> s; the sum stays below 2^32.

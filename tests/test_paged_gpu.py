@@ -258,7 +258,7 @@ class Requests:
             p = torch.exp(s - want_lse[:, None])
             want = torch.einsum("hn,nhd->hd", p, v)
             spread = torch.einsum("hn,nhd->hd", p, v.abs())
-            size = scale * torch.einsum("hd,nhd->hn", q.abs(), k.abs()).amax(1)
+            size = abs(scale) * torch.einsum("hd,nhd->hn", q.abs(), k.abs()).amax(1)
             e = 2 * (dim + 8) * V * size + 2.0 ** -20 * (1 + (s - want_lse[:, None]).abs().amax(1))
             bound = (2 * e + 2 * n * V + u)[:, None] * spread + u * want.abs() + TINY[self.dtype]
             err = (out[b].double() - want).abs()
@@ -326,6 +326,25 @@ def test_attention_views_and_streams(dtype):
     s.synchronize()
     r.check(out, lse, 64 ** -0.5)
     assert (wide[:, 0] == 7).all() and (wide[:, 7] == 7).all() and (wide[:, :, :3] == 7).all() and (wide[:, :, 67:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim,page", [(64, 16), (64, 7), (128, 64), (128, 5), (96, 16)])
+def test_attention_caches_of_two_layouts(dim, page, dtype):
+    """Keys kept token by token, values head by head."""
+    r = Requests([77, 0, 300, 5, 1024], 6, 2, dim, page, dtype, seed=dim)
+    held = r.v
+    r.v = _cache(held.shape[0], page, 2, dim, dtype, "heads")
+    r.v.copy_(held)
+    assert r.v.stride() != r.k.stride()
+    attend = r.attention()
+    out, lse = attend(r.q, r.k, r.v, r.table, r.lens)
+    assert attend.device_status() == 0
+    r.check(out, lse, dim ** -0.5)
+    out, lse = attend(r.q, r.k, r.v, r.table, r.lens, scale=-0.11)  # a negative scale turns the scores around
+    r.check(out, lse, -0.11)
+    out, lse = attend(r.q, r.k, r.v, r.table, r.lens, scale=0.0)    # no scale: the values' mean
+    r.check(out, lse, 0.0)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
