@@ -27,6 +27,17 @@ inline int elem_size(int elem) { return elem == SPMV_ELEM_F32 ? 4 : 2; }
 
 inline bool aligned_to(const void *p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
 
+// Division by a constant d, 1 <= d < 2^31 ("Division by Invariant Integers
+// using Multiplication", Granlund and Montgomery, 1994, section 4): with
+// 2^s >= d > 2^(s-1) and m = floor(2^32 (2^s - d) / d) + 1, t / d =
+// (mulhi(m, t) + t) >> s for every t < 2^32; for t < 2^31 the sum fits 32 bits.
+inline void set_divisor(uint32_t d, uint32_t *mul, uint32_t *shift) {
+    uint32_t s = 0;
+    while ((1ull << s) < d) ++s;
+    *mul = (uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+    *shift = s;
+}
+
 // N consecutive elements, moved by one load or store of sizeof(Vec) bytes.
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Vec {

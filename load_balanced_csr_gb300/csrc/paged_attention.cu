@@ -7,16 +7,17 @@ namespace lbcsr {
 
 namespace {
 
+// Stages as shared memory allows beside the queries.
 template <int GT, typename F>
 auto with_f32(int dim, F f) {
-    if (dim <= 64) return f(TileF32<64, GT, 8, 5>());
-    if (dim <= 96) return f(TileF32<96, GT, 8, 4>());
-    if (dim <= 128) return f(TileF32<128, GT, 8, 3>());
-    return f(TileF32<256, GT, 4, 3>());
+    if (dim <= 64) return f(TileF32<64, GT, 8, 4>());
+    if (dim <= 96) return f(TileF32<96, GT, 8, GT == 8 ? 3 : 4>());
+    if (dim <= 128) return f(TileF32<128, GT, 8, GT == 8 ? 2 : 3>());
+    return f(TileF32<256, GT, 4, GT == 8 ? 2 : 3>());
 }
 template <typename F>
 auto with_f32(int dim, int group, F f) {
-    return group == 1 ? with_f32<1>(dim, f) : with_f32<4>(dim, f);
+    return group == 1 ? with_f32<1>(dim, f) : group <= 4 ? with_f32<4>(dim, f) : with_f32<8>(dim, f);
 }
 
 const char *heads_bad(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int elem) {

@@ -403,14 +403,17 @@ struct TileF32 {
             }
         }
         float *weights = reinterpret_cast<float *>(qs + WEIGHTS);  // [position][head]
-        float own = 0.0f;
 #pragma unroll
-        for (int g = 0; g < GT; ++g) {
-            const float w = live ? pow2(fmaf(s[g], p.scale2, -base_of(m[g]))) : 0.0f;
-            if (quarter == 0) l[g] += w;
-            if (quarter == g) own = w;
+        for (int j = 0; j < GT; j += 4) {  // a quarter stores one head of four
+            float own = 0.0f;
+#pragma unroll
+            for (int g = j; g < GT && g < j + 4; ++g) {
+                const float w = live ? pow2(fmaf(s[g], p.scale2, -base_of(m[g]))) : 0.0f;
+                if (quarter == 0) l[g] += w;
+                if (quarter == g - j) own = w;
+            }
+            if (j + quarter < GT) weights[pos * GT + j + quarter] = own;
         }
-        if (quarter < GT) weights[pos * GT + quarter] = own;
         __syncwarp();
         const char *v = stage + CH * PITCH;
 #pragma unroll
@@ -462,7 +465,7 @@ struct Record {
     static constexpr int WARP = P::STAGES * STAGE + P::QBYTES;          // bytes of a warp's shared memory
     static_assert(2 * FLOATS * 4 <= P::STAGES * STAGE, "both records of a warp fit its stages");
     static_assert(FLOATS % 4 == 0 && ROW % 4 == 0 && P::PITCH % 16 == 0 && P::QBYTES % 16 == 0, "16-byte accesses");
-    static constexpr int PREFIX = (4 * (2 * kMaxSlice + 1) + 15) / 16 * 16;
+    static constexpr int PREFIX = (4 * (2 * kMaxSlice + 1) + 127) / 128 * 128;
     static constexpr int SMEM = PREFIX + P::NW * WARP;
 };
 
@@ -976,12 +979,7 @@ cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStrea
     p.q_pairs = pairs(a.q, a.q_stride);
     p.out_pairs = pairs(a.out, a.out_stride);
     p.same_strides = std::equal(a.k_stride, a.k_stride + 3, a.v_stride);
-    // Division by a constant d < 2^31 of t < 2^31 ("Division by Invariant Integers using Multiplication", Granlund and
-    // Montgomery, 1994, section 4): with 2^s >= d > 2^(s-1) and m = floor(2^32 (2^s - d) / d) + 1,
-    // t / d = (mulhi(m, t) + t) >> s; the sum stays below 2^32.
-    p.page_shift = 0;
-    while ((1ull << p.page_shift) < (uint64_t)a.page_size) ++p.page_shift;
-    p.page_mul = (uint32_t)(((1ull << 32) * ((1ull << p.page_shift) - (uint64_t)a.page_size)) / (uint64_t)a.page_size + 1);
+    set_divisor((uint32_t)a.page_size, &p.page_mul, &p.page_shift);
     char *w = static_cast<char *>(a.workspace);
     p.arrivals = reinterpret_cast<int32_t *>(w);
     p.warp_rec = reinterpret_cast<float *>(w + align16(4 * (size_t)sms));

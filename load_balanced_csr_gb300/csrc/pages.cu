@@ -20,7 +20,9 @@ namespace lbcsr {
 namespace {
 
 // ---------------------------------------------------------------- append
-constexpr int kAppendThreads = 512;
+constexpr int kAppendThreads = 1024;
+constexpr int kRequestsPerThread = 4;  // consecutive: 4096 requests are read at once
+static_assert(kAppendThreads == 1024, "a warp's lanes are the block's warps when their sums are added");
 constexpr int kTokensPerThread = 4;    // consecutive, so that they are stored together
 constexpr int kBlockRequests = 4096;
 
@@ -39,7 +41,15 @@ struct AppendArgs {
     int64_t ld_table;
     int32_t *token_ptr, *lens, *slots, *positions, *taken, *status;
     Request *made;  // workspace [requests], more than kBlockRequests only
+    uint32_t page_mul, page_shift;  // division by the page size
 };
+
+// t / page for t < 2^32: (mulhi(t, page_mul) + t) >> page_shift without losing the sum's carry.
+__device__ __forceinline__ uint32_t page_at(const AppendArgs &a, uint32_t t) {
+    return (uint32_t)(((unsigned long long)__umulhi(t, a.page_mul) + t) >> a.page_shift);
+}
+// the pages of n tokens
+__device__ __forceinline__ uint32_t pages_of(const AppendArgs &a, uint32_t n) { return n ? page_at(a, n - 1) + 1 : 0; }
 
 __device__ __forceinline__ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -52,20 +62,26 @@ __device__ __forceinline__ void scan_requests(const AppendArgs &a, Request *req,
     long long carry = 0;  // pages << 32 | tokens
     int32_t flags = 0, used = 0;
     if (threadIdx.x == 0) all_used = 0;
-    for (int64_t r0 = 0; r0 < a.requests; r0 += kAppendThreads) {
-        const int64_t r = r0 + threadIdx.x;
-        int32_t past = 0, fresh = 0, need = 0;
-        bool fits = true;
-        if (r < a.requests) {
-            past = a.past[r], fresh = a.fresh[r];
-            if (past < 0 || fresh < 0) flags |= kBadLength, past = max(past, 0), fresh = max(fresh, 0);
-            const long long held = ((long long)past + a.page - 1) / a.page;
-            const long long want = ((long long)past + fresh + a.page - 1) / a.page;
-            if (held > a.max_pages) fits = false, flags |= kBadLength;
-            else if (want > a.max_pages) fits = false, flags |= kRowShort;
-            else need = (int32_t)(want - held);
+    for (int64_t r0 = 0; r0 < a.requests; r0 += kAppendThreads * kRequestsPerThread) {
+        const int64_t r1 = r0 + threadIdx.x * kRequestsPerThread;
+        int32_t past[kRequestsPerThread], fresh[kRequestsPerThread], need[kRequestsPerThread];
+        bool fits[kRequestsPerThread];
+#pragma unroll
+        for (int j = 0; j < kRequestsPerThread; ++j) {
+            past[j] = r1 + j < a.requests ? a.past[r1 + j] : 0;
+            fresh[j] = r1 + j < a.requests ? a.fresh[r1 + j] : 0;
         }
-        const long long mine = ((long long)need << 32) + fresh;
+        long long mine = 0;
+#pragma unroll
+        for (int j = 0; j < kRequestsPerThread; ++j) {
+            if (past[j] < 0 || fresh[j] < 0) flags |= kBadLength, past[j] = max(past[j], 0), fresh[j] = max(fresh[j], 0);
+            const uint32_t held = pages_of(a, (uint32_t)past[j]), want = pages_of(a, (uint32_t)past[j] + (uint32_t)fresh[j]);
+            fits[j] = true, need[j] = 0;
+            if (held > (uint32_t)a.max_pages) fits[j] = false, flags |= kBadLength;
+            else if (want > (uint32_t)a.max_pages) fits[j] = false, flags |= kRowShort;
+            else need[j] = (int32_t)(want - held);
+            mine += ((long long)need[j] << 32) + fresh[j];
+        }
         long long scan = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -74,21 +90,26 @@ __device__ __forceinline__ void scan_requests(const AppendArgs &a, Request *req,
         }
         if (lane == 31) warp_sum[warp] = scan;
         __syncthreads();
-        long long start = carry + scan - mine;
+        long long before = lane < warp ? warp_sum[lane] : 0, all = warp_sum[lane];
 #pragma unroll
-        for (int w = 0; w < kAppendThreads / 32; ++w) {
-            const long long s = warp_sum[w];
-            if (w < warp) start += s;
-            carry += s;
+        for (int d = 16; d > 0; d >>= 1) {
+            before += __shfl_xor_sync(0xffffffffu, before, d);
+            all += __shfl_xor_sync(0xffffffffu, all, d);
         }
-        if (r < a.requests) {
+        long long start = carry + before + scan - mine;
+        carry += all;
+#pragma unroll
+        for (int j = 0; j < kRequestsPerThread; ++j) {
+            const int64_t r = r1 + j;
+            if (r >= a.requests) break;
             const int32_t first = (int32_t)(start >> 32), tokens = (int32_t)start;
-            bool served = fits;
-            if (need > 0 && (long long)first + need > a.num_free) served = false, flags |= kFreeEnded;
-            if (fresh > 0 && (long long)tokens + fresh > a.max_tokens) served = false, flags |= kTooManyTokens;
-            if (served && need > 0) used = max(used, first + need);
-            req[r] = Request{tokens, past, served ? first : -1};
-            if (writes) a.token_ptr[r] = tokens, a.lens[r] = served ? past + fresh : past;
+            bool served = fits[j];
+            if (need[j] > 0 && (long long)first + need[j] > a.num_free) served = false, flags |= kFreeEnded;
+            if (fresh[j] > 0 && (long long)tokens + fresh[j] > a.max_tokens) served = false, flags |= kTooManyTokens;
+            if (served && need[j] > 0) used = max(used, first + need[j]);
+            req[r] = Request{tokens, past[j], served ? first : -1};
+            if (writes) a.token_ptr[r] = tokens, a.lens[r] = served ? past[j] + fresh[j] : past[j];
+            start += ((long long)need[j] << 32) + fresh[j];
         }
         __syncthreads();
     }
@@ -134,10 +155,11 @@ __global__ void __launch_bounds__(kAppendThreads) pages_append_kernel(AppendArgs
             if (i >= tokens) continue;
             while (r + 1 < a.requests && req[r + 1].token <= i) ++r;
             const Request now = req[r];
-            const int32_t at = now.past + (int32_t)(i - now.token), page = at / a.page, inside = at - page * a.page;
+            const int32_t at = now.past + (int32_t)(i - now.token);
+            const int32_t page = (int32_t)page_at(a, (uint32_t)at), inside = at - page * a.page;
             position[u] = at;
             if (now.first < 0 || at < 0 || page >= a.max_pages) continue;  // the last two only if sums passed 32 bits
-            const int32_t held = (int32_t)(((long long)now.past + a.page - 1) / a.page);
+            const int32_t held = (int32_t)pages_of(a, (uint32_t)now.past);
             const int64_t place = (int64_t)now.first + page - held;
             int32_t *entry = a.table + r * a.ld_table + page;
             int32_t id = -1;
@@ -250,6 +272,7 @@ spmv_status_t spmv_pages_append(int32_t requests, const int32_t *past, const int
     a.token_ptr = token_ptr, a.lens = lens, a.slots = slots, a.positions = positions, a.taken = taken;
     a.status = status;
     a.made = static_cast<Request *>(workspace);
+    set_divisor((uint32_t)page_size, &a.page_mul, &a.page_shift);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
     const int64_t per_block = (int64_t)kAppendThreads * kTokensPerThread;
     const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>((max_tokens + per_block - 1) / per_block, 2 * device_sm_count()));
