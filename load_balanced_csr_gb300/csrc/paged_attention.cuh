@@ -674,6 +674,7 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     char *mine = smem + R::PREFIX + warp * R::WARP;
     char *qs = mine + P::STAGES * R::STAGE;
+    after_previous();
     const Rows rows = load_rows<P>(p, smem);
     for (int b = blockIdx.x; b < p.a.batch; b += gridDim.x) {
         if (rows.pre[b + 1] != rows.pre[b]) continue;  // nothing to attend to: zeros
@@ -996,8 +997,7 @@ cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStrea
         p.a.table = a.table + b * a.table_stride;
         p.a.lens = a.lens + b;
         const int64_t blocks = std::min<int64_t>(sms, most * p.a.batch);
-        paged_attention_kernel<P><<<(unsigned)blocks, P::NW * 32, R::SMEM, stream>>>(p);
-        e = cudaGetLastError();
+        e = launch_chained(paged_attention_kernel<P>, (unsigned)blocks, P::NW * 32, R::SMEM, 0, stream, p);
     }
     return e;
 }

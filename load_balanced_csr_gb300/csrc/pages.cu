@@ -123,13 +123,17 @@ __device__ __forceinline__ void scan_requests(const AppendArgs &a, Request *req,
     }
 }
 
-__global__ void __launch_bounds__(kAppendThreads) pages_scan_kernel(AppendArgs a) { scan_requests(a, a.made, true); }
+__global__ void __launch_bounds__(kAppendThreads) pages_scan_kernel(AppendArgs a) {
+    after_previous();
+    scan_requests(a, a.made, true);
+}
 
 // SCAN: the block makes the prefix sums itself.
 template <bool SCAN>
 __global__ void __launch_bounds__(kAppendThreads) pages_append_kernel(AppendArgs a) {
     extern __shared__ __align__(16) char smem[];
     const Request *req = a.made;
+    after_previous();
     if (SCAN) {
         scan_requests(a, reinterpret_cast<Request *>(smem), blockIdx.x == 0);
         req = reinterpret_cast<const Request *>(smem);
@@ -198,6 +202,7 @@ __global__ void __launch_bounds__(kStoreThreads)
 paged_store_kernel(StoreArgs a, const T *__restrict__ k, const T *__restrict__ v, T *__restrict__ kc,
                    T *__restrict__ vc) {
     using V = Vec<T, N>;
+    after_previous();
     const int lane = threadIdx.x & 31;
     const int64_t i = (int64_t)blockIdx.x * (kStoreThreads / 32) + (threadIdx.x >> 5);
     if (i >= a.tokens) return;
@@ -217,9 +222,8 @@ paged_store_kernel(StoreArgs a, const T *__restrict__ k, const T *__restrict__ v
 template <typename T, int N>
 cudaError_t launch_store(const StoreArgs &a, const void *k, const void *v, void *kc, void *vc, cudaStream_t stream) {
     const unsigned blocks = (unsigned)((a.tokens + (int64_t)kStoreThreads / 32 - 1) / (kStoreThreads / 32));
-    paged_store_kernel<T, N><<<blocks, kStoreThreads, 0, stream>>>(a, static_cast<const T *>(k), static_cast<const T *>(v),
-                                                                   static_cast<T *>(kc), static_cast<T *>(vc));
-    return cudaGetLastError();
+    return launch_chained(paged_store_kernel<T, N>, blocks, kStoreThreads, 0, 0, stream, a, static_cast<const T *>(k),
+                          static_cast<const T *>(v), static_cast<T *>(kc), static_cast<T *>(vc));
 }
 
 bool on_16(const void *p, const int64_t *strides, int n, int size) {
@@ -281,17 +285,11 @@ spmv_status_t spmv_pages_append(int32_t requests, const int32_t *past, const int
         const size_t smem = sizeof(Request) * ((size_t)requests + 1);
         if (smem > 47 * 1024)
             e = cudaFuncSetAttribute(pages_append_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e == cudaSuccess) {
-            pages_append_kernel<true><<<blocks, kAppendThreads, smem, stream>>>(a);
-            e = cudaGetLastError();
-        }
+        if (e == cudaSuccess) e = launch_chained(pages_append_kernel<true>, blocks, kAppendThreads, smem, 0, stream, a);
     } else {
-        pages_scan_kernel<<<1, kAppendThreads, 0, stream>>>(a);
-        e = cudaGetLastError();
-        if (e == cudaSuccess && max_tokens > 0) {
-            pages_append_kernel<false><<<blocks, kAppendThreads, 0, stream>>>(a);
-            e = cudaGetLastError();
-        }
+        e = launch_chained(pages_scan_kernel, 1, kAppendThreads, 0, 0, stream, a);
+        if (e == cudaSuccess && max_tokens > 0)
+            e = launch_chained(pages_append_kernel<false>, blocks, kAppendThreads, 0, 0, stream, a);
     }
     return llm_launched("spmv_pages_append launch", e);
 }

@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kBuildThreads)
 route_hist_kernel(const I *__restrict__ ids, int64_t ld, int k, int64_t n, int experts, int64_t tile,
                   int32_t *__restrict__ hist) {
     extern __shared__ int32_t h[];
+    after_previous();
     const int bins = experts + 1;
     for (int b = threadIdx.x; b < bins; b += kBuildThreads) h[b] = 0;
     __syncthreads();
@@ -98,6 +99,7 @@ route_rank_kernel(const I *__restrict__ ids, int64_t ld, int k, int64_t n, int e
                   const int32_t *__restrict__ hist, int32_t *__restrict__ expert_ptr, int32_t *__restrict__ entry,
                   int32_t *__restrict__ slot) {
     extern __shared__ int32_t smem[];
+    after_previous();
     __shared__ int32_t warp_sum[kBuildWarps];
     const int bins = experts + 1, bits = 32 - __clz(bins);  // keys, and `bins` for no entry
     int32_t *base = smem, *total = smem + bins, *sum = smem + 2 * bins;
@@ -236,24 +238,12 @@ cudaError_t launch_build(int64_t n, int k, int experts, const I *ids, int64_t ld
         if (e != cudaSuccess) return e;
     }
     if (!clustered) {
-        route_hist_kernel<I><<<tiles, kBuildThreads, bins * 4, stream>>>(ids, ld, k, n, experts, tile, hist);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_chained(route_hist_kernel<I>, tiles, kBuildThreads, bins * 4, 0, stream, ids, ld, k, n,
+                                             experts, tile, hist);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)tiles;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t config = {};
-    config.gridDim = dim3((unsigned)tiles);
-    config.blockDim = dim3(kBuildThreads);
-    config.dynamicSmemBytes = smem;
-    config.stream = stream;
-    config.attrs = &attr;
-    config.numAttrs = clustered ? 1 : 0;
-    const int32_t *counted = clustered ? nullptr : hist;
-    return cudaLaunchKernelEx(&config, route_rank_kernel<I>, ids, ld, k, n, experts, tile, tiles, counted, expert_ptr,
-                              entry, slot);
+    return launch_chained(route_rank_kernel<I>, tiles, kBuildThreads, smem, clustered ? tiles : 0, stream, ids, ld, k, n,
+                          experts, tile, tiles, clustered ? nullptr : hist, expert_ptr, entry, slot);
 }
 
 // ---------------------------------------------------------------- rows
@@ -275,6 +265,7 @@ template <typename T, int N, int U>
 __global__ void __launch_bounds__(kRowThreads)
 route_dispatch_kernel(RowArgs a, const T *__restrict__ x, int64_t ldx, T *__restrict__ xs, int64_t ldxs) {
     using V = Vec<T, N>;
+    after_previous();
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     if (item >= a.items) return;
@@ -300,6 +291,7 @@ template <typename T, int N, int U>
 __global__ void __launch_bounds__(kRowThreads)
 route_combine_kernel(RowArgs a, const T *__restrict__ ys, int64_t ldys, T *__restrict__ y, int64_t ldy) {
     using V = Vec<T, N>;
+    after_previous();
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     if (item >= a.items) return;
@@ -368,6 +360,7 @@ __global__ void __launch_bounds__(kBackThreads)
 route_combine_backward_kernel(RowArgs a, const T *__restrict__ dy, int64_t lddy, const T *ys, int64_t ldys, T *dys,
                               int64_t lddys, float *__restrict__ dw, int64_t lddw) {
     using V = Vec<T, N>;
+    after_previous();
     __shared__ float part[K][kBackThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = blockIdx.x;
@@ -455,9 +448,8 @@ template <typename T, int N, int U>
 cudaError_t launch_dispatch_u(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const void *x, int64_t ldx,
                               void *xs, int64_t ldxs, cudaStream_t stream) {
     const RowArgs a = row_args(tokens, k, hidden, N, U, slot, nullptr, 0);
-    route_dispatch_kernel<T, N, U><<<row_blocks(a), kRowThreads, 0, stream>>>(a, static_cast<const T *>(x), ldx,
-                                                                              static_cast<T *>(xs), ldxs);
-    return cudaGetLastError();
+    return launch_chained(route_dispatch_kernel<T, N, U>, row_blocks(a), kRowThreads, 0, 0, stream, a,
+                          static_cast<const T *>(x), ldx, static_cast<T *>(xs), ldxs);
 }
 template <typename T, int N>
 cudaError_t launch_dispatch(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const void *x, int64_t ldx,
@@ -470,9 +462,8 @@ template <typename T, int N, int U>
 cudaError_t launch_combine_u(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const float *w, int64_t ldw,
                              const void *ys, int64_t ldys, void *y, int64_t ldy, cudaStream_t stream) {
     const RowArgs a = row_args(tokens, k, hidden, N, U, slot, w, ldw);
-    route_combine_kernel<T, N, U><<<row_blocks(a), kRowThreads, 0, stream>>>(a, static_cast<const T *>(ys), ldys,
-                                                                             static_cast<T *>(y), ldy);
-    return cudaGetLastError();
+    return launch_chained(route_combine_kernel<T, N, U>, row_blocks(a), kRowThreads, 0, 0, stream, a,
+                          static_cast<const T *>(ys), ldys, static_cast<T *>(y), ldy);
 }
 template <typename T, int N>
 cudaError_t launch_combine(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const float *w, int64_t ldw,
@@ -484,9 +475,9 @@ cudaError_t launch_combine(int32_t tokens, int32_t k, int32_t hidden, const int3
 template <typename T, int N, int K, int U>
 cudaError_t launch_combine_backward_k(const RowArgs &a, int32_t tokens, const void *dy, int64_t lddy, const void *ys,
                                       int64_t ldys, void *dys, int64_t lddys, float *dw, int64_t lddw, cudaStream_t stream) {
-    route_combine_backward_kernel<T, N, K, U><<<(unsigned)tokens, kBackThreads, 0, stream>>>(
-        a, static_cast<const T *>(dy), lddy, static_cast<const T *>(ys), ldys, static_cast<T *>(dys), lddys, dw, lddw);
-    return cudaGetLastError();
+    return launch_chained(route_combine_backward_kernel<T, N, K, U>, (unsigned)tokens, kBackThreads, 0, 0, stream, a,
+                          static_cast<const T *>(dy), lddy, static_cast<const T *>(ys), ldys, static_cast<T *>(dys), lddys,
+                          dw, lddw);
 }
 template <typename T, int N>
 cudaError_t launch_combine_backward(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const float *w,
