@@ -262,6 +262,8 @@ spmv_status_t spmv_pages_append(int32_t requests, const int32_t *past, const int
     if ((int64_t)num_pages * page_size >= (1LL << 31)) return llm_bad("num_pages * page_size must be < 2^31");
     if (!token_ptr || !taken || !status) return llm_bad("token_ptr, taken or status is NULL");
     if (requests > 0 && (!past || !fresh || !lens)) return llm_bad("past, fresh or lens is NULL");
+    // every block reads the lengths while one writes lens
+    if (requests > 0 && (past == lens || fresh == lens)) return llm_bad("lens must not be past or fresh");
     if (requests > 0 && max_pages > 0 && !table) return llm_bad("table is NULL");
     if (ld_table < max_pages) return llm_bad("ld_table is smaller than max_pages");
     if (num_free > 0 && !free_pages) return llm_bad("free_pages is NULL");

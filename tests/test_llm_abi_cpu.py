@@ -12,6 +12,7 @@ from load_balanced_csr_gb300 import _build
 
 FAKE = ctypes.c_void_p(0x1000)
 ODD = ctypes.c_void_p(0x1001)
+OTHER = ctypes.c_void_p(0x2000)
 BAD = 1
 
 
@@ -65,7 +66,7 @@ def test_pages_refusals():
     assert L.spmv_pages_workspace(100, ctypes.byref(size)) == 0
 
     def append(requests=2, past=FAKE, fresh=FAKE, page=16, num_pages=10, free=FAKE, num_free=4, table=FAKE, ld=8,
-               max_pages=8, max_tokens=5, ptr=FAKE, lens=FAKE, slots=FAKE, positions=FAKE, taken=FAKE, status=FAKE,
+               max_pages=8, max_tokens=5, ptr=FAKE, lens=OTHER, slots=FAKE, positions=FAKE, taken=FAKE, status=FAKE,
                work=FAKE, room=1 << 20):
         return L.spmv_pages_append(requests, past, fresh, page, num_pages, free, num_free, table, ld, max_pages,
                                    max_tokens, ptr, lens, slots, positions, taken, status, work, room, None)
@@ -73,7 +74,7 @@ def test_pages_refusals():
     for bad in (dict(requests=-1), dict(page=0), dict(num_pages=-1), dict(num_free=-1), dict(max_pages=-1, ld=0),
                 dict(max_tokens=-1), dict(num_pages=2 ** 27), dict(past=None), dict(fresh=None), dict(lens=None),
                 dict(ptr=None), dict(taken=None), dict(status=None), dict(table=None), dict(ld=7), dict(free=None),
-                dict(slots=None), dict(positions=None)):
+                dict(slots=None), dict(positions=None), dict(lens=FAKE)):
         assert append(**bad) == BAD, bad
     if size.value:
         assert append(work=None) == BAD and append(room=0) == BAD
