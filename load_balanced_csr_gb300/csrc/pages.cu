@@ -7,8 +7,15 @@
 // row), computes its slot from the table or, for a page not held before, from
 // the free list, and the token that opens a page writes the table's entry.
 // It is bound by latency: up to kBlockRequests requests every block makes the
-// prefix sums for itself in shared memory, and there is one launch; beyond,
-// one block makes them in global memory first.
+// prefix sums for itself in shared memory, and there is one launch (256
+// requests with a token each 6.5 us a step, 2,048 requests with 860 thousand
+// tokens 12.4 us, of which its 6.9 MB are 1 us); beyond, one block makes them
+// in global memory first.  One block's sums and a second launch took 11.6 and
+// 21.8 us.
+//
+// spmv_paged_store: a copy, a warp per token, 16 bytes a lane; 65,535 tokens
+// of 8 heads of 128 f16, 5 % of them padding (510 MB) 79 us: 6.5 TB/s, 0.97 of
+// the measured copy.
 #include <algorithm>
 #include <climits>
 

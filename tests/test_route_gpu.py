@@ -56,7 +56,8 @@ def build(ids, experts, wide, max_tokens=None, stride=None):
 @pytest.mark.parametrize("t,k,experts,drop", [
     (0, 4, 8, 0.0), (1, 1, 1, 0.0), (1, 8, 128, 0.0), (3, 2, 2048, 0.2), (33, 7, 5, 0.3), (512, 8, 128, 0.0),
     (513, 8, 127, 1.0), (2048, 2, 16, 0.1), (2049, 2, 16, 0.1), (4097, 3, 300, 0.05), (20000, 8, 256, 0.0),
-    (100003, 8, 61, 0.01), (5000, 5, 2048, 0.5)])
+    (100003, 8, 61, 0.01), (5000, 5, 2048, 0.5),
+    (16384, 8, 33, 0.0), (16385, 8, 33, 0.0), (200003, 8, 61, 0.01)])  # a cluster's last size, two launches, several rounds
 def test_sorted_by_expert(t, k, experts, drop, wide):
     rng = np.random.default_rng(t + experts)
     ids = random_ids(rng, t, k, experts, drop, skew=t % 2 == 1)
