@@ -335,9 +335,9 @@ struct TileMma {
 // every head of the tile; for the output lane l takes elements 2 l, 2 l + 1,
 // 64 + 2 l, ... of every head.  Products and sums in 32 bits: there is no
 // matrix instruction that keeps 32-bit inputs whole.  Bound by the latency of
-// its instructions with 8 warps an SM: 16 requests of up to 5,000 positions,
-// 4 kv heads of 72 and 3 query heads each, 7 positions a page (98 MB) 40 us;
-// groups of 8 heads with a tile of 8 74 us, with two of 4 102 us.
+// its instructions with 12 warps an SM: 16 requests of up to 5,000 positions,
+// 4 kv heads of 72 and 3 query heads each, 7 positions a page (98 MB) 39 us;
+// groups of 8 heads of 128 with a tile of 8 74 us, with two of 4 102 us.
 template <int DP_, int GT_, int NW_, int STAGES_>
 struct TileF32 {
     using T = float;
@@ -1025,15 +1025,23 @@ cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStrea
 }
 
 // Calls f with the tile of 16-bit elements T for the head size and group.
+//
+// Warps and stages: what an SM's registers and shared memory hold.  Of both
+// measured ways for tiles of 8 heads (64 requests of up to 4,000 positions, 4
+// kv heads): 96 elements 67.6 us with 10 warps of 3 stages, 69.7 with 8 of 4;
+// 128 elements 75.8 with 8 of 3, 86.0 with 10 or 12 of 2, whose registers do
+// not suffice; 192 elements 106 with 8 of 2, 135 with 4 of 4; 256 elements 129
+// with 6 of 2, 133 with 4 of 3.  Tiles of 16 heads need their registers, and
+// their records the stages' room.
 template <typename T, int GT, typename F>
 auto with_mma(int dim, F f) {
+    constexpr bool small = GT == 8;
     if (dim <= 64) return f(TileMma<T, GT, 64, 32, 8, 3>());
-    if (dim <= 96) return f(TileMma<T, GT, 96, 16, 8, 4>());
+    if (dim <= 96) return f(TileMma<T, GT, 96, 16, small ? 10 : 8, small ? 3 : 4>());
     if (dim <= 128) return f(TileMma<T, GT, 128, 16, 8, 3>());
-    if (dim <= 192) return f(TileMma<T, GT, 192, 16, 4, 4>());
-    return f(TileMma<T, GT, 256, 16, 4, 3>());
+    if (dim <= 192) return f(TileMma<T, GT, 192, 16, small ? 8 : 4, small ? 2 : 4>());
+    return f(TileMma<T, GT, 256, 16, small ? 6 : 4, small ? 2 : 3>());
 }
-
 template <typename T, typename F>
 auto with_mma(int dim, int group, F f) {
     return group <= 8 ? with_mma<T, 8>(dim, f) : with_mma<T, 16>(dim, f);
