@@ -9,7 +9,7 @@
 // It is bound by latency: up to kBlockRequests requests every block makes the
 // prefix sums for itself in shared memory, and there is one launch (256
 // requests with a token each 6.5 us a step, 2,048 requests with 860 thousand
-// tokens 12.4 us, of which its 6.9 MB are 1 us); beyond, one block makes them
+// tokens 10.4 us, of which its 6.9 MB are 1 us); beyond, one block makes them
 // in global memory first.  One block's sums and a second launch took 11.6 and
 // 21.8 us.
 //
@@ -158,29 +158,40 @@ __global__ void __launch_bounds__(kAppendThreads) pages_append_kernel(AppendArgs
                 else hi = mid - 1;
             }
         }
-        int32_t slot[kTokensPerThread], position[kTokensPerThread];
+        // where each token's page number is, so that all are read together; then the slots
+        int32_t slot[kTokensPerThread], position[kTokensPerThread], inside[kTokensPerThread], id[kTokensPerThread];
+        const int32_t *from[kTokensPerThread];
+        int32_t *opens[kTokensPerThread];  // the table's entry, for the token that opens a page
 #pragma unroll
         for (int u = 0; u < kTokensPerThread; ++u) {
             const int64_t i = i0 + u;
-            slot[u] = position[u] = -1;
+            slot[u] = position[u] = -1, inside[u] = 0;
+            from[u] = nullptr, opens[u] = nullptr;
             if (i >= tokens) continue;
             while (r + 1 < a.requests && req[r + 1].token <= i) ++r;
             const Request now = req[r];
             const int32_t at = now.past + (int32_t)(i - now.token);
-            const int32_t page = (int32_t)page_at(a, (uint32_t)at), inside = at - page * a.page;
+            const int32_t page = (int32_t)page_at(a, (uint32_t)at);
             position[u] = at;
+            inside[u] = at - page * a.page;
             if (now.first < 0 || at < 0 || page >= a.max_pages) continue;  // the last two only if sums passed 32 bits
             const int32_t held = (int32_t)pages_of(a, (uint32_t)now.past);
             const int64_t place = (int64_t)now.first + page - held;
             int32_t *entry = a.table + r * a.ld_table + page;
-            int32_t id = -1;
             if (page < held) {
-                id = *entry;
+                from[u] = entry;
             } else if (place < a.num_free) {
-                id = __ldg(a.free_pages + place);
-                if (inside == 0) *entry = id;
+                from[u] = a.free_pages + place;
+                if (inside[u] == 0) opens[u] = entry;
             }
-            if ((uint32_t)id < (uint32_t)a.num_pages) slot[u] = id * a.page + inside;
+        }
+#pragma unroll
+        for (int u = 0; u < kTokensPerThread; ++u) id[u] = from[u] ? *from[u] : -1;
+#pragma unroll
+        for (int u = 0; u < kTokensPerThread; ++u) {
+            if (!from[u]) continue;
+            if (opens[u]) *opens[u] = id[u];
+            if ((uint32_t)id[u] < (uint32_t)a.num_pages) slot[u] = id[u] * a.page + inside[u];
             else atomicOr(a.status, kBadPage);
         }
         if (whole && i0 + kTokensPerThread <= a.max_tokens) {
@@ -288,7 +299,8 @@ spmv_status_t spmv_pages_append(int32_t requests, const int32_t *past, const int
     set_divisor((uint32_t)page_size, &a.page_mul, &a.page_shift);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
     const int64_t per_block = (int64_t)kAppendThreads * kTokensPerThread;
-    const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>((max_tokens + per_block - 1) / per_block, 2 * device_sm_count()));
+    // one block an SM (its registers): more would make the prefix sums a second time
+    const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>((max_tokens + per_block - 1) / per_block, device_sm_count()));
     cudaError_t e = cudaSuccess;
     if (requests <= kBlockRequests) {
         const size_t smem = sizeof(Request) * ((size_t)requests + 1);
