@@ -58,12 +58,12 @@ constexpr int kMaxSlice = 1024;  // requests per launch: their lengths and prefi
 // Units a row costs beside its chunks (its queries, its output): without, a
 // batch of 128 requests of 1 to 16,384 positions took 190 us instead of 158,
 // the blocks with the short ones being last.
-constexpr uint32_t kRowCost = 2;
+constexpr uint32_t kRowCost = 3;
 // Rows of so few chunks are not cut between blocks, of so few not between
 // warps: joining would take longer than the row (4 requests of up to 300
 // positions 18.4 us with every row cut alike, 14.3 so; both with L2 flushed).
 constexpr uint32_t kBlockRow = 32;
-constexpr uint32_t kWarpRow = 4;
+constexpr uint32_t kWarpRow = 2;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
