@@ -8,7 +8,9 @@
     dys, dw = route.combine_backward(dy, ys, weights)
     dx = route.dispatch_backward(dxs)
 
-Argument marshalling only; include/spmv.h (spmv_route_*) has the contract.
+The methods record no autograd graph: a torch.autograd.Function calls them in
+its forward and backward.  Argument marshalling only; include/spmv.h
+(spmv_route_*) has the contract.
 """
 from __future__ import annotations
 
@@ -146,8 +148,9 @@ class ExpertRoute:
         if out is None:
             out = _launch.empty(stream, d, (t * k, hidden), dy.dtype)
         if dweights is None:
-            dweights = _launch.empty(stream, d, (t, k), torch.float32)
-        lddw = _launch.rows("dweights", dweights, (t, k), torch.float32, d)
+            dweights, lddw = _launch.empty(stream, d, (t, k), torch.float32), k
+        else:
+            lddw = _launch.rows("dweights", dweights, (t, k), torch.float32, d)
         _launch.call(self._L.spmv_route_combine_backward, "spmv_route_combine_backward", d, t, k, hidden, e,
                      self._pointers[2], w, ldw, dy.data_ptr(), lddy, ys.data_ptr(), ldys, out.data_ptr(), ldo,
                      dweights.data_ptr(), lddw, _launch.handle(stream, d))

@@ -199,6 +199,56 @@ def test_gradients_against_differences():
     assert dys.shape == ys.shape and dw.shape == w.shape
 
 
+def test_through_autograd():
+    """A layer's training step: dispatch and combine as autograd functions
+    around a product per expert, against the same layer written token by token
+    in 64 bits."""
+    import torch
+    import load_balanced_csr_gb300 as lb
+    t, k, experts, hidden = 50, 2, 4, 24
+
+    class Dispatch(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, route):
+            ctx.route = route
+            return route.dispatch(x)
+
+        @staticmethod
+        def backward(ctx, dxs):
+            return ctx.route.dispatch_backward(dxs.contiguous()), None
+
+    class Combine(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, ys, w, route):
+            ctx.route = route
+            ctx.save_for_backward(ys, w)
+            return route.combine(ys, w)
+
+        @staticmethod
+        def backward(ctx, dy):
+            return *ctx.route.combine_backward(dy.contiguous(), *ctx.saved_tensors), None
+
+    torch.manual_seed(3)
+    ids = torch.randint(-1, experts, (t, k), device="cuda")
+    x, w, m = torch.randn(t, hidden), torch.rand(t, k), torch.randn(experts, hidden, hidden) / hidden ** 0.5
+    got = [v.cuda().requires_grad_() for v in (x, w, m)]
+    route = lb.ExpertRoute(t, k, experts).build(ids)
+    rows = Dispatch.apply(got[0], route)
+    begin = route.expert_ptr.tolist()
+    parts = [rows[begin[e]:begin[e + 1]] @ got[2][e] for e in range(experts)] + [rows[begin[-1]:]]
+    y = Combine.apply(torch.cat(parts), got[1], route)
+    want = [v.double().cuda().requires_grad_() for v in (x, w, m)]
+    kept = (ids >= 0).double()
+    each = torch.einsum("th,tkhf->tkf", want[0], want[2][ids.clamp(min=0)])
+    y64 = (each * (want[1] * kept)[:, :, None]).sum(1)
+    (y.square().sum() / 2).backward()
+    (y64.square().sum() / 2).backward()
+    # sums of at most a few hundred products of values of a few units, in 32 bits
+    for a, b in ((y, y64), *((g.grad, h.grad) for g, h in zip(got, want))):
+        a, b = a.detach().double(), b.detach()
+        assert float((a - b).abs().max()) <= 512 * V * float(b.abs().max())
+
+
 def test_dispatch_keeps_bits_and_another_stream():
     """NaN payloads and signed zeros pass through; a call on its own stream
     uses that stream's memory."""
