@@ -614,6 +614,8 @@ spmv_status_t spmv_pages_append(int32_t requests, const int32_t *past, const int
  *     = k[i * k_stride[0] + h * k_stride[1] + d],   0 <= d < head_dim,
  * and likewise v.  Other slots are skipped.  Strides (HOST arrays) count
  * elements; the last index is contiguous.  Two tokens must not share a slot.
+ * Limits: num_pages * page_size < 2^31, heads * head_dim < 2^30, tokens *
+ * heads * head_dim < 2^41.
  * Errors: INVALID_ARG, CUDA.
  */
 spmv_status_t spmv_paged_store(int32_t tokens, int32_t heads, int32_t head_dim, spmv_elem_t elem,

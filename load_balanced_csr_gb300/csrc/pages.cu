@@ -13,9 +13,11 @@
 // in global memory first.  One block's sums and a second launch took 11.6 and
 // 21.8 us.
 //
-// spmv_paged_store: a copy, a warp per token, 16 bytes a lane; 65,535 tokens
-// of 8 heads of 128 f16, 5 % of them padding (510 MB) 79 us: 6.5 TB/s, 0.97 of
-// the measured copy.
+// spmv_paged_store: a copy, 16 bytes a lane, four in flight for keys and
+// values each; 65,535 tokens of 8 heads of 128 f16, 5 % of them padding (510
+// MB) 75.5 us: 6.75 TB/s, the measured copy's rate.  5 heads of 72 bf16 32.5
+// us (28 at that rate); a warp per token, whose last turn such rows fill in
+// part, took 47.
 #include <algorithm>
 #include <climits>
 
@@ -209,39 +211,65 @@ __global__ void __launch_bounds__(kAppendThreads) pages_append_kernel(AppendArgs
 constexpr int kStoreThreads = 256;
 
 struct StoreArgs {
-    int32_t tokens, heads, vecs, num_pages, page;  // vecs: vectors in a head
+    int64_t items;            // vectors of all tokens
+    int32_t row, vecs;        // vectors of a token, of a head
+    int32_t num_pages, page;
+    uint32_t row_mul, row_shift, vecs_mul, vecs_shift, page_mul, page_shift;
     const int32_t *slots;
     int64_t ks[2], vs[2], kc[3], vc[3];
 };
 
-// A warp per token.
-template <typename T, int N>
+__device__ __forceinline__ uint32_t divided(uint32_t t, uint32_t mul, uint32_t shift) {
+    return (uint32_t)(((unsigned long long)__umulhi(t, mul) + t) >> shift);
+}
+
+// A block takes kStoreThreads * U neighbouring vectors, whichever tokens they
+// are of, so that rows of any length fill its lanes.
+template <typename T, int N, int U>
 __global__ void __launch_bounds__(kStoreThreads)
 paged_store_kernel(StoreArgs a, const T *__restrict__ k, const T *__restrict__ v, T *__restrict__ kc,
                    T *__restrict__ vc) {
     using V = Vec<T, N>;
     after_previous();
-    const int lane = threadIdx.x & 31;
-    const int64_t i = (int64_t)blockIdx.x * (kStoreThreads / 32) + (threadIdx.x >> 5);
-    if (i >= a.tokens) return;
-    const int32_t slot = __ldg(a.slots + i);
-    if (slot < 0 || slot / a.page >= a.num_pages) return;
-    const int64_t page = slot / a.page, in = slot % a.page;
-    const int total = a.heads * a.vecs;
-    for (int e = lane; e < total; e += 32) {
-        const int64_t h = e / a.vecs, d = (int64_t)(e % a.vecs) * N;
-        const V kv = *reinterpret_cast<const V *>(k + i * a.ks[0] + h * a.ks[1] + d);
-        const V vv = *reinterpret_cast<const V *>(v + i * a.vs[0] + h * a.vs[1] + d);
-        *reinterpret_cast<V *>(kc + page * a.kc[0] + in * a.kc[1] + h * a.kc[2] + d) = kv;
-        *reinterpret_cast<V *>(vc + page * a.vc[0] + in * a.vc[1] + h * a.vc[2] + d) = vv;
+    const int64_t first = (int64_t)blockIdx.x * (kStoreThreads * U), token0 = first / a.row;
+    const uint32_t over = (uint32_t)(first - token0 * a.row) + threadIdx.x;
+    int64_t token[U];
+    uint32_t head[U], at[U];
+    int32_t slot[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        // past the last vector: the first again, not stored
+        const bool in = first + threadIdx.x + u * kStoreThreads < a.items;
+        const uint32_t e = in ? over + u * kStoreThreads : 0, t = divided(e, a.row_mul, a.row_shift), in_row = e - t * a.row;
+        token[u] = token0 + t;
+        head[u] = divided(in_row, a.vecs_mul, a.vecs_shift);
+        at[u] = (in_row - head[u] * a.vecs) * N;
+        slot[u] = in ? __ldg(a.slots + token[u]) : -1;
+    }
+    // read whatever the slot says, so that no load waits for it
+    V kv[U], vv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        kv[u] = *reinterpret_cast<const V *>(k + token[u] * a.ks[0] + head[u] * a.ks[1] + at[u]);
+        vv[u] = *reinterpret_cast<const V *>(v + token[u] * a.vs[0] + head[u] * a.vs[1] + at[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t page = divided((uint32_t)slot[u], a.page_mul, a.page_shift);
+        if (slot[u] < 0 || page >= (uint32_t)a.num_pages) continue;
+        const int64_t in = (uint32_t)slot[u] - page * a.page;
+        *reinterpret_cast<V *>(kc + page * a.kc[0] + in * a.kc[1] + head[u] * a.kc[2] + at[u]) = kv[u];
+        *reinterpret_cast<V *>(vc + page * a.vc[0] + in * a.vc[1] + head[u] * a.vc[2] + at[u]) = vv[u];
     }
 }
 
 template <typename T, int N>
 cudaError_t launch_store(const StoreArgs &a, const void *k, const void *v, void *kc, void *vc, cudaStream_t stream) {
-    const unsigned blocks = (unsigned)((a.tokens + (int64_t)kStoreThreads / 32 - 1) / (kStoreThreads / 32));
-    return launch_chained(paged_store_kernel<T, N>, blocks, kStoreThreads, 0, 0, stream, a, static_cast<const T *>(k),
-                          static_cast<const T *>(v), static_cast<T *>(kc), static_cast<T *>(vc));
+    constexpr int U = N == 1 ? 8 : 4;
+    const int64_t per_block = kStoreThreads * U;
+    return launch_chained(paged_store_kernel<T, N, U>, (unsigned)((a.items + per_block - 1) / per_block), kStoreThreads, 0, 0,
+                          stream, a, static_cast<const T *>(k), static_cast<const T *>(v), static_cast<T *>(kc),
+                          static_cast<T *>(vc));
 }
 
 bool on_16(const void *p, const int64_t *strides, int n, int size) {
@@ -323,7 +351,8 @@ spmv_status_t spmv_paged_store(int32_t tokens, int32_t heads, int32_t head_dim, 
     if (tokens < 0 || heads < 0 || head_dim < 0 || num_pages < 0) return llm_bad("negative size");
     if (page_size < 1) return llm_bad("page_size must be at least 1");
     if ((int64_t)num_pages * page_size >= (1LL << 31)) return llm_bad("num_pages * page_size must be < 2^31");
-    if ((int64_t)heads * head_dim >= (1LL << 31)) return llm_bad("heads * head_dim must be < 2^31");
+    if ((int64_t)heads * head_dim >= (1LL << 30)) return llm_bad("heads * head_dim must be < 2^30");
+    if ((int64_t)tokens * heads * head_dim >= (1LL << 41)) return llm_bad("tokens * heads * head_dim must be < 2^41");
     if (!elem_ok(elem)) return llm_bad("unknown element type");
     if (!k_stride || !v_stride || !k_cache_stride || !v_cache_stride) return llm_bad("a stride array is NULL");
     if (tokens == 0 || heads == 0 || head_dim == 0 || num_pages == 0) return SPMV_OK;
@@ -334,8 +363,13 @@ spmv_status_t spmv_paged_store(int32_t tokens, int32_t heads, int32_t head_dim, 
     const bool wide = head_dim * size % 16 == 0 && on_16(k, k_stride, 2, size) && on_16(v, v_stride, 2, size) &&
                       on_16(k_cache, k_cache_stride, 3, size) && on_16(v_cache, v_cache_stride, 3, size);
     StoreArgs a;
-    a.tokens = tokens, a.heads = heads, a.num_pages = num_pages, a.page = page_size, a.slots = slots;
+    a.num_pages = num_pages, a.page = page_size, a.slots = slots;
     a.vecs = wide ? head_dim * size / 16 : head_dim;
+    a.row = heads * a.vecs;
+    a.items = (int64_t)tokens * a.row;
+    set_divisor((uint32_t)a.row, &a.row_mul, &a.row_shift);
+    set_divisor((uint32_t)a.vecs, &a.vecs_mul, &a.vecs_shift);
+    set_divisor((uint32_t)page_size, &a.page_mul, &a.page_shift);
     for (int i = 0; i < 2; ++i) a.ks[i] = k_stride[i], a.vs[i] = v_stride[i];
     for (int i = 0; i < 3; ++i) a.kc[i] = k_cache_stride[i], a.vc[i] = v_cache_stride[i];
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);

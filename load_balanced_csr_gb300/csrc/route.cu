@@ -312,7 +312,7 @@ route_combine_kernel(RowArgs a, const T *__restrict__ ys, int64_t ldys, T *__res
 #pragma unroll
         for (int n = 0; n < N; ++n) sum[u][n] = 0.0f;
     if constexpr (U == 1) {
-        // few rows: what counts is that the choices' rows are on their way together
+        // few or short rows: what counts is that the choices' rows are on their way together
         constexpr int BATCH = 4;
         for (int j0 = 0; j0 < a.k; j0 += BATCH) {
             int32_t p[BATCH];
@@ -442,6 +442,8 @@ unsigned row_blocks(const RowArgs &a) { return (unsigned)((a.items + kRowThreads
 // the rows spread over the SMs: 64 tokens of 2,048 bf16 and 8 choices take
 // 3.3 us by dispatch and 4.6 by combine, 5.1 and 7.6 with the large span; many
 // rows with the small span 130 us instead of 63 (16,384 tokens, combine).
+// Rows of one vector a lane have the small span anyway: 16,384 tokens, 8
+// choices, 256 bf16 are combined in 10.7 us, 20.0 with the large one.
 bool few_rows(int32_t tokens, int32_t hidden, int n) { return (int64_t)tokens * (hidden / n) < 152 * 64 * 32; }
 
 template <typename T, int N, int U>
@@ -468,7 +470,7 @@ cudaError_t launch_combine_u(int32_t tokens, int32_t k, int32_t hidden, const in
 template <typename T, int N>
 cudaError_t launch_combine(int32_t tokens, int32_t k, int32_t hidden, const int32_t *slot, const float *w, int64_t ldw,
                            const void *ys, int64_t ldys, void *y, int64_t ldy, cudaStream_t stream) {
-    return few_rows(tokens, hidden, N) ? launch_combine_u<T, N, 1>(tokens, k, hidden, slot, w, ldw, ys, ldys, y, ldy, stream)
+    return few_rows(tokens, hidden, N) || hidden / N <= 32 ? launch_combine_u<T, N, 1>(tokens, k, hidden, slot, w, ldw, ys, ldys, y, ldy, stream)
                                        : launch_combine_u<T, N, 4>(tokens, k, hidden, slot, w, ldw, ys, ldys, y, ldy, stream);
 }
 
