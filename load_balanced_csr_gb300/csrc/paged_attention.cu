@@ -71,9 +71,9 @@ spmv_status_t spmv_paged_attention(const spmv_paged_attention_t *args, spmv_stre
     if (a.num_pages < 0 || a.max_pages < 0) return llm_bad("negative size");
     if (a.page_size < 1) return llm_bad("page_size must be at least 1");
     if ((int64_t)a.num_pages * a.page_size >= (1LL << 31)) return llm_bad("num_pages * page_size must be < 2^31");
-    // one request's chunks of at least 8 positions, over its rows, are counted in 32 bits
+    // one request's units (chunks of at least 8 positions, and its rows' own) are counted in 32 bits
     if ((int64_t)a.max_pages * a.page_size >= (1LL << 31) - 64 ||
-        ((int64_t)a.max_pages * a.page_size / 8 + 3) * std::max(a.q_heads, a.kv_heads) >= (1LL << 31))
+        ((int64_t)a.max_pages * a.page_size / 8 + 1 + kRowCost) * std::max(a.q_heads, a.kv_heads) >= (1LL << 31))
         return llm_bad("max_pages * page_size * q_heads is too large");
     if (a.batch == 0 || a.q_heads == 0) return SPMV_OK;
     if (!a.q || !a.out || !a.lens || !a.status) return llm_bad("q, out, lens or status is NULL");
