@@ -4,8 +4,10 @@
 //
 // in one pass over the positions with the running maximum m and sum of the
 // softmax: when a score above m comes, the sums so far are scaled by
-// exp(m_old - m_new).  Scores are kept in units of ln 2, so the exponentials
-// are powers of two.
+// exp(m_old - m_new).  The maximum is the dot products' own, before their
+// scale: a weight is 2^((x - m) scale / ln 2), whose difference is taken before
+// anything is rounded, so that the highest score's weight is 1 however large
+// the scores are.
 //
 // The work is a sparse product's with very uneven rows: row (request, kv
 // head), one unit per chunk of positions and kRowCost for the row itself.
@@ -136,9 +138,13 @@ __device__ __forceinline__ float pow2(float x) {
 template <int CH>
 constexpr uint32_t FULL_MASK = 0xffffffffu >> (32 - CH);
 
-// what scores are taken relative to; the running maximum m is -infinity
-// until a score has come, and nothing has weight then
+// what products are taken relative to; the running maximum m is -infinity
+// until one has come, and nothing has weight then
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
+// what sums relative to m are worth relative to `base`, a maximum not below m
+__device__ __forceinline__ float worth(float m, float base, float scale2) {
+    return m == -INFINITY ? 0.0f : pow2((m - base) * scale2);
+}
 
 // ------------------------------------------------------------ 16-bit elements
 // A chunk is 16 positions, or 32 of small heads, so that a chunk's fixed work
@@ -247,13 +253,13 @@ struct TileMma {
                 }
             raw = fmaxf(raw, __shfl_xor_sync(0xffffffffu, raw, 1));
             raw = fmaxf(raw, __shfl_xor_sync(0xffffffffu, raw, 2));
-            top[h] = fmaxf(m[h], raw * p.scale2);
+            top[h] = fmaxf(m[h], raw);
             higher |= top[h] > m[h];
         }
         if (__any_sync(0xffffffffu, higher)) {
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                const float keep = pow2(m[h] - base_of(top[h]));
+                const float keep = worth(m[h], top[h], p.scale2);
                 l[h] *= keep;
                 m[h] = top[h];
 #pragma unroll
@@ -272,7 +278,7 @@ struct TileMma {
                 T high[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    w[c] = pow2(fmaf(s[n][h][c], p.scale2, -base));
+                    w[c] = pow2((s[n][h][c] - base) * p.scale2);
                     if (!whole && !((mask >> (n * 8 + (lane & 3) * 2 + c)) & 1)) w[c] = 0.0f;
                     high[c] = from_float<T>(w[c]);
                 }
@@ -411,13 +417,13 @@ struct TileF32 {
         bool higher = false;  // the same on every lane
 #pragma unroll
         for (int g = 0; g < GT; ++g) {
-            top[g] = fmaxf(m[g], top[g] * p.scale2);
+            top[g] = fmaxf(m[g], top[g]);
             higher |= top[g] > m[g];
         }
         if (higher) {
 #pragma unroll
             for (int g = 0; g < GT; ++g) {
-                const float keep = pow2(m[g] - base_of(top[g]));
+                const float keep = worth(m[g], top[g], p.scale2);
                 l[g] *= keep;
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) o[g][i].x *= keep, o[g][i].y *= keep;
@@ -430,7 +436,7 @@ struct TileF32 {
             float own = 0.0f;
 #pragma unroll
             for (int g = j; g < GT && g < j + 4; ++g) {
-                const float w = live ? pow2(fmaf(s[g], p.scale2, -base_of(m[g]))) : 0.0f;
+                const float w = live ? pow2((s[g] - base_of(m[g])) * p.scale2) : 0.0f;
                 if (quarter == 0) l[g] += w;
                 if (quarter == g - j) own = w;
             }
@@ -560,7 +566,7 @@ __device__ __forceinline__ void write_out(const AttendArgs &p, int b, int head, 
 // no weight at all: zeros (a NaN stays)
 __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 __device__ __forceinline__ void write_lse(const AttendArgs &p, int b, int head, float m, float l) {
-    if (p.a.lse) p.a.lse[(int64_t)b * p.a.q_heads + head] = (m + log2f(l)) * kLn2;
+    if (p.a.lse) p.a.lse[(int64_t)b * p.a.q_heads + head] = l == 0.0f ? -INFINITY : fmaf(m, p.scale2, log2f(l)) * kLn2;
 }
 
 // Prefix sums of the requests' chunks into shared memory, with their lengths.
@@ -613,7 +619,7 @@ struct Part {
 };
 
 // One warp joins `count` parts of a row for head g of its tile: part i has
-// weight 2^(m_i - max m), and its record is at from + i * step + FLOATS, the
+// weight 2^((m_i - max m) scale2), and its record is at from + i * step + FLOATS, the
 // last one's, if the row ends there, at from + i * step.  Writes the head's
 // output, or the parts' sum to `to`.  GLOBAL: other blocks wrote the records,
 // so they are read past L1.
@@ -632,7 +638,6 @@ __device__ __forceinline__ void join(const AttendArgs &p, const float *from, int
     for (int i = lane; i < count; i += 32) m = fmaxf(m, one(record(i) + P::GT * R::ROW + g));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float base = base_of(m);
     constexpr int QUADS = P::DP / 4, PER = (QUADS + 31) / 32;  // quads of elements, of a lane
     float4 sum[PER];
 #pragma unroll
@@ -641,7 +646,7 @@ __device__ __forceinline__ void join(const AttendArgs &p, const float *from, int
         float w = 0.0f;
         if (i0 + lane < count) {
             const float *rec = record(i0 + lane) + P::GT * R::ROW + g;
-            w = pow2(one(rec) - base);
+            w = worth(one(rec), m, p.scale2);
             l = fmaf(w, one(rec + P::GT), l);
         }
         const int n = min(32, count - i0);

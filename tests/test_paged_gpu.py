@@ -347,6 +347,37 @@ def test_attention_caches_of_two_layouts(dim, page, dtype):
     r.check(out, lse, 0.0)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("lens", [[33, 900], [40000]], ids=["short", "cut"])
+@pytest.mark.parametrize("q_heads", [4, 32])
+def test_attention_scores_past_24_bits(q_heads, lens, dtype):
+    """Scores so large that rounding them moves them by many units: the
+    highest one still has weight 1.  All products but one are zero and the
+    highest score is far above the others, so the output is that position's
+    value (the weight's own error, the sum and the division: 8 V), and the
+    log-sum the score (its scale and units: 8 V)."""
+    import torch
+    r = Requests(lens, q_heads, 2, 64, 16, dtype, seed=5)
+    big = {"f32": 1e15, "bf16": 1e15, "f16": 2.0 ** 15}[dtype]
+    r.q.zero_()
+    r.q[:, :, 0] = big * (1 + torch.rand(len(lens), q_heads, device="cuda") / 2).to(r.q.dtype)
+    top = []
+    for b, n in enumerate(lens):
+        pos = torch.arange(n, device="cuda")
+        at = r.table[b].long()[pos // 16]
+        r.k[at, pos % 16, :, 0] = big / 2
+        top.append((int(r.table[b, (n // 3) // 16]), n // 3 % 16))
+        r.k[top[b]][:, 0] = big
+    attend = r.attention()
+    out, lse = attend(r.q, r.k, r.v, r.table, r.lens, scale=0.3)
+    assert attend.device_status() == 0
+    for b in range(len(lens)):
+        v = r.v[top[b]].double().repeat_interleave(q_heads // 2, 0)
+        assert bool(((out[b].double() - v).abs() <= (U[dtype] + 8 * V) * v.abs() + TINY[dtype]).all())
+        score = 0.3 * r.q[b, :, 0].double() * r.k[top[b]][:, 0].double().repeat_interleave(q_heads // 2)
+        assert bool(((lse[b].double() - score).abs() <= 8 * V * score).all())
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_attention_extreme_scores(dtype):
     """Scores hundreds apart: the running maximum moves late, early and never;
