@@ -38,6 +38,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "internal.cuh"
 #include "llm.cuh"
@@ -156,6 +157,9 @@ __device__ __forceinline__ float worth(float m, float base, float scale2) {
 // 22 (f16) bits: with hi alone the output's error against 64 bits is 1.4
 // times that of one rounding.  A tile of 8 heads has hi in the product's
 // first 8 rows and lo in its last 8, and so costs no more than hi alone.
+// f16 weights are taken 2^15 times as large, as are the sums: its smallest
+// step is then 2^-39 of a row's largest weight (2^-24 otherwise, below half of
+// which a weight is lost: many positions behind one high score).
 template <typename T_, int GT_, int DP_, int CH_, int NW_, int STAGES_>
 struct TileMma {
     using T = T_;
@@ -164,6 +168,7 @@ struct TileMma {
     static constexpr int NT = CH / 8;      // the scores' product in columns of 8 positions
     static constexpr int PITCH = DP * 2 + 16;  // bytes: rows 16 bytes apart modulo 128, so ldmatrix has no conflicts
     static constexpr int QBYTES = 0;
+    static constexpr float LIFT = std::is_same<T, __half>::value ? 15.0f : 0.0f;  // log2 of a weight of 1
     static constexpr int H = GT / 8;  // heads of a lane: lane / 4 and, with 16, lane / 4 + 8
 
     static constexpr bool AHEAD = GT * DP <= 1024;  // registers for the next row's queries too
@@ -278,7 +283,7 @@ struct TileMma {
                 T high[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    w[c] = pow2((s[n][h][c] - base) * p.scale2);
+                    w[c] = pow2(fmaf(s[n][h][c] - base, p.scale2, LIFT));
                     if (!whole && !((mask >> (n * 8 + (lane & 3) * 2 + c)) & 1)) w[c] = 0.0f;
                     high[c] = from_float<T>(w[c]);
                 }
@@ -349,6 +354,7 @@ struct TileF32 {
     using T = float;
     static constexpr int DP = DP_, NW = NW_, STAGES = STAGES_, GT = GT_, CH = 8, PAGE_UNIT = 8;
     static constexpr int PITCH = DP * 4 + 16;
+    static constexpr float LIFT = 0.0f;
     static constexpr int WEIGHTS = GT * DP * 4;                // offset of the weights of a chunk behind the queries
     static constexpr int QBYTES = WEIGHTS + GT * CH * 4;
     static constexpr bool AHEAD = true;
@@ -565,8 +571,9 @@ __device__ __forceinline__ void write_out(const AttendArgs &p, int b, int head, 
 }
 // no weight at all: zeros (a NaN stays)
 __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+template <class P>
 __device__ __forceinline__ void write_lse(const AttendArgs &p, int b, int head, float m, float l) {
-    if (p.a.lse) p.a.lse[(int64_t)b * p.a.q_heads + head] = l == 0.0f ? -INFINITY : fmaf(m, p.scale2, log2f(l)) * kLn2;
+    if (p.a.lse) p.a.lse[(int64_t)b * p.a.q_heads + head] = l == 0.0f ? -INFINITY : fmaf(m, p.scale2, log2f(l) - P::LIFT) * kLn2;
 }
 
 // Prefix sums of the requests' chunks into shared memory, with their lengths.
@@ -681,7 +688,7 @@ __device__ __forceinline__ void join(const AttendArgs &p, const float *from, int
     }
     if (lane == 0) {
         if (to) to[P::GT * R::ROW + g] = m, to[P::GT * R::ROW + P::GT + g] = l;
-        else write_lse(p, part.b, head, m, l);
+        else write_lse<P>(p, part.b, head, m, l);
     }
 }
 
@@ -907,7 +914,7 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
                 if (g < heads) write_out<P>(p, note.x, h0 + g, d, x, y, inverse(l));
             });
             tile.each_head(lane, [&](int g, float m, float l) {
-                if (g < heads) write_lse(p, note.x, h0 + g, m, l);
+                if (g < heads) write_lse<P>(p, note.x, h0 + g, m, l);
             });
         }
     }

@@ -378,6 +378,30 @@ def test_attention_scores_past_24_bits(q_heads, lens, dtype):
         assert bool(((lse[b].double() - score).abs() <= 8 * V * score).all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("q_heads,dim", [(4, 64), (32, 128)])
+@pytest.mark.parametrize("above", [17.0, 19.0])
+def test_attention_one_score_far_above(above, q_heads, dim, dtype):
+    """One position with most of the weight and a value of zero: the output is
+    what the others, of weights around 2^-24 and 2^-27, add up to."""
+    import torch
+    lens = [3000, 700, 20000]
+    r = Requests(lens, q_heads, 2, dim, 16, dtype, seed=6)
+    r.q[:, :, 0] = 16.0
+    scale = dim ** -0.5
+    for b, n in enumerate(lens):
+        pos = torch.arange(n, device="cuda")
+        at = r.table[b].long()[pos // 16]
+        r.k[at, pos % 16] = (r.k[at, pos % 16].float() / 4).to(r.k.dtype)
+        r.k[at, pos % 16, :, 0] = 0.0
+        r.v[at, pos % 16] = (r.v[at, pos % 16].float() + 3).to(r.v.dtype)
+        first = int(r.table[b, 0])
+        r.k[first, 0, :, 0] = above / (16 * scale)
+        r.v[first, 0] = 0.0
+    out, lse = r.attention()(r.q, r.k, r.v, r.table, r.lens)
+    r.check(out, lse, scale)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_attention_extreme_scores(dtype):
     """Scores hundreds apart: the running maximum moves late, early and never;
