@@ -33,6 +33,18 @@ def empty(stream, device, shape, dtype):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def settle(device) -> None:
+    """Waits for the device's current stream: the last step of a constructor.
+    What it set is then set for every stream, and no earlier user of the
+    memory it took is still at work.  (While the stream is captured nothing
+    has run and the object belongs to the graph.)"""
+    stream = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        capturing = torch.cuda.is_current_stream_capturing()
+    if not capturing:
+        stream.synchronize()
+
+
 _current_device = torch._C._cuda_getDevice
 
 

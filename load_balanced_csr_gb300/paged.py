@@ -28,7 +28,7 @@ class PageTable:
     is extended in place.  ``append`` fills, for the requests of one step,
     ``token_ptr`` (requests + 1), ``lens`` (requests), ``slots`` and
     ``positions`` (max_tokens) and ``taken`` (1), and adds its flags to
-    ``status`` (1)."""
+    ``status`` (1).  Keep the object until its calls have run."""
 
     def __init__(self, table, page_size: int, num_pages: int, max_tokens: int):
         if table.dtype != torch.int32 or not table.is_cuda or table.dim() != 2:
@@ -51,6 +51,7 @@ class PageTable:
                          self._workspace.data_ptr(), size.value)
         self.token_ptr = self.lens = None
         self._requests = None
+        _launch.settle(self.device)
 
     def append(self, past, fresh, free_pages, stream=None) -> "PageTable":
         """Add ``fresh[r]`` tokens to request r, which holds ``past[r]``
@@ -139,7 +140,8 @@ class PagedAttentionArgs(ctypes.Structure):
 class PagedAttention:
     """Attention of one new token for each of up to ``max_batch`` requests.
     Keeps the workspace that joins requests cut between blocks: calls that may
-    overlap on the GPU (two streams) need objects of their own."""
+    overlap on the GPU (two streams) need objects of their own, and an object
+    is kept until its calls have run."""
 
     def __init__(self, max_batch: int, q_heads: int, kv_heads: int, head_dim: int, dtype, device="cuda"):
         self._L, self.device, self.dtype = lib(), _launch.cuda_device(device), dtype
@@ -161,6 +163,7 @@ class PagedAttention:
         self._dense, self._scale, self._args_ref = False, self.head_dim ** -0.5, ctypes.byref(a)
         a.workspace, a.workspace_bytes, a.status = (self._workspace.data_ptr(), size.value,
                                                     self._status.data_ptr())
+        _launch.settle(self.device)
 
     def __call__(self, q, k_cache, v_cache, table, lens, scale=None, out=None, lse=None, stream=None):
         """(out, lse) of q (batch, q_heads, head_dim) over the first

@@ -29,7 +29,7 @@ class ExpertRoute:
     (tokens * top_k) and ``slot`` (tokens, top_k), int32; the other methods
     read ``slot``.  A route is rebuilt for each batch; it must not be rebuilt
     on one stream while another still uses it, and a training step keeps one
-    per layer until its backward pass."""
+    per layer until its backward pass.  Keep it until its calls have run."""
 
     def __init__(self, max_tokens: int, top_k: int, experts: int, device="cuda"):
         from . import check, lib
@@ -50,6 +50,7 @@ class ExpertRoute:
         self.entry = self.slot = None
         # the layouts of each method's tensors that were checked last, and what the checks gave
         self._seen = {}
+        _launch.settle(self.device)
 
     def build(self, expert_ids, stream=None) -> "ExpertRoute":
         """Sort the entries of ``expert_ids`` (tokens, top_k) by expert; ids

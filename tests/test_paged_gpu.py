@@ -328,6 +328,35 @@ def test_attention_views_and_streams(dtype):
     assert (wide[:, 0] == 7).all() and (wide[:, 7] == 7).all() and (wide[:, :, :3] == 7).all() and (wide[:, :, 67:] == 7).all()
 
 
+def test_objects_made_on_a_busy_stream():
+    """Made while the current stream is still at work, used on another at once."""
+    import torch
+    import load_balanced_csr_gb300 as lb
+    r = Requests([60000, 3], 4, 2, 64, 16, "bf16", seed=4)
+    attend = r.attention()
+    attend(r.q, r.k, r.v, r.table, r.lens)  # a kernel's first call may wait for the device
+    attend._workspace.fill_(0x7f)  # what the memory that the next object takes may hold
+    attend._status.fill_(64)
+    del attend
+    past, fresh = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([3, 20], [1, 30]))
+    free = torch.arange(4, 40, dtype=torch.int32, device="cuda")
+    table = torch.tensor([[0, -1, -1, -1], [1, 2, -1, -1]], dtype=torch.int32, device="cuda")
+    lb.PageTable(table.clone(), 16, 64, 40).append(past, fresh, free)
+    s = torch.cuda.Stream()
+    out, lse = torch.empty_like(r.q), torch.empty(2, 4, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # about 50 ms
+    attend = r.attention()
+    attend(r.q, r.k, r.v, r.table, r.lens, out=out, lse=lse, stream=s)
+    torch.cuda._sleep(100_000_000)
+    pages = lb.PageTable(table, 16, 64, 40)
+    pages.append(past, fresh, free, stream=s)
+    s.synchronize()
+    flags, taken = attend.device_status(), int(pages.taken)
+    r.check(out, lse, 64 ** -0.5)
+    assert flags == 0 and taken == 2 and int(pages.status) == 0 and pages.lens.tolist() == [4, 50]
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("dim,page", [(64, 16), (64, 7), (128, 64), (128, 5), (96, 16)])
 def test_attention_caches_of_two_layouts(dim, page, dtype):
