@@ -645,7 +645,8 @@ spmv_status_t spmv_paged_store(int32_t tokens, int32_t heads, int32_t head_dim, 
  */
 typedef struct {
     int32_t batch, q_heads, kv_heads, head_dim; /* q_heads a multiple of kv_heads; head_dim a
-                                                   multiple of 8, at most 256 */
+                                                   multiple of 8, at most 256; q_heads * head_dim
+                                                   < 2^30 */
     int32_t page_size, num_pages, max_pages;    /* max_pages: entries in a table row */
     int32_t elem;                               /* spmv_elem_t of q, the caches and out */
     float scale;

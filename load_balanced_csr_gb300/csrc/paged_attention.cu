@@ -30,6 +30,7 @@ const char *heads_bad(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t 
     if (head_dim < 8 || head_dim > kMaxDim || head_dim % 8) return "head_dim must be a multiple of 8 in [8, 256]";
     if (kv_heads < 1 || q_heads % kv_heads) return "q_heads must be a multiple of kv_heads";
     if ((int64_t)batch * q_heads >= (1LL << 31)) return "batch * q_heads must be < 2^31";
+    if ((int64_t)q_heads * head_dim >= (1LL << 30)) return "q_heads * head_dim must be < 2^30";
     return nullptr;
 }
 

@@ -119,6 +119,14 @@ def test_attention_refusals():
     assert L.spmv_paged_attention(args(batch=0), None) == 0
 
 
+def test_attention_refuses_rows_past_32_bits():
+    """A request's elements are counted in 32 bits."""
+    L = lb.lib()
+    size = ctypes.c_size_t(77)
+    assert L.spmv_paged_attention_workspace(1, 2 ** 23, 1, 256, 1, ctypes.byref(size)) == BAD and size.value == 0
+    assert L.spmv_paged_attention(args(q_heads=2 ** 23, kv_heads=1, head_dim=256, max_pages=1), None) == BAD
+
+
 def test_attention_arguments_match_the_header(tmp_path):
     from load_balanced_csr_gb300.paged import PagedAttentionArgs
     cc = shutil.which("gcc") or shutil.which("cc")
