@@ -30,7 +30,12 @@ inline bool aligned_to(const void *p, int64_t bytes) { return reinterpret_cast<u
 // The operators are chained: each kernel is launched while the one before it
 // in the stream still runs, and waits for it (all of it, its writes visible)
 // before it touches global memory; so a launch costs the stream about 2 us
-// less.  after_previous() is every such kernel's first statement.
+// less.  after_previous() is every such kernel's first statement.  What the
+// kernel before wrote is visible after it to ordinary loads only: a load
+// through the read-only path is defined for data that nobody writes while the
+// kernel lives, which begins before the wait, and may be moved above it.  So
+// these kernels take no pointer as __restrict__ and use no __ldg; loads that
+// are to be in flight together are written before the stores.
 __device__ __forceinline__ void after_previous() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");

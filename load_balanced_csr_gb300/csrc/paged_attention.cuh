@@ -589,7 +589,7 @@ __device__ __forceinline__ Rows load_rows(const AttendArgs &p, char *smem) {
         const int b = b0 + threadIdx.x;
         uint32_t n = 0;
         if (b < p.a.batch) {
-            const int given = __ldg(p.a.lens + b);
+            const int given = p.a.lens[b];
             const int len = given < 0 ? 0 : (int)min((long long)given, (long long)p.a.max_pages * p.a.page_size);
             if (blockIdx.x == 0 && len != given) atomicOr(p.a.status, kBadLength);
             n = len ? ((uint32_t)((len + P::CH - 1) / P::CH) + kRowCost) * p.rows : 0;
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
     // this lane's entry of the batch of request b that begins at unit u
     auto read_pages = [&](int b, int len, int u) {
         const int64_t pos = (int64_t)(u + lane) * (one_page ? P::PAGE_UNIT : 1);
-        return pos < len ? __ldg(p.a.table + b * p.a.table_stride + page_at((int)pos)) : -1;
+        return pos < len ? p.a.table[b * p.a.table_stride + page_at((int)pos)] : -1;
     };
     auto read_next_request = [&] {
         int b = load.b + 1;

@@ -227,8 +227,7 @@ __device__ __forceinline__ uint32_t divided(uint32_t t, uint32_t mul, uint32_t s
 // are of, so that rows of any length fill its lanes.
 template <typename T, int N, int U>
 __global__ void __launch_bounds__(kStoreThreads)
-paged_store_kernel(StoreArgs a, const T *__restrict__ k, const T *__restrict__ v, T *__restrict__ kc,
-                   T *__restrict__ vc) {
+paged_store_kernel(StoreArgs a, const T *k, const T *v, T *kc, T *vc) {
     using V = Vec<T, N>;
     after_previous();
     const int64_t first = (int64_t)blockIdx.x * (kStoreThreads * U), token0 = first / a.row;
@@ -244,7 +243,7 @@ paged_store_kernel(StoreArgs a, const T *__restrict__ k, const T *__restrict__ v
         token[u] = token0 + t;
         head[u] = divided(in_row, a.vecs_mul, a.vecs_shift);
         at[u] = (in_row - head[u] * a.vecs) * N;
-        slot[u] = in ? __ldg(a.slots + token[u]) : -1;
+        slot[u] = in ? a.slots[token[u]] : -1;
     }
     // read whatever the slot says, so that no load waits for it
     V kv[U], vv[U];

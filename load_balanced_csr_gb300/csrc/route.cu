@@ -51,7 +51,7 @@ int64_t build_tile(int64_t n) {
 int build_tiles(int64_t n) { return (int)std::max<int64_t>(1, (n + build_tile(n) - 1) / build_tile(n)); }
 
 template <typename I>
-__device__ __forceinline__ int key_of(const I *__restrict__ ids, int64_t ld, int k, int experts, int64_t i) {
+__device__ __forceinline__ int key_of(const I *ids, int64_t ld, int k, int experts, int64_t i) {
     const I id = ld == k ? ids[i] : ids[(i / k) * ld + i % k];
     return id >= 0 && id < (I)experts ? (int)id : experts;  // the last bin: dropped
 }
@@ -76,16 +76,23 @@ __device__ __forceinline__ unsigned same_key(int key, int bits) {
 // hist[tile * (experts + 1) + bin]: entries of the tile in each bin
 template <typename I>
 __global__ void __launch_bounds__(kBuildThreads)
-route_hist_kernel(const I *__restrict__ ids, int64_t ld, int k, int64_t n, int experts, int64_t tile,
-                  int32_t *__restrict__ hist) {
+route_hist_kernel(const I *ids, int64_t ld, int k, int64_t n, int experts, int64_t tile, int32_t *hist) {
     extern __shared__ int32_t h[];
     after_previous();
     const int bins = experts + 1;
     for (int b = threadIdx.x; b < bins; b += kBuildThreads) h[b] = 0;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * tile, t1 = min(t0 + tile, n);
-#pragma unroll 4
-    for (int64_t i = t0 + threadIdx.x; i < t1; i += kBuildThreads) atomicAdd(&h[key_of(ids, ld, k, experts, i)], 1);
+    constexpr int BATCH = 4;  // ids read together
+    for (int64_t i0 = t0 + threadIdx.x; i0 < t1; i0 += BATCH * kBuildThreads) {
+        int key[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j)
+            if (i0 + j * kBuildThreads < t1) key[j] = key_of(ids, ld, k, experts, i0 + j * kBuildThreads);
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j)
+            if (i0 + j * kBuildThreads < t1) atomicAdd(&h[key[j]], 1);
+    }
     __syncthreads();
     for (int b = threadIdx.x; b < bins; b += kBuildThreads) hist[(int64_t)blockIdx.x * bins + b] = h[b];
 }
@@ -97,9 +104,8 @@ route_hist_kernel(const I *__restrict__ ids, int64_t ld, int k, int64_t n, int e
 // the earlier blocks' entries.  hist is null in a cluster.
 template <typename I>
 __global__ void __launch_bounds__(kBuildThreads)
-route_rank_kernel(const I *__restrict__ ids, int64_t ld, int k, int64_t n, int experts, int64_t tile, int tiles,
-                  const int32_t *__restrict__ hist, int32_t *__restrict__ expert_ptr, int32_t *__restrict__ entry,
-                  int32_t *__restrict__ slot) {
+route_rank_kernel(const I *ids, int64_t ld, int k, int64_t n, int experts, int64_t tile, int tiles, const int32_t *hist,
+                  int32_t *expert_ptr, int32_t *entry, int32_t *slot) {
     extern __shared__ int32_t smem[];
     after_previous();
     __shared__ int32_t warp_sum[kBuildWarps];
@@ -148,12 +154,22 @@ route_rank_kernel(const I *__restrict__ ids, int64_t ld, int k, int64_t n, int e
             // base: the earlier blocks' entries of each bin; sum: all blocks'
             __syncthreads();
             if (hist) {
-                for (int t = warp; t < tiles; t += kBuildWarps)
-                    for (int b = lane; b < bins; b += 32) {
-                        const int32_t c = __ldg(hist + (int64_t)t * bins + b);
-                        atomicAdd(sum + b, c);
-                        if (t < blockIdx.x) atomicAdd(base + b, c);
+                constexpr int PER = (kMaxTiles + kBuildWarps - 1) / kBuildWarps;  // tiles of a warp
+                for (int b = lane; b < bins; b += 32) {
+                    int32_t c[PER], all = 0, before = 0;
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        const int t = warp + j * kBuildWarps;
+                        c[j] = t < tiles ? hist[(int64_t)t * bins + b] : 0;
                     }
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        all += c[j];
+                        if (warp + j * kBuildWarps < (int)blockIdx.x) before += c[j];
+                    }
+                    atomicAdd(sum + b, all);
+                    atomicAdd(base + b, before);
+                }
                 __syncthreads();
             } else {
                 cg::cluster_group cluster = cg::this_cluster();
@@ -256,10 +272,10 @@ constexpr int kRowThreads = 256;
 // its top_k rows of the experts' side are written (read), each 16 bytes a
 // lane; no sharing between warps, so nothing waits but for memory.  With
 // 8,192 tokens, 8 choices and rows of 4,096 bf16 (604 MB) dispatch takes
-// 93.6 us and combine 91.7: 6.45 and 6.6 TB/s, 0.96 and 0.98 of the measured
-// copy; with 16,384 tokens and 2 choices (403 MB) 62.0 and 63.2 us.  Rows off
+// 91.9 us and combine 89.9: 6.57 and 6.72 TB/s, 0.98 and 1.00 of the measured
+// copy; with 16,384 tokens and 2 choices (403 MB) 59.7 and 61.5 us.  Rows off
 // 16-byte boundaries go element by element: 2,999 tokens, 6 choices, 1,001
-// floats (84 MB) 15.3 and 13.0 us.
+// floats (84 MB) 13.5 and 10.7 us.
 struct RowArgs {
     int64_t items;   // tokens * spans
     int32_t spans;
@@ -272,7 +288,7 @@ struct RowArgs {
 
 template <typename T, int N, int U>
 __global__ void __launch_bounds__(kRowThreads)
-route_dispatch_kernel(RowArgs a, const T *__restrict__ x, int64_t ldx, T *__restrict__ xs, int64_t ldxs) {
+route_dispatch_kernel(RowArgs a, const T *x, int64_t ldx, T *xs, int64_t ldxs) {
     using V = Vec<T, N>;
     after_previous();
     const int lane = threadIdx.x & 31;
@@ -287,18 +303,25 @@ route_dispatch_kernel(RowArgs a, const T *__restrict__ x, int64_t ldx, T *__rest
 #pragma unroll
     for (int u = 0; u < U; ++u)
         if (v0 + 32 * u < a.vecs) row[u] = src[v0 + 32 * u];
-    for (int j = 0; j < a.k; ++j) {
-        const int32_t p = __ldg(a.slot + t * a.k + j);
-        V *dst = reinterpret_cast<V *>(xs + (int64_t)(p < 0 ? -1 - p : p) * ldxs);
+    constexpr int BATCH = 4;  // slots read together
+    for (int j0 = 0; j0 < a.k; j0 += BATCH) {
+        int32_t p[BATCH];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v0 + 32 * u < a.vecs) dst[v0 + 32 * u] = p < 0 ? none : row[u];
+        for (int j = 0; j < BATCH; ++j) p[j] = j0 + j < a.k ? a.slot[t * a.k + j0 + j] : 0;
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            if (j0 + j >= a.k) break;
+            V *dst = reinterpret_cast<V *>(xs + (int64_t)(p[j] < 0 ? -1 - p[j] : p[j]) * ldxs);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v0 + 32 * u < a.vecs) dst[v0 + 32 * u] = p[j] < 0 ? none : row[u];
+        }
     }
 }
 
 template <typename T, int N, int U>
 __global__ void __launch_bounds__(kRowThreads)
-route_combine_kernel(RowArgs a, const T *__restrict__ ys, int64_t ldys, T *__restrict__ y, int64_t ldy) {
+route_combine_kernel(RowArgs a, const T *ys, int64_t ldys, T *y, int64_t ldy) {
     using V = Vec<T, N>;
     after_previous();
     const int lane = threadIdx.x & 31;
@@ -321,8 +344,8 @@ route_combine_kernel(RowArgs a, const T *__restrict__ ys, int64_t ldys, T *__res
 #pragma unroll
             for (int j = 0; j < BATCH; ++j) {
                 const bool in = j0 + j < a.k;
-                p[j] = in ? __ldg(a.slot + t * a.k + j0 + j) : -1;
-                w[j] = in && a.w ? __ldg(a.w + t * a.ldw + j0 + j) : 1.0f;
+                p[j] = in ? a.slot[t * a.k + j0 + j] : -1;
+                w[j] = in && a.w ? a.w[t * a.ldw + j0 + j] : 1.0f;
             }
 #pragma unroll
             for (int j = 0; j < BATCH; ++j)
@@ -334,19 +357,27 @@ route_combine_kernel(RowArgs a, const T *__restrict__ ys, int64_t ldys, T *__res
                     for (int n = 0; n < N; ++n) sum[0][n] = fmaf(w[j], to_float(r[j].v[n]), sum[0][n]);
         }
     } else {
+        for (int j0 = 0; j0 < a.k; j0 += 32) {
+            // the choices' slots and weights, one a lane, read together before the rows that they point to (a slot
+            // read before each row: 101.9 us for the 8,192 tokens, 89.9 so)
+            const bool in = j0 + lane < a.k;
+            const int32_t ps = in ? a.slot[t * a.k + j0 + lane] : -1;
+            const float ws = in && a.w ? a.w[t * a.ldw + j0 + lane] : 1.0f;
+            const int choices = min(32, a.k - j0);
 #pragma unroll 4
-        for (int j = 0; j < a.k; ++j) {
-            const int32_t p = __ldg(a.slot + t * a.k + j);
-            if (p < 0) continue;
-            const float w = a.w ? __ldg(a.w + t * a.ldw + j) : 1.0f;
-            const V *src = reinterpret_cast<const V *>(ys + (int64_t)p * ldys);
+            for (int j = 0; j < choices; ++j) {
+                const int32_t p = __shfl_sync(0xffffffffu, ps, j);
+                const float w = __shfl_sync(0xffffffffu, ws, j);
+                if (p < 0) continue;
+                const V *src = reinterpret_cast<const V *>(ys + (int64_t)p * ldys);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (v0 + 32 * u < a.vecs) {
-                    const V r = src[v0 + 32 * u];
+                for (int u = 0; u < U; ++u)
+                    if (v0 + 32 * u < a.vecs) {
+                        const V r = src[v0 + 32 * u];
 #pragma unroll
-                    for (int n = 0; n < N; ++n) sum[u][n] = fmaf(w, to_float(r.v[n]), sum[u][n]);
-                }
+                        for (int n = 0; n < N; ++n) sum[u][n] = fmaf(w, to_float(r.v[n]), sum[u][n]);
+                    }
+            }
         }
     }
     V *dst = reinterpret_cast<V *>(y + t * ldy);
@@ -370,8 +401,8 @@ route_combine_kernel(RowArgs a, const T *__restrict__ ys, int64_t ldys, T *__res
 // took 118 and 247 us.
 template <typename T, int N, int U>
 __global__ void __launch_bounds__(kRowThreads)
-route_combine_backward_kernel(RowArgs a, const T *__restrict__ dy, int64_t lddy, const T *ys, int64_t ldys, T *dys,
-                              int64_t lddys, float *__restrict__ dw, int64_t lddw) {
+route_combine_backward_kernel(RowArgs a, const T *dy, int64_t lddy, const T *ys, int64_t ldys, T *dys, int64_t lddys,
+                              float *dw, int64_t lddw) {
     using V = Vec<T, N>;
     after_previous();
     const int lane = threadIdx.x & 31;
@@ -379,8 +410,8 @@ route_combine_backward_kernel(RowArgs a, const T *__restrict__ dy, int64_t lddy,
     if (item >= a.items) return;
     const int64_t t = item / a.k;
     const int j = (int)(item - t * a.k);
-    const int32_t p = __ldg(a.slot + item);
-    const float w = a.w ? __ldg(a.w + t * a.ldw + j) : 1.0f;
+    const int32_t p = a.slot[item];
+    const float w = a.w ? a.w[t * a.ldw + j] : 1.0f;
     const V *g = reinterpret_cast<const V *>(dy + t * lddy);
     V *to = reinterpret_cast<V *>(dys + (int64_t)(p < 0 ? -1 - p : p) * lddys);
     if (p < 0) {
