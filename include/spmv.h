@@ -505,7 +505,8 @@ spmv_status_t spmv_spgemm_destroy(spmv_spgemm_t handle);
  */
 typedef enum { SPMV_ELEM_F32 = 0, SPMV_ELEM_BF16 = 1, SPMV_ELEM_F16 = 2 } spmv_elem_t;
 
-/* Bytes of workspace (HOST *bytes; 0 possible) spmv_route_build needs. */
+/* Bytes of workspace (HOST *bytes; 0 possible) spmv_route_build needs.  More
+ * tokens never need less: a workspace for the most serves them all. */
 spmv_status_t spmv_route_workspace(int32_t tokens, int32_t top_k, int32_t experts, size_t *bytes);
 
 /*

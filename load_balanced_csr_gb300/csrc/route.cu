@@ -560,7 +560,8 @@ spmv_status_t spmv_route_workspace(int32_t tokens, int32_t top_k, int32_t expert
     if (experts < 1 || experts > kMaxExperts) return llm_bad("experts must be in [1, 2048]");
     const int64_t n = (int64_t)tokens * top_k;
     if (n >= (1LL << 31)) return llm_bad("tokens * top_k must be < 2^31");
-    *bytes = build_clustered(n) ? 0 : (size_t)build_tiles(n) * (experts + 1) * 4;
+    // never below build_tiles of fewer entries, whose tiles may be smaller and more (152 of 1,245,184 entries, 77 of one more)
+    *bytes = build_clustered(n) ? 0 : (size_t)std::min<int64_t>(kMaxTiles, (n + kBuildTile - 1) / kBuildTile) * (experts + 1) * 4;
     return SPMV_OK;
 }
 

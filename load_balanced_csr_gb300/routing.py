@@ -42,7 +42,7 @@ class ExpertRoute:
         int32 = dict(dtype=torch.int32, device=self.device)
         self.expert_ptr = torch.empty(self.experts + 1, **int32)
         self._entry, self._slot = torch.empty(n, **int32), torch.empty(n, **int32)
-        # fewer tokens never need more workspace
+        # fewer tokens never need more workspace (spmv_route_workspace)
         self._workspace = torch.empty(size.value, dtype=torch.uint8, device=self.device)
         self._pointers = (self.expert_ptr.data_ptr(), self._entry.data_ptr(), self._slot.data_ptr(),
                           self._workspace.data_ptr(), size.value)

@@ -1,0 +1,14 @@
+"""Sizes and limits of the language-model operators' C entry points."""
+import ctypes
+
+import load_balanced_csr_gb300 as lb
+
+
+def test_route_workspace_never_shrinks():
+    """A workspace sized for more tokens serves fewer."""
+    L, size, last = lb.lib(), ctypes.c_size_t(), 0
+    edges = [0, 1, 131072, 131073, 1245184, 1245185, 2490368, 2490369, 3735552, 3735553, 2 ** 30, 2 ** 31 - 1]
+    for n in sorted(set(edges + [8192 * i + d for i in range(1, 700) for d in (0, 1)])):
+        assert L.spmv_route_workspace(n, 1, 2048, ctypes.byref(size)) == 0
+        assert size.value >= last, n
+        last = size.value

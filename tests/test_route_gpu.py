@@ -328,3 +328,15 @@ def test_refusals():
         r.combine(ys, out=torch.zeros(4, 8, device="cuda", dtype=torch.float16))
     with pytest.raises(TypeError):
         r.combine_backward(x, ys.half())
+
+
+@pytest.mark.parametrize("made_for,built", [(160000, 150000), (320000, 311296)])
+def test_fewer_tokens_than_the_route_was_made_for(made_for, built):
+    """The workspace of more tokens serves fewer, also where these are cut into more tiles."""
+    rng = np.random.default_rng(built)
+    ids = random_ids(rng, built, 8, 24, 0.01)
+    ptr, entry, slot = sorted_entries(ids, 24)
+    r = build(ids, 24, False, max_tokens=made_for)
+    np.testing.assert_array_equal(r.expert_ptr.cpu().numpy(), ptr)
+    np.testing.assert_array_equal(r.entry.cpu().numpy(), entry)
+    np.testing.assert_array_equal(r.slot.cpu().numpy(), slot)
