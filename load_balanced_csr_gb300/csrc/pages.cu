@@ -331,8 +331,9 @@ spmv_status_t spmv_pages_append(int32_t requests, const int32_t *past, const int
     cudaError_t e = cudaSuccess;
     if (requests <= kBlockRequests) {
         const size_t smem = sizeof(Request) * ((size_t)requests + 1);
-        if (smem > 47 * 1024)
-            e = cudaFuncSetAttribute(pages_append_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (smem > 47 * 1024)  // the function's limit is every host thread's: the most that any call needs
+            e = cudaFuncSetAttribute(pages_append_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)(sizeof(Request) * (kBlockRequests + 1)));
         if (e == cudaSuccess) e = launch_chained(pages_append_kernel<true>, blocks, kAppendThreads, smem, 0, stream, a);
     } else {
         e = launch_chained(pages_scan_kernel, 1, kAppendThreads, 0, 0, stream, a);

@@ -244,10 +244,12 @@ cudaError_t launch_build(int64_t n, int k, int experts, const I *ids, int64_t ld
                          int32_t *slot, int32_t *hist, cudaStream_t stream) {
     const int64_t tile = build_tile(n);
     const int tiles = build_tiles(n);
-    const size_t bins = (size_t)experts + 1, smem = bins * (3 * 4 + kBuildWarps * 2);
+    constexpr int per_bin = 3 * 4 + kBuildWarps * 2;
+    const size_t bins = (size_t)experts + 1, smem = bins * per_bin;
     if (smem > 47 * 1024) {
+        // the function's limit is every host thread's: the most that any call needs, not this one
         const cudaError_t e = cudaFuncSetAttribute(route_rank_kernel<I>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)smem);
+                                                   (kMaxExperts + 1) * per_bin);
         if (e != cudaSuccess) return e;
     }
     const bool clustered = build_clustered(n);

@@ -87,3 +87,68 @@ def test_build_dispatch_combine(tokens, k):
     for s in range(steps):
         entry = torch.argsort(ids[s].reshape(-1), stable=True)
         assert torch.equal(xs[s], x[s][entry // k])
+
+
+def _from_two_threads(*calls, times=4000):
+    """Each call made `times` times by a host thread of its own; the statuses other than 0."""
+    import threading
+    start, failed = threading.Barrier(len(calls)), []
+
+    def work(call):
+        start.wait()
+        for _ in range(times):
+            status = call()
+            if status:
+                failed.append(status)
+                return
+
+    threads = [threading.Thread(target=work, args=(call,)) for call in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return failed
+
+
+def test_builds_from_two_host_threads():
+    """Routes of 2,048 and of 700 experts, whose kernels need different
+    amounts of shared memory, built on streams of their own."""
+    import torch
+    import load_balanced_csr_gb300 as lb
+    L, n = lb.lib(), 64
+    calls, routes = [], []
+    for experts in (2048, 700):
+        ids = torch.randint(0, experts, (n, 1), device="cuda", dtype=torch.int32)
+        route, stream = lb.ExpertRoute(n, 1, experts).build(ids), torch.cuda.Stream()
+        routes.append((route, ids, stream))
+        ptr, entry, slot = (x.data_ptr() for x in (route.expert_ptr, route.entry, route.slot))
+        args = (n, 1, experts, ids.data_ptr(), 4, 1, ptr, entry, slot, None, 0, stream.cuda_stream)
+        calls.append(lambda args=args: L.spmv_route_build(*args))
+    torch.cuda.synchronize()
+    failed = _from_two_threads(*calls)
+    torch.cuda.synchronize()
+    assert not failed, lb.lib().spmv_last_error()
+    for route, ids, _ in routes:
+        assert torch.equal(route.entry.long(), torch.argsort(ids[:, 0], stable=True))
+
+
+def test_appends_from_two_host_threads():
+    """Steps of 4,096 and of 4,020 requests, as above."""
+    import torch
+    import load_balanced_csr_gb300 as lb
+    L = lb.lib()
+    calls, tables = [], []
+    for requests in (4096, 4020):
+        i32 = dict(dtype=torch.int32, device="cuda")
+        past, fresh, free = torch.zeros(requests, **i32), torch.ones(requests, **i32), torch.arange(requests, **i32)
+        pages, stream = lb.PageTable(torch.full((requests, 1), -1, **i32), 16, requests, requests), torch.cuda.Stream()
+        tables.append((pages, past, fresh, free, stream))
+        args = (requests, past.data_ptr(), fresh.data_ptr(), 16, requests, free.data_ptr(), requests, pages.table.data_ptr(),
+                1, 1, requests, *pages._outputs, stream.cuda_stream)
+        calls.append(lambda args=args: L.spmv_pages_append(*args))
+    torch.cuda.synchronize()
+    failed = _from_two_threads(*calls)
+    torch.cuda.synchronize()
+    assert not failed
+    for pages, _, fresh, free, _ in tables:
+        assert int(pages.status) == 0 and torch.equal(pages.table[:, 0], free) and torch.equal(pages.slots, free * 16)
