@@ -537,6 +537,8 @@ spmv_status_t spmv_route_build(int32_t tokens, int32_t top_k, int32_t experts, c
  * dropped entries (the last ones of xs) are set to zero, so xs is written
  * whole.  A copy: NaN payloads and signed zeros are kept.  The gradient of x
  * is spmv_route_combine of xs's gradient with null weights.
+ * Limits, here and in the two functions below: tokens * top_k < 2^31, hidden <
+ * 2^31 - 1024, tokens * hidden (rounded up to a multiple of 32) < 2^39.
  * Errors: INVALID_ARG, CUDA.  tokens, top_k or hidden of 0 is a no-op.
  */
 spmv_status_t spmv_route_dispatch(int32_t tokens, int32_t top_k, int32_t hidden, spmv_elem_t elem,

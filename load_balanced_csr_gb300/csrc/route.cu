@@ -542,7 +542,9 @@ const char *rows_bad(int32_t tokens, int32_t top_k, int32_t hidden, int elem) {
     if (tokens < 0 || top_k < 0 || hidden < 0) return "negative size";
     if ((int64_t)tokens * top_k >= (1LL << 31)) return "tokens * top_k must be < 2^31";
     if (!elem_ok(elem)) return "unknown element type";
-    // the passes' grids: one block per token, or eight warps of 32 elements
+    // a lane's place in a row, up to 32 * 8 elements of its last turn past the end, is counted in 32 bits
+    if (hidden >= INT32_MAX - 1023) return "hidden must be < 2^31 - 1024";
+    // the passes' grids: eight warps a block, each of at least 32 elements of a token or of one of its entries
     if ((int64_t)tokens * ((hidden + 31) / 32) / 8 >= (1LL << 31) - 1) return "tokens * hidden is too large";
     return nullptr;
 }
