@@ -599,7 +599,8 @@ spmv_status_t spmv_pages_workspace(int32_t requests, size_t *bytes);
  * served); bit 4 a page outside [0, num_pages) among those used (its tokens'
  * slots are -1).
  * Limits: page_size >= 1, num_pages * page_size < 2^31, the sums of past and
- * fresh over the requests < 2^31.  The workspace holds at least
+ * fresh over the requests < 2^31.  past and fresh must not overlap an output (a
+ * step's lens is copied before it is the next step's past).  The workspace holds at least
  * spmv_pages_workspace bytes, 16-byte aligned.
  * Errors: INVALID_ARG, CUDA.
  */

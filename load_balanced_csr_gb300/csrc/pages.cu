@@ -271,6 +271,12 @@ cudaError_t launch_store(const StoreArgs &a, const void *k, const void *v, void 
                           static_cast<T *>(vc));
 }
 
+// n entries at a and m at b have bytes in common
+bool overlap(const int32_t *a, int64_t n, const int32_t *b, int64_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return n > 0 && m > 0 && x < y + 4 * (uintptr_t)m && y < x + 4 * (uintptr_t)n;
+}
+
 bool on_16(const void *p, const int64_t *strides, int n, int size) {
     if (!aligned_to(p, 16)) return false;
     for (int i = 0; i < n; ++i)
@@ -307,8 +313,12 @@ spmv_status_t spmv_pages_append(int32_t requests, const int32_t *past, const int
     if ((int64_t)num_pages * page_size >= (1LL << 31)) return llm_bad("num_pages * page_size must be < 2^31");
     if (!token_ptr || !taken || !status) return llm_bad("token_ptr, taken or status is NULL");
     if (requests > 0 && (!past || !fresh || !lens)) return llm_bad("past, fresh or lens is NULL");
-    // every block reads the lengths while one writes lens
-    if (requests > 0 && (past == lens || fresh == lens)) return llm_bad("lens must not be past or fresh");
+    // every block reads the lengths while others write
+    const int64_t n = requests;
+    for (const int32_t *in : {past, fresh})
+        if (overlap(in, n, lens, n) || overlap(in, n, token_ptr, n + 1) || overlap(in, n, slots, max_tokens) ||
+            overlap(in, n, positions, max_tokens))
+            return llm_bad("lens, token_ptr, slots and positions must not overlap past or fresh");
     if (requests > 0 && max_pages > 0 && !table) return llm_bad("table is NULL");
     if (ld_table < max_pages) return llm_bad("ld_table is smaller than max_pages");
     if (num_free > 0 && !free_pages) return llm_bad("free_pages is NULL");

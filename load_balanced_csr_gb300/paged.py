@@ -56,7 +56,9 @@ class PageTable:
     def append(self, past, fresh, free_pages, stream=None) -> "PageTable":
         """Add ``fresh[r]`` tokens to request r, which holds ``past[r]``
         (both int32, one entry per request of the step, in the table's row
-        order); new pages come from ``free_pages`` (int32) in its order."""
+        order); new pages come from ``free_pages`` (int32) in its order.
+        ``past`` must not be ``lens`` itself: a step's lens is copied before
+        it is the next step's past."""
         d, n, free = self.device, past.numel(), free_pages.numel()
         if n > self.max_requests:
             raise ValueError(f"{n} requests, but the table has {self.max_requests} rows")

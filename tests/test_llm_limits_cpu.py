@@ -23,3 +23,23 @@ def test_rows_of_nearly_2_31_elements_are_refused():
         assert L.spmv_route_combine_backward(1, 1, hidden, 1, fake, None, 0, fake, hidden, fake, hidden, fake, hidden, fake, 1,
                                              None) == bad
     assert L.spmv_route_dispatch(0, 1, 2 ** 31 - 1025, 1, None, None, 2 ** 31, None, 2 ** 31, None) == 0
+
+
+def append(L, requests=100, work=0x900000, room=1 << 20, **at):
+    """spmv_pages_append with arguments that do not overlap, but for those given."""
+    p = dict(past=0x100000, fresh=0x200000, table=0x300000, free=0x400000, ptr=0x500000, lens=0x600000, slots=0x700000,
+             positions=0x800000, taken=0xa00000, status=0xb00000)
+    p.update(at)
+    return L.spmv_pages_append(requests, p["past"], p["fresh"], 16, 100, p["free"], 50, p["table"], 8, 8, 300, p["ptr"], p["lens"],
+                               p["slots"], p["positions"], p["taken"], p["status"], work, room, None)
+
+
+def test_outputs_of_an_append_may_not_overlap_the_lengths():
+    """Every block reads past and fresh while others write."""
+    L = lb.lib()
+    for name in ("past", "fresh"):
+        base = 0x100000
+        for out, length in (("lens", 100), ("ptr", 101), ("slots", 300), ("positions", 300)):
+            for off in (-4 * (length - 1), -4, 0, 4, 4 * 99):
+                assert append(L, **{name: base, out: base + off, "fresh" if name == "past" else "past": 0x200000}) == 1, (name, out, off)
+                assert b"overlap" in L.spmv_last_error()
