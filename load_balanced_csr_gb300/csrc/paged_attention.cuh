@@ -57,6 +57,7 @@ cudaError_t launch_attention_f16(const spmv_paged_attention_t &a, int sms, cudaS
 namespace {
 
 constexpr int kMaxDim = 256;
+constexpr int kSmemAlign = 32;  // bytes, of a block's shared memory: what the widest vector read from it asks for
 constexpr int kMaxSlice = 1024;  // requests per launch: their lengths and prefix sums live in shared memory
 // Units a row costs beside its chunks (its queries, its output): without, a
 // batch of 128 requests of 1 to 16,384 positions took 190 us instead of 158,
@@ -357,6 +358,8 @@ struct TileF32 {
     static constexpr float LIFT = 0.0f;
     static constexpr int WEIGHTS = GT * DP * 4;                // offset of the weights of a chunk behind the queries
     static constexpr int QBYTES = WEIGHTS + GT * CH * 4;
+    using Weights = Vec<float, GT>;                            // of a position
+    static_assert(kSmemAlign % alignof(Weights) == 0 && WEIGHTS % alignof(Weights) == 0, "a position's weights are aligned");
     static constexpr bool AHEAD = true;
     static constexpr int PAIRS = (DP + 63) / 64;               // pairs of elements of a lane; the last may not exist
 
@@ -456,7 +459,7 @@ struct TileF32 {
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i)
                 vv[i] = has_pair(lane, i) ? reinterpret_cast<const float2 *>(v + t * PITCH)[lane + 32 * i] : make_float2(0.0f, 0.0f);
-            const Vec<float, GT> w = *reinterpret_cast<const Vec<float, GT> *>(weights + t * GT);
+            const Weights w = *reinterpret_cast<const Weights *>(weights + t * GT);
 #pragma unroll
             for (int g = 0; g < GT; ++g)
 #pragma unroll
@@ -500,6 +503,7 @@ struct Record {
     static_assert(2 * FLOATS * 4 <= P::STAGES * STAGE, "both records of a warp fit its stages");
     static_assert(FLOATS % 4 == 0 && ROW % 4 == 0 && P::PITCH % 16 == 0 && P::QBYTES % 16 == 0, "16-byte accesses");
     static constexpr int PREFIX = (4 * (2 * kMaxSlice + 1) + 127) / 128 * 128;
+    static_assert(PREFIX % kSmemAlign == 0 && WARP % kSmemAlign == 0 && STAGE % kSmemAlign == 0, "as the block's shared memory");
     static constexpr int SMEM = PREFIX + P::NW * WARP;
 };
 
@@ -699,7 +703,7 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
     constexpr int NT = P::NW * 32;
     constexpr uint32_t FULL = FULL_MASK<P::CH>;
     enum { kFresh = 1, kBefore = 2, kRowEnd = 4, kShareEnd = 8 };
-    extern __shared__ __align__(16) char smem[];
+    extern __shared__ __align__(kSmemAlign) char smem[];
     __shared__ int4 notes[P::NW][P::STAGES];  // a stage's request, row, mask of positions, flags
     __shared__ int has[P::NW];                // bit 0: a head record, 1: a tail record, 2: its row began in an earlier warp
     __shared__ int rows_of[P::NW][4];         // head record's request and row, tail record's
