@@ -1,7 +1,10 @@
 """Shared by the language-model operators' bindings: streams, outputs, checks."""
 from __future__ import annotations
 
+import contextlib
+
 import torch
+import torch.autograd.forward_ad as _forward_mode
 
 ELEMS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
@@ -22,15 +25,53 @@ def handle(stream, device) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def on(stream, device):
+    """A context with ``stream`` current (None: as it is)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle(stream, device), device=device)
+    return torch.cuda.stream(stream)
+
+
 def empty(stream, device, shape, dtype):
     """An output for a launch on ``stream``, taken from that stream's own
     memory: memory of another stream could still be in use there."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(handle(stream, device), device=device)
-    with torch.cuda.stream(stream):
+    with on(stream, device):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def tracked(*tensors) -> bool:
+    """Whether torch differentiates a call on these tensors (or None)."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    if _forward_mode._current_level < 0:
+        return False
+    return any(t is not None and _forward_mode.unpack_dual(t).tangent is not None for t in tensors)
+
+
+def no_outputs_given(what, *given) -> None:
+    """Refuses outputs of the caller's for a call that torch differentiates, as torch's own operators do."""
+    if any(t is not None for t in given):
+        raise RuntimeError(f"{what}: outputs given by the caller (out=...) have no gradient, but a tensor of the call "
+                           "requires one")
+
+
+class NoDerivative(torch.autograd.Function):
+    """run()'s outputs, which raise an error when a gradient through them is asked for."""
+
+    @staticmethod
+    def forward(ctx, what, run, *tensors):
+        ctx.what = what
+        return run()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.what} has no derivative")
 
 
 def settle(device) -> None:

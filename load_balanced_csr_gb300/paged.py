@@ -114,7 +114,8 @@ def _check_store(k, v, k_cache, v_cache):
 def paged_store(k, v, k_cache, v_cache, slots, stream=None) -> None:
     """Write token i's keys and values (k, v: (tokens, kv_heads, head_dim),
     contiguous in the last dimension) into slot ``slots[i]`` (int32) of the
-    caches; slots outside the caches (-1: padding) are skipped."""
+    caches; slots outside the caches (-1: padding) are skipped.  For serving:
+    no gradient flows through the caches."""
     like = (k.shape, k.stride(), k.dtype, k.device, v.shape, v.stride(), v.dtype, v.device,
             k_cache.shape, k_cache.stride(), k_cache.dtype, k_cache.device,
             v_cache.shape, v_cache.stride(), v_cache.dtype, v_cache.device)
@@ -170,7 +171,16 @@ class PagedAttention:
     def __call__(self, q, k_cache, v_cache, table, lens, scale=None, out=None, lse=None, stream=None):
         """(out, lse) of q (batch, q_heads, head_dim) over the first
         ``lens[b]`` (int32) positions of each request, whose pages are row b
-        of ``table`` (int32).  ``scale``: head_dim ** -0.5 if None."""
+        of ``table`` (int32).  ``scale``: head_dim ** -0.5 if None.  It has no
+        derivative."""
+        if _launch.tracked(q, k_cache, v_cache, out):
+            _launch.no_outputs_given("PagedAttention", out, lse)
+            with _launch.on(stream, self.device):
+                return _launch.NoDerivative.apply("PagedAttention", lambda: self._attend(q, k_cache, v_cache, table, lens, scale),
+                                                  q, k_cache, v_cache)
+        return self._attend(q, k_cache, v_cache, table, lens, scale, out, lse, stream)
+
+    def _attend(self, q, k_cache, v_cache, table, lens, scale=None, out=None, lse=None, stream=None):
         d, a = self.device, self._args
         like = (q.shape, q.stride(), q.dtype, q.device, k_cache.shape, k_cache.stride(), k_cache.dtype, k_cache.device,
                 v_cache.shape, v_cache.stride(), v_cache.dtype, v_cache.device, table.shape, table.stride(), table.dtype,

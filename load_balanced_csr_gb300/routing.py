@@ -8,19 +8,70 @@
     dys, dw = route.combine_backward(dy, ys, weights)
     dx = route.dispatch_backward(dxs)
 
-The methods record no autograd graph: a torch.autograd.Function calls them in
-its forward and backward.  Argument marshalling only; include/spmv.h
-(spmv_route_*) has the contract.
+dispatch and combine are differentiable: torch's backward pass calls the two
+gradients above, on the stream of the forward call.  The forward call keeps a
+copy of ``slot`` for it, so the route may be rebuilt in between.  Argument
+marshalling only; include/spmv.h (spmv_route_*) has the contract.
 """
 from __future__ import annotations
 
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _launch
 
 __all__ = ["ExpertRoute"]
+
+
+def _contiguous_rows(g):
+    # torch's gradients may be expanded or transposed
+    return g if g.stride(-1) == 1 or g.shape[-1] == 1 else g.contiguous()
+
+
+def _at(slot):
+    return slot.shape[0], slot.data_ptr()
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, route, slot):
+        ctx.route = route
+        ctx.save_for_backward(slot)
+        return route._dispatch(_at(slot), x)
+
+    @staticmethod
+    def backward(ctx, dxs):
+        return _Sum.apply(_contiguous_rows(dxs), ctx.route, *ctx.saved_tensors), None, None
+
+
+class _Sum(torch.autograd.Function):
+    """combine without weights: dispatch's gradient, and its gradient is dispatch."""
+
+    @staticmethod
+    def forward(ctx, ys, route, slot):
+        ctx.route = route
+        ctx.save_for_backward(slot)
+        return route._combine(_at(slot), ys)
+
+    @staticmethod
+    def backward(ctx, dy):
+        return _Dispatch.apply(_contiguous_rows(dy), ctx.route, *ctx.saved_tensors), None, None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ys, weights, route, slot):
+        ctx.route = route
+        ctx.save_for_backward(ys, weights, slot)
+        return route._combine(_at(slot), ys, weights)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        ys, weights, slot = ctx.saved_tensors
+        return *ctx.route._combine_backward(_at(slot), _contiguous_rows(dy), ys, weights), None, None
 
 
 class ExpertRoute:
@@ -28,8 +79,9 @@ class ExpertRoute:
     experts each.  ``build`` fills ``expert_ptr`` (experts + 1), ``entry``
     (tokens * top_k) and ``slot`` (tokens, top_k), int32; the other methods
     read ``slot``.  A route is rebuilt for each batch; it must not be rebuilt
-    on one stream while another still uses it, and a training step keeps one
-    per layer until its backward pass.  Keep it until its calls have run."""
+    on one stream while another still uses it, and a training step that calls
+    the gradients itself keeps one per layer until its backward pass.  Keep it
+    until its calls have run."""
 
     def __init__(self, max_tokens: int, top_k: int, experts: int, device="cuda"):
         from . import check, lib
@@ -75,10 +127,15 @@ class ExpertRoute:
             self.tokens = tokens
         return self
 
-    def _built(self) -> int:
+    def _built(self):
+        """The tokens and where their slots are."""
         if self.tokens is None:
             raise RuntimeError("the route has not been built")
-        return self.tokens
+        return self.tokens, self._pointers[2]
+
+    def _kept_slot(self):
+        self._built()
+        return self.slot.clone()
 
     def _rows(self, what, like, *given):
         """The element type, hidden size and row strides of a call's tensors
@@ -91,19 +148,26 @@ class ExpertRoute:
         known = self._seen[what] = (like, _launch.elem(first.dtype), hidden, *found)
         return known
 
-    def _weights(self, weights):
+    def _weights(self, tokens, weights):
         if weights is None:
             return 0, 0
-        like = (self.tokens, weights.shape, weights.stride(), weights.dtype, weights.device)
+        like = (tokens, weights.shape, weights.stride(), weights.dtype, weights.device)
         known = self._seen.get("weights")
         if known is None or known[0] != like:
-            ld = _launch.rows("weights", weights, (self.tokens, self.top_k), torch.float32, self.device)
+            ld = _launch.rows("weights", weights, (tokens, self.top_k), torch.float32, self.device)
             known = self._seen["weights"] = (like, ld)
         return weights.data_ptr(), known[1]
 
     def dispatch(self, x, out=None, stream=None):
         """xs[p] = x[entry[p] // top_k]; rows of dropped entries are zero."""
-        t, k, d = self._built(), self.top_k, self.device
+        if _launch.tracked(x, out):
+            _launch.no_outputs_given("dispatch", out)
+            with _launch.on(stream, self.device):
+                return _Dispatch.apply(x, self, self._kept_slot())
+        return self._dispatch(self._built(), x, out, stream)
+
+    def _dispatch(self, at, x, out=None, stream=None):
+        (t, slot), k, d = at, self.top_k, self.device
         like = (t, x.shape, x.stride(), x.dtype, x.device,
                 None if out is None else (out.shape, out.stride(), out.dtype, out.device))
         known = self._seen.get("dispatch")
@@ -112,23 +176,31 @@ class ExpertRoute:
         _, e, hidden, ldx, ldo = known
         if out is None:
             out = _launch.empty(stream, d, (t * k, hidden), x.dtype)
-        _launch.call(self._L.spmv_route_dispatch, "spmv_route_dispatch", d, t, k, hidden, e, self._pointers[2],
+        _launch.call(self._L.spmv_route_dispatch, "spmv_route_dispatch", d, t, k, hidden, e, slot,
                      x.data_ptr(), ldx, out.data_ptr(), ldo, _launch.handle(stream, d))
         return out
 
     def combine(self, ys, weights=None, out=None, stream=None):
         """y[t] = sum over j of weights[t, j] * ys[slot[t, j]] (weights float32; None: 1)."""
-        t, k, d = self._built(), self.top_k, self.device
+        if _launch.tracked(ys, weights, out):
+            _launch.no_outputs_given("combine", out)
+            with _launch.on(stream, self.device):
+                slot = self._kept_slot()
+                return _Sum.apply(ys, self, slot) if weights is None else _Combine.apply(ys, weights, self, slot)
+        return self._combine(self._built(), ys, weights, out, stream)
+
+    def _combine(self, at, ys, weights=None, out=None, stream=None):
+        (t, slot), k, d = at, self.top_k, self.device
         like = (t, ys.shape, ys.stride(), ys.dtype, ys.device,
                 None if out is None else (out.shape, out.stride(), out.dtype, out.device))
         known = self._seen.get("combine")
         if known is None or known[0] != like:
             known = self._rows("combine", like, ("ys", ys, t * k), ("out", out, t))
         _, e, hidden, ldys, ldo = known
-        w, ldw = self._weights(weights)
+        w, ldw = self._weights(t, weights)
         if out is None:
             out = _launch.empty(stream, d, (t, hidden), ys.dtype)
-        _launch.call(self._L.spmv_route_combine, "spmv_route_combine", d, t, k, hidden, e, self._pointers[2], w, ldw,
+        _launch.call(self._L.spmv_route_combine, "spmv_route_combine", d, t, k, hidden, e, slot, w, ldw,
                      ys.data_ptr(), ldys, out.data_ptr(), ldo, _launch.handle(stream, d))
         return out
 
@@ -137,15 +209,24 @@ class ExpertRoute:
         return self.combine(dxs, None, out, stream)
 
     def combine_backward(self, dy, ys, weights=None, out=None, dweights=None, stream=None):
-        """The gradient of combine: (dys, dweights).  ``out`` may be ``ys``."""
-        t, k, d = self._built(), self.top_k, self.device
+        """The gradient of combine: (dys, dweights).  ``out`` may be ``ys``.
+        It has no derivative of its own."""
+        if _launch.tracked(dy, ys, weights, out, dweights):
+            _launch.no_outputs_given("combine_backward", out, dweights)
+            with _launch.on(stream, self.device):
+                return _launch.NoDerivative.apply(
+                    "combine_backward", lambda: self._combine_backward(self._built(), dy, ys, weights), dy, ys, weights)
+        return self._combine_backward(self._built(), dy, ys, weights, out, dweights, stream)
+
+    def _combine_backward(self, at, dy, ys, weights=None, out=None, dweights=None, stream=None):
+        (t, slot), k, d = at, self.top_k, self.device
         like = (t, dy.shape, dy.stride(), dy.dtype, dy.device, ys.shape, ys.stride(), ys.dtype, ys.device,
                 None if out is None else (out.shape, out.stride(), out.dtype, out.device))
         known = self._seen.get("combine_backward")
         if known is None or known[0] != like:
             known = self._rows("combine_backward", like, ("dy", dy, t), ("ys", ys, t * k), ("out", out, t * k))
         _, e, hidden, lddy, ldys, ldo = known
-        w, ldw = self._weights(weights)
+        w, ldw = self._weights(t, weights)
         if out is None:
             out = _launch.empty(stream, d, (t * k, hidden), dy.dtype)
         if dweights is None:
@@ -153,6 +234,6 @@ class ExpertRoute:
         else:
             lddw = _launch.rows("dweights", dweights, (t, k), torch.float32, d)
         _launch.call(self._L.spmv_route_combine_backward, "spmv_route_combine_backward", d, t, k, hidden, e,
-                     self._pointers[2], w, ldw, dy.data_ptr(), lddy, ys.data_ptr(), ldys, out.data_ptr(), ldo,
+                     slot, w, ldw, dy.data_ptr(), lddy, ys.data_ptr(), ldys, out.data_ptr(), ldo,
                      dweights.data_ptr(), lddw, _launch.handle(stream, d))
         return out, dweights
