@@ -639,8 +639,11 @@ spmv_status_t spmv_paged_store(int32_t tokens, int32_t heads, int32_t head_dim, 
  * a request's last page, and cache contents past its length, are not used
  * (they may hold anything, NaN included).  16-bit products are summed in 32
  * bits with weights of two elements each (16 or 22 bits; f16 weights in steps
- * of no less than 2^-39 of a row's largest); an infinity or NaN among the
- * values used makes its outputs infinite or NaN.
+ * of no less than 2^-39 of a row's largest).  An infinity in V makes its
+ * element infinite, or NaN where its weight is lost (below 2^-126 of the row's
+ * largest, f16 2^-40) or another infinity has the other sign; a score of minus
+ * infinity weighs nothing, a row of such scores only gets out = 0 and lse =
+ * -infinity, and a score of plus infinity or NaN makes its row NaN.
  *
  * The positions of all requests and kv heads together are cut into equal
  * shares, one per warp, whatever the lengths (the equal shares of the
