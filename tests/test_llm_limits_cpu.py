@@ -43,3 +43,13 @@ def test_outputs_of_an_append_may_not_overlap_the_lengths():
             for off in (-4 * (length - 1), -4, 0, 4, 4 * 99):
                 assert append(L, **{name: base, out: base + off, "fresh" if name == "past" else "past": 0x200000}) == 1, (name, out, off)
                 assert b"overlap" in L.spmv_last_error()
+
+
+def test_workspace_of_an_append():
+    """Needed above 4,096 requests only, and then whole and aligned."""
+    L, size = lb.lib(), ctypes.c_size_t(77)
+    assert L.spmv_pages_workspace(4096, ctypes.byref(size)) == 0 and size.value == 0
+    assert L.spmv_pages_workspace(5000, ctypes.byref(size)) == 0 and size.value > 0
+    for work, room in ((None, size.value), (0x900000, size.value - 1), (0x900000, 0), (0x900008, size.value)):
+        assert append(L, requests=5000, work=work, room=room) == 1
+        assert b"workspace" in L.spmv_last_error()
