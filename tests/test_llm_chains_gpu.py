@@ -152,3 +152,47 @@ def test_appends_from_two_host_threads():
     assert not failed
     for pages, _, fresh, free, _ in tables:
         assert int(pages.status) == 0 and torch.equal(pages.table[:, 0], free) and torch.equal(pages.slots, free * 16)
+
+
+def test_graph_with_copies_and_a_side_stream_between():
+    """Captured with copies, memsets and another stream's work before the
+    kernels: an edge to what is not a kernel, or is on another stream, is a
+    whole dependency."""
+    import torch
+    import load_balanced_csr_gb300 as lb
+    torch.manual_seed(4)
+    tokens, k, experts, hidden = 900, 2, 11, 64
+    source = [torch.randint(0, experts, (tokens, k), device="cuda") for _ in range(4)]
+    x, w = torch.randn(tokens, hidden, device="cuda"), torch.full((tokens, k), 0.5, device="cuda")
+    now, ids, row = source[0].clone(), torch.zeros_like(source[0]), torch.zeros_like(x)
+    route, side = lb.ExpertRoute(tokens, k, experts), torch.cuda.Stream()
+    xs, y = torch.empty(tokens * k, hidden, device="cuda"), torch.empty(tokens, hidden, device="cuda")
+
+    def step():
+        ids.zero_()
+        ids.copy_(now)
+        route.build(ids)
+        row.copy_(x)
+        route.dispatch(row, out=xs)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            y.zero_()
+            route.combine(xs, w, out=y)
+        torch.cuda.current_stream().wait_stream(side)
+        route.dispatch(y, out=xs)
+
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        step()
+    torch.cuda.current_stream().wait_stream(warm)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for s in source:
+        now.copy_(s)
+        x.normal_()
+        graph.replay()
+        entry = torch.argsort(s.reshape(-1), stable=True)
+        assert torch.equal(y, x)  # x / 2 + x / 2 is exact
+        assert torch.equal(xs, x[entry // k]) and torch.equal(route.entry.long(), entry)
