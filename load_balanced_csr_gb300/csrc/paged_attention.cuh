@@ -65,7 +65,8 @@ constexpr int kMaxSlice = 1024;  // requests per launch: their lengths and prefi
 constexpr uint32_t kRowCost = 3;
 // Rows of so few chunks are not cut between blocks, of so few not between
 // warps: joining would take longer than the row (4 requests of up to 300
-// positions 18.4 us with every row cut alike, 14.3 so; both with L2 flushed).
+// positions, lengths even over the logarithm, 16 heads of 64 f16 over as many:
+// 18.4 us with every row cut alike, 14.3 so; both with L2 flushed).
 constexpr uint32_t kBlockRow = 32;
 constexpr uint32_t kWarpRow = 2;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -323,8 +324,8 @@ struct TileMma {
                 mma16816<T>(o[2 * i + 1], pa, vb[2], vb[3]);
             }
             if (H == 2) {
-                // in a loop of its own, V read again: with both products at each V, the 64 requests of with_mma below
-                // took, 16 heads a kv head, 168 us instead of 150 with 256 elements, 152 instead of 140 with 192
+                // in a loop of its own, V read again: with both products at each V, 64 requests of 1 to 4,000 positions,
+                // 4 kv heads with 16 heads each, took 168 us instead of 150 with 256 elements, 152 instead of 140 with 192
 #pragma unroll
                 for (int i = 0; i < DP / 16; ++i) {
                     uint32_t vb[4];
@@ -1071,12 +1072,13 @@ cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStrea
 // Calls f with the tile of 16-bit elements T for the head size and group.
 //
 // Warps and stages: what an SM's registers and shared memory hold.  Of both
-// measured ways for tiles of 8 heads (64 requests of up to 4,000 positions, 4
-// kv heads): 96 elements 67.6 us with 10 warps of 3 stages, 69.7 with 8 of 4;
-// 128 elements 75.8 with 8 of 3, 86.0 with 10 or 12 of 2, whose registers do
-// not suffice; 192 elements 106 with 8 of 2, 135 with 4 of 4; 256 elements 129
-// with 6 of 2, 133 with 4 of 3.  Tiles of 16 heads need their registers, and
-// their records the stages' room.
+// measured ways for tiles of 8 heads (64 requests, their lengths even up to
+// 4,000, 4 kv heads with 4 heads each, 16 positions a page, bf16, calls one
+// after another): 96 elements (213 MB) 57.1 us with 10 warps of 3 stages, 58.5
+// with 8 of 4; 128 elements (284 MB) 61.2 with 8 of 3, 65.9 with 10 of 2, whose
+// registers do not suffice; 192 elements (426 MB) 89.3 with 8 of 2, 119.7 with
+// 4 of 4; 256 elements (568 MB) 111.7 with 6 of 2, 116.4 with 4 of 3.  Tiles of
+// 16 heads need their registers, and their records the stages' room.
 template <typename T, int GT, typename F>
 auto with_mma(int dim, F f) {
     constexpr bool small = GT == 8;

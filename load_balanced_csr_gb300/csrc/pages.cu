@@ -6,11 +6,12 @@
 // binary search in the prefix sums (as a merge-path tile finds its first
 // row), computes its slot from the table or, for a page not held before, from
 // the free list, and the token that opens a page writes the table's entry.
-// It is bound by latency: up to kBlockRequests requests every block makes the
-// prefix sums for itself in shared memory, and there is one launch (256
-// requests with a token each 6.5 us a step, 2,048 requests with 860 thousand
-// tokens 10.4 us, of which its 6.9 MB are 1 us); beyond, one block makes them
-// in global memory first.  One block's sums and a second launch took 11.6 and
+// It is bound by latency when there are few tokens, by its instructions when
+// there are many (0.69 of the issue slots): up to kBlockRequests requests every
+// block makes the prefix sums for itself in shared memory, and there is one
+// launch (256 requests with a token each 6.4 us a step, 2,048 requests with 860
+// thousand tokens 10.4 us, of which its 6.9 MB are 1 us); beyond, one block
+// makes them in global memory first.  One block's sums and a second launch took 11.6 and
 // 21.8 us.
 //
 // spmv_paged_store: a copy, 16 bytes a lane, four in flight for keys and
