@@ -425,7 +425,9 @@ route_combine_backward_kernel(RowArgs a, const T *dy, int64_t lddy, const T *ys,
         return;
     }
     const V *y = reinterpret_cast<const V *>(ys + (int64_t)p * ldys);
-    float dot[2] = {0.0f, 0.0f};
+    // eight sums a lane: as one or two, a long row's were off by up to half as many units of the last place as they have terms
+    constexpr int CHAINS = 8;
+    float dot[CHAINS] = {};
     for (int v0 = lane; v0 < a.vecs; v0 += 32 * U) {
         V gv[U], yv[U];
 #pragma unroll
@@ -441,14 +443,19 @@ route_combine_backward_kernel(RowArgs a, const T *dy, int64_t lddy, const T *ys,
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
                     const float gf = to_float(gv[u].v[n]);
-                    if (dw) dot[n & 1] = fmaf(gf, to_float(yv[u].v[n]), dot[n & 1]);
+                    float &sum = dot[(u * N + n) % CHAINS];
+                    if (dw) sum = fmaf(gf, to_float(yv[u].v[n]), sum);
                     r.v[n] = from_float<T>(w * gf);
                 }
                 to[v0 + 32 * u] = r;
             }
     }
     if (dw) {
-        float d = dot[0] + dot[1];
+#pragma unroll
+        for (int c = CHAINS / 2; c > 0; c /= 2)
+#pragma unroll
+            for (int i = 0; i < c; ++i) dot[i] += dot[i + c];
+        float d = dot[0];
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
         if (lane == 0) dw[t * lddw + j] = d;
