@@ -397,7 +397,7 @@ route_combine_kernel(RowArgs a, const T *ys, int64_t ldys, T *y, int64_t ldy) {
 // its gradient row, and sums its dot product over its lanes.  The choices of
 // a token are neighbouring warps, so dy's row comes from memory once and from
 // L1 for the others.  With rows of 4,096 bf16: 16,384 tokens, 2 choices
-// (671 MB) 99.6 us, 8,192 tokens, 8 choices (1,141 MB) 175 us: 6.7 and 6.5
+// (671 MB) 99.8 us, 8,192 tokens, 8 choices (1,141 MB) 176 us: 6.7 and 6.5
 // TB/s, 1.00 and 0.97 of the measured copy.  A block per token with dy's row
 // in registers for all choices needed 130-170 registers, so few warps fit, and
 // took 118 and 247 us.
