@@ -689,6 +689,95 @@ spmv_status_t spmv_paged_attention_workspace(int32_t max_batch, int32_t q_heads,
  * Errors: INVALID_ARG, CUDA. */
 spmv_status_t spmv_paged_attention(const spmv_paged_attention_t *args, spmv_stream_t stream);
 
+/*
+ * A paged cache of elements, or of 8-bit codes with scales.  Codes are e4m3:
+ * a sign, four exponent and three mantissa bits, no infinities, largest value
+ * 448, NaN 0x7f.  `block` neighbouring positions of a page share a float32
+ * scale per head: page * page_size / block + s / block is the block of
+ * position s of a page, and element d of it stands for
+ *   value(k_cache[page * k_stride[0] + s * k_stride[1] + h * k_stride[2] + d])
+ *     * k_scales[page * k_scale_stride[0] + (s / block) * k_scale_stride[1] + h * k_scale_stride[2]].
+ */
+typedef struct {
+    int32_t num_pages, page_size; /* num_pages * page_size < 2^31 */
+    int32_t block;                /* divides page_size; 0: the cache holds elements, no scales */
+    int32_t reserved;
+    int64_t k_stride[3];          /* page, position in it, head (elements or codes); the last index is contiguous */
+    int64_t v_stride[3];
+    int64_t k_scale_stride[3];    /* page, block in it, head */
+    int64_t v_scale_stride[3];
+    void *k_cache;
+    void *v_cache;
+    float *k_scales;
+    float *v_scales;
+} spmv_paged_cache_t;
+
+/*
+ * spmv_paged_store into a cache of codes (cache is a HOST structure, read
+ * before the call returns, with 1 <= block <= 64).  For a block of positions
+ * that tokens of this call are written to, a head, and keys or values:
+ *   need = the least power of two p >= 2^-126 with every finite |x| <= 448 p,
+ *          x over those tokens;
+ *   old  = the scale held; where the block's first position is written, the
+ *          block begins anew, and nothing it held counts;
+ *   new  = need in a block that begins anew, else max(old, need).
+ * The tokens' codes are x / new rounded to nearest, ties to even, NaN where x
+ * is not finite; new is stored; and where new > old in a block that does not
+ * begin anew the codes of its other positions become code * (old / new),
+ * rounded (exact for powers of two, but for codes below 2^-6).  The codes of
+ * the other positions of a block that begins anew stay as they are, without
+ * meaning.  So a block filled from its first position on, in any number of
+ * calls, keeps one scale for what it holds.
+ * Tokens of one call that go to the same block are neighbours in slots, in any
+ * order, skipped slots and at most 63 of these between two (as
+ * spmv_pages_append places them); with block 1 any order will do.  Two tokens
+ * must not share a slot.  Where either does not hold, what the blocks
+ * concerned hold is not specified.
+ * Limits: as spmv_paged_store, tokens * heads < 2^33.
+ * Errors: INVALID_ARG, CUDA.
+ */
+spmv_status_t spmv_paged_store_e4m3(int32_t tokens, int32_t heads, int32_t head_dim, spmv_elem_t elem, const int32_t *slots,
+                                    const spmv_paged_cache_t *cache, const void *k, const int64_t *k_stride, const void *v,
+                                    const int64_t *v_stride, spmv_stream_t stream);
+
+/*
+ * Read requests' positions back from a paged cache into packed rows: row i of
+ * k and v (i * k_stride[0] + h * k_stride[1] + d), token_ptr[r] <= i <
+ * token_ptr[r + 1], is position i - token_ptr[r] of request r, whose pages are
+ * row r of table (table + r * table_stride, max_pages entries).  token_ptr
+ * (device, requests + 1) does not fall and begins at 0.  A cache of codes
+ * gives code * scale in 32 bits, rounded to elem (block > 0); a cache of elements
+ * (block 0, type elem) is copied.  Rows behind token_ptr[requests] or from
+ * `tokens` on are left as they were; rows whose page is outside
+ * [0, num_pages) or past max_pages are zeros.
+ * Limits: tokens * heads * head_dim < 2^40, heads * head_dim < 2^30.
+ * Errors: INVALID_ARG, CUDA.
+ */
+spmv_status_t spmv_paged_load(int32_t requests, int32_t tokens, int32_t heads, int32_t head_dim, spmv_elem_t elem,
+                              const int32_t *table, int64_t table_stride, int32_t max_pages, const int32_t *token_ptr,
+                              const spmv_paged_cache_t *cache, void *k, const int64_t *k_stride, void *v,
+                              const int64_t *v_stride, spmv_stream_t stream);
+
+/*
+ * spmv_paged_attention over caches of codes: the key of position t is its
+ * codes times its key scale, and likewise the value (spmv_paged_cache_t has
+ * the layout; the scales need not be powers of two).  args->elem is the type
+ * of q and out, bf16 or f16; k_cache and v_cache hold codes and their strides
+ * count these (multiples of 16); head_dim is a multiple of 16.  q is taken in
+ * f16 times a power of two per head, without loss down to 2^-29 of the head's
+ * largest element; weights times value scales in 22 bits, in steps of no less
+ * than 2^-38 of a row's largest weight times its largest value scale.  A NaN
+ * code of a position makes its score, or its element of the output, NaN.
+ * workspace: spmv_paged_attention_e4m3_workspace bytes.  For the rest as
+ * spmv_paged_attention.
+ * Errors: INVALID_ARG, CUDA.
+ */
+spmv_status_t spmv_paged_attention_e4m3_workspace(int32_t max_batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                                  spmv_elem_t elem, size_t *bytes);
+spmv_status_t spmv_paged_attention_e4m3(const spmv_paged_attention_t *args, int32_t block, const float *k_scales,
+                                        const int64_t *k_scale_stride, const float *v_scales, const int64_t *v_scale_stride,
+                                        spmv_stream_t stream);
+
 /* Static text for a status code. */
 const char *spmv_status_string(spmv_status_t status);
 

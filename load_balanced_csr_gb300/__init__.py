@@ -11,7 +11,9 @@ the import of ``lib()`` raises.
 
 The language-model operators -- routing to experts (``ExpertRoute``), page
 tables and the paged cache (``PageTable``, ``paged_store``) and its attention
-(``PagedAttention``) -- are in ``routing`` and ``paged``.
+(``PagedAttention``), the same in 8 bits (``paged_store_e4m3``,
+``paged_load``, ``PagedAttentionE4M3``) -- are in ``routing``, ``paged`` and
+``paged_e4m3``.
 """
 from __future__ import annotations
 
@@ -21,7 +23,8 @@ import os
 from . import _build
 
 __all__ = ["Plan", "SpGEMM", "spgemm", "SpmvError", "lib", "KERNELS", "EXPORTS", "header_functions",
-           "gather_ceiling", "GATHER_PATHS", "ExpertRoute", "PageTable", "PagedAttention", "paged_store"]
+           "gather_ceiling", "GATHER_PATHS", "ExpertRoute", "PageTable", "PagedAttention", "paged_store",
+           "PagedAttentionE4M3", "paged_load", "paged_store_e4m3"]
 
 KERNELS = {"auto": 0, "merge_path": 1, "thread_row": 2, "rgcsr": 3, "long_rows": 4, "rgcsr_sorted": 5,
            "group_mapped": 6}
@@ -144,6 +147,10 @@ def _load(path: str) -> ctypes.CDLL:
         "spmv_paged_store": [i32, i32, i32, ctypes.c_int, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp],
         "spmv_paged_attention_workspace": [i32, i32, i32, i32, ctypes.c_int, ctypes.POINTER(sz)],
         "spmv_paged_attention": [vp, vp],
+        "spmv_paged_store_e4m3": [i32, i32, i32, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp],
+        "spmv_paged_load": [i32, i32, i32, i32, ctypes.c_int, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp],
+        "spmv_paged_attention_e4m3_workspace": [i32, i32, i32, i32, ctypes.c_int, ctypes.POINTER(sz)],
+        "spmv_paged_attention_e4m3": [vp, i32, vp, vp, vp, vp, vp],
     }
     for name, args in sigs.items():
         fn = getattr(L, name)
@@ -472,6 +479,9 @@ def __getattr__(name):
     elif name in ("PageTable", "PagedAttention", "paged_store"):
         from . import paged
         found = getattr(paged, name)
+    elif name in ("PagedAttentionE4M3", "paged_load", "paged_store_e4m3"):
+        from . import paged_e4m3
+        found = getattr(paged_e4m3, name)
     else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     globals()[name] = found

@@ -50,9 +50,18 @@ namespace lbcsr {
 size_t attention_workspace_f32(int dim, int group, int sms);
 size_t attention_workspace_bf16(int dim, int group, int sms);
 size_t attention_workspace_f16(int dim, int group, int sms);
+size_t attention_workspace_e4m3(int dim, int group, int sms);
 cudaError_t launch_attention_f32(const spmv_paged_attention_t &a, int sms, cudaStream_t stream);
 cudaError_t launch_attention_bf16(const spmv_paged_attention_t &a, int sms, cudaStream_t stream);
 cudaError_t launch_attention_f16(const spmv_paged_attention_t &a, int sms, cudaStream_t stream);
+
+// The scales of caches of 8-bit codes (paged_attention_e4m3.cu has the tile).
+struct AttendScales {
+    const float *k, *v;
+    int64_t k_stride[3], v_stride[3];  // page, block in it, head
+    uint32_t mul, shift;               // division by a block's positions
+};
+cudaError_t launch_attention_e4m3(const spmv_paged_attention_t &a, const AttendScales &scales, int sms, cudaStream_t stream);
 
 namespace {
 
@@ -89,10 +98,17 @@ struct AttendArgs {
     float *block_rec;    // [blocks][2] records: of the row that began earlier and ends here, of the one that goes on
 };
 
+struct ScaledArgs : AttendArgs {
+    AttendScales scales;
+};
+
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 // 16 bytes from global to shared memory; zeros when !real (src is then not read)
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool real) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -181,6 +197,10 @@ __device__ __forceinline__ float worth(float m, float base, float scale2) {
 template <typename T_, int GT_, int DP_, int CH_, int NW_, int STAGES_>
 struct TileMma {
     using T = T_;
+    using Cache = T;           // the caches' elements
+    using Args = AttendArgs;
+    static constexpr int SLICE = kMaxSlice;
+    static constexpr bool SCALES = false;
     static constexpr int DP = DP_, NW = NW_, STAGES = STAGES_, GT = GT_, CH = CH_;
     static constexpr int PAGE_UNIT = 16;   // positions that lie in one page when page_size is a multiple
     static constexpr int NT = CH / 8;      // the scores' product in columns of 8 positions
@@ -382,6 +402,10 @@ struct TileMma {
 template <int DP_, int GT_, int NW_, int STAGES_>
 struct TileF32 {
     using T = float;
+    using Cache = float;
+    using Args = AttendArgs;
+    static constexpr int SLICE = kMaxSlice;
+    static constexpr bool SCALES = false;
     static constexpr int DP = DP_, NW = NW_, STAGES = STAGES_, GT = GT_, CH = 8, PAGE_UNIT = 8;
     static constexpr int PITCH = DP * 4 + 16;
     static constexpr float LIFT = 0.0f;
@@ -527,11 +551,12 @@ template <class P>
 struct Record {
     static constexpr int ROW = P::DP + 8;  // the rows' first banks differ
     static constexpr int FLOATS = (P::GT * ROW + 2 * P::GT + 3) / 4 * 4;  // records are read 16 bytes at a time
-    static constexpr int STAGE = 2 * P::CH * P::PITCH;                  // bytes of a chunk's K and V
+    static constexpr int KV = 2 * P::CH * P::PITCH;                     // bytes of a chunk's K and V
+    static constexpr int STAGE = KV + (P::SCALES ? 8 * P::CH : 0);      // and their scales
     static constexpr int WARP = P::STAGES * STAGE + P::QBYTES;          // bytes of a warp's shared memory
     static_assert(2 * FLOATS * 4 <= P::STAGES * STAGE, "both records of a warp fit its stages");
     static_assert(FLOATS % 4 == 0 && ROW % 4 == 0 && P::PITCH % 16 == 0 && P::QBYTES % 16 == 0, "16-byte accesses");
-    static constexpr int PREFIX = (4 * (2 * kMaxSlice + 1) + 127) / 128 * 128;
+    static constexpr int PREFIX = (4 * (2 * P::SLICE + 1) + 127) / 128 * 128;
     static_assert(PREFIX % kSmemAlign == 0 && WARP % kSmemAlign == 0 && STAGE % kSmemAlign == 0, "as the block's shared memory");
     static constexpr int SMEM = PREFIX + P::NW * WARP;
 };
@@ -616,7 +641,7 @@ __device__ __forceinline__ Rows load_rows(const AttendArgs &p, char *smem) {
     __shared__ uint32_t warp_sum[P::NW];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t *pre = reinterpret_cast<uint32_t *>(smem);
-    int32_t *lens = reinterpret_cast<int32_t *>(smem) + kMaxSlice + 1;
+    int32_t *lens = reinterpret_cast<int32_t *>(smem) + P::SLICE + 1;
     uint32_t carry = 0;
     for (int b0 = 0; b0 < p.a.batch; b0 += NT) {
         const int b = b0 + threadIdx.x;
@@ -726,7 +751,7 @@ __device__ __forceinline__ void join(const AttendArgs &p, const float *from, int
 }
 
 template <class P>
-__global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendArgs p) {
+__global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(typename P::Args p) {
     using R = Record<P>;
     using T = typename P::T;
     constexpr int NT = P::NW * 32;
@@ -802,7 +827,8 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
         }
     };
     // copies chunk `at` into a stage and moves on
-    constexpr int PER = 16 / sizeof(T), VPR = P::DP / PER;  // elements in a copy, copies in a row
+    using C = typename P::Cache;
+    constexpr int PER = 16 / sizeof(C), VPR = P::DP / PER;  // elements in a copy, copies in a row
     auto copy = [&](int stage) {
         const int pos = (int)load.ch * P::CH + tok;
         const int32_t page = __shfl_sync(0xffffffffu, pages, (int)load.ch * unit - base + (one_page ? tok / P::PAGE_UNIT : tok));
@@ -816,6 +842,15 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
         opened = false;
         const int inside = pos - page_at(pos) * p.a.page_size;
         const uint32_t dst = smem_addr(mine + stage * R::STAGE);
+        if constexpr (P::SCALES) {
+            const int64_t pg = real ? page : 0;
+            const uint32_t in0 = real ? inside : 0, bl = (__umulhi(in0, p.scales.mul) + in0) >> p.scales.shift;
+            if (lane < P::CH) {
+                const AttendScales &s = p.scales;
+                copy4(dst + R::KV + lane * 4, s.k + pg * s.k_stride[0] + bl * s.k_stride[1] + kv_head * s.k_stride[2], real);
+                copy4(dst + R::KV + (P::CH + lane) * 4, s.v + pg * s.v_stride[0] + bl * s.v_stride[1] + kv_head * s.v_stride[2], real);
+            }
+        }
         if (32 % VPR == 0 && one_page && mask == FULL) {
             // a whole chunk: in a unit row r is r strides after row 0, and neighbouring lanes copy neighbours
             constexpr int STEP = 32 / VPR > 0 ? 32 / VPR : 1;  // rows a warp copies at once
@@ -825,9 +860,9 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
             for (int h = 0; h < P::CH / P::PAGE_UNIT; ++h) {
                 const int64_t page_h = __shfl_sync(0xffffffffu, page, h * P::PAGE_UNIT);
                 const int64_t in0 = __shfl_sync(0xffffffffu, inside, h * P::PAGE_UNIT) + row0;
-                const T *ks = static_cast<const T *>(p.a.k_cache) + page_h * p.a.k_stride[0] + in0 * p.a.k_stride[1] +
+                const C *ks = static_cast<const C *>(p.a.k_cache) + page_h * p.a.k_stride[0] + in0 * p.a.k_stride[1] +
                               kv_head * p.a.k_stride[2] + col * PER;
-                const T *vs = static_cast<const T *>(p.a.v_cache) + page_h * p.a.v_stride[0] + in0 * p.a.v_stride[1] +
+                const C *vs = static_cast<const C *>(p.a.v_cache) + page_h * p.a.v_stride[0] + in0 * p.a.v_stride[1] +
                               kv_head * p.a.v_stride[2] + col * PER;
                 const uint32_t to = dst + (h * P::PAGE_UNIT + row0) * P::PITCH + col * 16;
                 if (col * PER < p.a.head_dim) {
@@ -847,7 +882,7 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(AttendAr
             const int64_t pg = real ? page : 0, in0 = real ? inside : 0;
             const int64_t ko = pg * p.a.k_stride[0] + in0 * p.a.k_stride[1] + kv_head * p.a.k_stride[2];
             const int64_t vo = pg * p.a.v_stride[0] + in0 * p.a.v_stride[1] + kv_head * p.a.v_stride[2];
-            const T *kc = static_cast<const T *>(p.a.k_cache), *vc = static_cast<const T *>(p.a.v_cache);
+            const C *kc = static_cast<const C *>(p.a.k_cache), *vc = static_cast<const C *>(p.a.v_cache);
 #pragma unroll
             for (int i = 0; i < P::CH * VPR / 32; ++i) {
                 const int e = lane + 32 * i, row = e / VPR, col = e % VPR;
@@ -1030,10 +1065,11 @@ size_t workspace_of(int blocks) {
 }
 
 template <class P>
-cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStream_t stream) {
+cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStream_t stream, const AttendScales *scales = nullptr) {
     using R = Record<P>;
     using T = typename P::T;
-    AttendArgs p;
+    typename P::Args p;
+    if constexpr (P::SCALES) p.scales = *scales;
     p.a = a;
     p.group = a.q_heads / a.kv_heads;
     p.tiles = (p.group + P::GT - 1) / P::GT;
@@ -1055,7 +1091,7 @@ cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStrea
     cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::SMEM);
     // a launch's units are counted in 32 bits
     const int64_t most = (((int64_t)a.max_pages * a.page_size + P::CH - 1) / P::CH + kRowCost) * p.rows;
-    const int slice = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxSlice, ((1LL << 31) - 1) / std::max<int64_t>(1, most)));
+    const int slice = (int)std::max<int64_t>(1, std::min<int64_t>(P::SLICE, ((1LL << 31) - 1) / std::max<int64_t>(1, most)));
     for (int b = 0; b < a.batch && e == cudaSuccess; b += slice) {
         p.a.batch = std::min(slice, a.batch - b);
         p.a.q = static_cast<const char *>(a.q) + (int64_t)b * a.q_stride[0] * size;

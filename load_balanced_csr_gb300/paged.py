@@ -146,6 +146,8 @@ class PagedAttention:
     overlap on the GPU (two streams) need objects of their own, and an object
     is kept until its calls have run."""
 
+    _workspace_of, _cache_dtype = "spmv_paged_attention_workspace", None  # None: as q
+
     def __init__(self, max_batch: int, q_heads: int, kv_heads: int, head_dim: int, dtype, device="cuda"):
         self._L, self.device, self.dtype = lib(), _launch.cuda_device(device), dtype
         self._args = a = PagedAttentionArgs()
@@ -155,8 +157,8 @@ class PagedAttention:
         a.q_heads, a.kv_heads, a.head_dim = self.q_heads, self.kv_heads, self.head_dim
         size = ctypes.c_size_t()
         with torch.cuda.device(self.device):
-            check(self._L.spmv_paged_attention_workspace(self.max_batch, self.q_heads, self.kv_heads, self.head_dim,
-                                                         a.elem, ctypes.byref(size)), "spmv_paged_attention_workspace")
+            check(getattr(self._L, self._workspace_of)(self.max_batch, self.q_heads, self.kv_heads, self.head_dim, a.elem,
+                                                       ctypes.byref(size)), self._workspace_of)
         self._workspace = torch.empty(size.value, dtype=torch.uint8, device=self.device)
         self._workspace[:4096].zero_()
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
@@ -180,14 +182,18 @@ class PagedAttention:
                                                   q, k_cache, v_cache)
         return self._attend(q, k_cache, v_cache, table, lens, scale, out, lse, stream)
 
-    def _attend(self, q, k_cache, v_cache, table, lens, scale=None, out=None, lse=None, stream=None):
+    def _attend(self, q, k_cache, v_cache, table, lens, scale=None, out=None, lse=None, stream=None, scales=None):
         d, a = self.device, self._args
         like = (q.shape, q.stride(), q.dtype, q.device, k_cache.shape, k_cache.stride(), k_cache.dtype, k_cache.device,
                 v_cache.shape, v_cache.stride(), v_cache.dtype, v_cache.device, table.shape, table.stride(), table.dtype,
                 table.device, lens.shape, lens.stride(), lens.dtype, lens.device)
+        if scales is not None:
+            like += tuple((s.shape, s.stride(), s.dtype, s.device) for s in scales)
         if like != self._like:
             self._like = None
             self._check(q, k_cache, v_cache, table, lens)
+            if scales is not None:
+                self._check_scales(k_cache, scales)
             self._like, self._shape, self._dense = like, (q.shape, q.shape[:2]), False
         shape, heads = self._shape
         if out is not None:
@@ -208,8 +214,11 @@ class PagedAttention:
         a.scale = self._scale if scale is None else scale
         a.q, a.k_cache, a.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
         a.table, a.lens, a.out, a.lse = table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr()
-        _launch.call(self._L.spmv_paged_attention, "spmv_paged_attention", d, self._args_ref,
-                     _launch.handle(stream, d))
+        if scales is None:
+            _launch.call(self._L.spmv_paged_attention, "spmv_paged_attention", d, self._args_ref,
+                         _launch.handle(stream, d))
+        else:
+            self._launch_with(scales, stream)
         return out, lse
 
     def _check(self, q, k_cache, v_cache, table, lens):
@@ -222,8 +231,8 @@ class PagedAttention:
         batch, qs = q.shape[0], q.stride()
         if qs[2] != 1:
             raise ValueError("q must have a contiguous last dimension")
-        ks = _cache_strides("k_cache", k_cache, self.kv_heads, dim, dtype, d)
-        vs = _cache_strides("v_cache", v_cache, self.kv_heads, dim, dtype, d)
+        ks = _cache_strides("k_cache", k_cache, self.kv_heads, dim, self._cache_dtype or dtype, d)
+        vs = _cache_strides("v_cache", v_cache, self.kv_heads, dim, self._cache_dtype or dtype, d)
         if k_cache.shape != v_cache.shape:
             raise ValueError("k_cache and v_cache differ in shape")
         if table.dim() != 2 or table.shape[0] < batch:
