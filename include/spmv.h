@@ -778,6 +778,52 @@ spmv_status_t spmv_paged_attention_e4m3(const spmv_paged_attention_t *args, int3
                                         const int64_t *k_scale_stride, const float *v_scales, const int64_t *v_scale_stride,
                                         spmv_stream_t stream);
 
+/*
+ * Attention of packed prompts, or of chunks of them behind what their
+ * requests hold already.  Request r's queries are rows q_ptr[r] ..
+ * q_ptr[r + 1] - 1 of q (nq of them), its keys and values rows kv_ptr[r] ..
+ * kv_ptr[r + 1] - 1 of k and v (nk), kv head c = h / (q_heads / kv_heads) for
+ * query head h.  Query i (0 <= i < nq) sees the keys j <= i + nk - nq where
+ * `causal` is not 0 (its last query stands at its last key), else all:
+ *   s_j = scale * <q_i, k_j>,   lse = log sum_j exp(s_j),
+ *   out_i = sum_j exp(s_j - lse) v_j   over the keys it sees.
+ * A query that sees none gets out = 0 and lse = -infinity.  Keys and values
+ * that a query does not see may hold anything, NaN and infinities included;
+ * rows of out and lse that belong to no request are left as they were.  Sums
+ * and the softmax are in 32 bits; a weight is rounded to the elements' type
+ * once, as the second product's operand.  A score of minus infinity weighs
+ * nothing, a row of such scores only gets out = 0 and lse = -infinity, and a
+ * score of plus infinity or NaN makes its row NaN.
+ */
+typedef struct {
+    int32_t requests, tokens, keys; /* tokens: rows of q and out, keys: rows of k and v */
+    int32_t q_heads, kv_heads;      /* q_heads a multiple of kv_heads, at most 128 times as many;
+                                       tokens * q_heads < 2^31 */
+    int32_t head_dim;               /* a multiple of 8, at most 256 */
+    int32_t elem;                   /* spmv_elem_t of q, k, v and out: bf16 or f16 */
+    int32_t causal;
+    float scale;
+    int32_t reserved;
+    int64_t q_stride[2];            /* row, head (elements); multiples of 16 bytes, as are the addresses */
+    int64_t k_stride[2];
+    int64_t v_stride[2];
+    int64_t out_stride[2];
+    const void *q;
+    const void *k;
+    const void *v;
+    const int32_t *q_ptr;           /* [requests + 1], device; do not fall */
+    const int32_t *kv_ptr;          /* [requests + 1], or null: q_ptr */
+    void *out;
+    float *lse;                     /* [tokens * q_heads], or null */
+    int32_t *status;                /* device int32; flags are OR-ed in.  Bit 0: a request's queries are
+                                       not rows of q, bit 1: its keys are not rows of k; such a request
+                                       is left out, its rows of out stay as they were */
+} spmv_prompt_attention_t;
+
+/* args is a HOST structure, read before the call returns.
+ * Errors: INVALID_ARG, CUDA.  No requests, tokens or heads: nothing is done. */
+spmv_status_t spmv_prompt_attention(const spmv_prompt_attention_t *args, spmv_stream_t stream);
+
 /* Static text for a status code. */
 const char *spmv_status_string(spmv_status_t status);
 

@@ -12,8 +12,9 @@ the import of ``lib()`` raises.
 The language-model operators -- routing to experts (``ExpertRoute``), page
 tables and the paged cache (``PageTable``, ``paged_store``) and its attention
 (``PagedAttention``), the same in 8 bits (``paged_store_e4m3``,
-``paged_load``, ``PagedAttentionE4M3``) -- are in ``routing``, ``paged`` and
-``paged_e4m3``.
+``paged_load``, ``PagedAttentionE4M3``), attention of whole prompts
+(``PromptAttention``) -- are in ``routing``, ``paged``, ``paged_e4m3`` and
+``prompt``.
 """
 from __future__ import annotations
 
@@ -24,7 +25,7 @@ from . import _build
 
 __all__ = ["Plan", "SpGEMM", "spgemm", "SpmvError", "lib", "KERNELS", "EXPORTS", "header_functions",
            "gather_ceiling", "GATHER_PATHS", "ExpertRoute", "PageTable", "PagedAttention", "paged_store",
-           "PagedAttentionE4M3", "paged_load", "paged_store_e4m3"]
+           "PagedAttentionE4M3", "paged_load", "paged_store_e4m3", "PromptAttention"]
 
 KERNELS = {"auto": 0, "merge_path": 1, "thread_row": 2, "rgcsr": 3, "long_rows": 4, "rgcsr_sorted": 5,
            "group_mapped": 6}
@@ -151,6 +152,7 @@ def _load(path: str) -> ctypes.CDLL:
         "spmv_paged_load": [i32, i32, i32, i32, ctypes.c_int, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp],
         "spmv_paged_attention_e4m3_workspace": [i32, i32, i32, i32, ctypes.c_int, ctypes.POINTER(sz)],
         "spmv_paged_attention_e4m3": [vp, i32, vp, vp, vp, vp, vp],
+        "spmv_prompt_attention": [vp, vp],
     }
     for name, args in sigs.items():
         fn = getattr(L, name)
@@ -482,6 +484,8 @@ def __getattr__(name):
     elif name in ("PagedAttentionE4M3", "paged_load", "paged_store_e4m3"):
         from . import paged_e4m3
         found = getattr(paged_e4m3, name)
+    elif name == "PromptAttention":
+        from .prompt import PromptAttention as found
     else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     globals()[name] = found
