@@ -3,69 +3,540 @@
 //   s_ij = scale <q_i, k_j>,  out_i = sum_j exp(s_ij - m_i) v_j / sum_j exp(s_ij - m_i)
 //
 // with j over the keys of i's request, of them those up to i's own place where
-// it is causal.
+// it is causal, in one pass over the keys with the running maximum and sum of
+// the softmax.
+//
+// A tile of queries is 128 rows of one kv head: neighbouring tokens times the
+// query heads that share it, so that few tokens fill a tile and the keys are
+// read once for all of them.  A block takes two tiles (heads of up to 128
+// elements) and goes through their keys 128 at a time, or one tile and 64 keys.
+// Its warps are
+//   one that loads (TMA tensor copies, a ring of K and V tiles),
+//   one that issues the products (tcgen05, one thread), and
+//   four for each tile's softmax: a thread has a row.
+// Scores S = Q K^T and outputs O live in tensor memory.  A thread takes its row
+// of S into registers, and writes the weights over it as the left operand of
+// O += P V.  The products of one tile run while the other's softmax does: with
+// P_A ready the order is P_A V, then the next S_A, then P_B V, then the next
+// S_B, each in the order of issue, so S needs one buffer a tile.  With one tile
+// S has two buffers, and the next scores are there when the weights are done.
+//
+// The maximum that weights are relative to is raised only when a score is
+// kRaise powers of two above it, so that O is rarely rescaled; by the row's own
+// thread, which knows from the barrier of S that the product before is done.
+//
+// Keys and values behind a row's last are loaded with the tile.  Their weights
+// are zero, which a NaN or infinity in V would survive as NaN: in tiles that
+// any row sees in part the loading warp looks V over, puts zeros in the place
+// of what is not finite and notes it; the rows that do see such a value then
+// add it at the end.
+#include <algorithm>
+#include <cfloat>
 #include <cmath>
+#include <mutex>
+#include <type_traits>
+
+#include <cudaTypedefs.h>
 
 #include "internal.cuh"
 #include "llm.cuh"
+#include "tcgen05.cuh"
 
 namespace lbcsr {
 
 namespace {
 
-enum { kBadQueries = 1, kBadKeys = 2 };
+enum { kBadQueries = 1, kBadKeys = 2, kGaveUp = 4 };
 
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kRows = 128;
+constexpr int kCut = 4;  // tiles of keys that a block's rows see in part: its tokens span at most two tiles
+
+// DP: the head's elements rounded up to 64; NQ: tiles of a block.
+template <typename T_, int DP_, int NQ_>
+struct Shape {
+    using T = T_;
+    static constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
+    static constexpr int DP = DP_, NQ = NQ_, KEYS = NQ == 2 ? 128 : 64, HALVES = DP / 64;
+    static constexpr int THREADS = NQ * 128 + 128;  // two of the last four warps have nothing to do
+    static constexpr int QHALF = kRows * 128, QBYTES = HALVES * QHALF;    // 64 elements of a tile's rows; the tile
+    static constexpr int KHALF = KEYS * 128, KVBYTES = HALVES * KHALF;
+    static constexpr int SLOTS = DP == 64 ? 8 : DP == 192 ? 6 : 5;        // K and V tiles in shared memory
+    static constexpr int SMEM = 1024 + NQ * QBYTES + SLOTS * KVBYTES;
+    static constexpr uint32_t O = NQ == 2 ? 256 : 128;                    // columns of tensor memory: S at 0 and KEYS, then O
+    // Weights are 2^LIFT times as large, and up to 2^RAISE times that before the maximum is raised.  bf16 has the
+    // range of 32 bits; in f16 the largest stay below 2^15, and the smallest step is 2^-35 of a row's largest.
+    static constexpr float LIFT = BF16 ? 0.0f : 11.0f, RAISE = BF16 ? 8.0f : 4.0f;
+};
+
+struct PromptArgs {
+    spmv_prompt_attention_t a;
+    int32_t group, tile_tokens;  // query heads per kv head; tokens of a tile
+    uint32_t group_mul, group_shift;
+    float scale2;                // |scale| / ln 2
+    uint32_t negate;             // scale < 0
+};
+
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 template <typename T>
-__global__ void __launch_bounds__(128) prompt_attention_kernel(spmv_prompt_attention_t a) {
+__device__ __forceinline__ uint32_t pack(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack<__half>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The request and the place in it of a block, counted from the last request's last tokens, whose rows have most keys.
+struct Work {
+    int q0, nq, k0, nk;  // the request's rows
+    int t0;              // the block's first token in it
+};
+
+template <class S>
+__device__ __forceinline__ bool find_work(const PromptArgs &p, int block, Work *work, int *warp_sums, int *found) {
+    const int block_tokens = S::NQ * p.tile_tokens;
+    const int32_t *kv_ptr = p.a.kv_ptr ? p.a.kv_ptr : p.a.q_ptr;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int carry = 0;
+    if (threadIdx.x == 0) *found = 0;
+    for (int base = 0; base < p.a.requests; base += S::THREADS) {
+        const int r = p.a.requests - 1 - base - (int)threadIdx.x;
+        Work w{};
+        int n = 0, flag = 0;
+        if (r >= 0) {
+            const int q0 = p.a.q_ptr[r], q1 = p.a.q_ptr[r + 1], k0 = kv_ptr[r], k1 = kv_ptr[r + 1];
+            if (q0 < 0 || q1 < q0 || q1 > p.a.tokens) flag = kBadQueries;
+            else if (k0 < 0 || k1 < k0 || k1 > p.a.keys) flag = kBadKeys;
+            else w = Work{q0, q1 - q0, k0, k1 - k0, 0}, n = (w.nq + block_tokens - 1) / block_tokens;
+        }
+        if (flag && blockIdx.x == 0) atomicOr(p.a.status, flag);
+        int scan = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, scan, d);
+            if (lane >= d) scan += up;
+        }
+        if (lane == 31) warp_sums[warp] = scan;
+        __syncthreads();
+        int before = carry + scan - n;
+        for (int i = 0; i < S::THREADS / 32; ++i) {
+            if (i < warp) before += warp_sums[i];
+            carry += warp_sums[i];
+        }
+        if (block >= before && block < before + n) {
+            w.t0 = (n - 1 - (block - before)) * block_tokens;
+            *work = w;
+            *found = 1;
+        }
+        __syncthreads();
+        if (carry > block && blockIdx.x != 0) break;  // the first block looks all requests over
+    }
+    return *found;
+}
+
+template <class S>
+struct Shared {
+    uint64_t q_full, full[S::SLOTS], empty[S::SLOTS], scores[2], weights[2], clean[kCut], product[S::NQ], done[S::NQ], last;
+    uint32_t tmem;
+    int gave_up, not_finite, found, warp_sums[S::THREADS / 32];
+    Work work;
+};
+
+template <class S>
+__global__ void __launch_bounds__(S::THREADS, 1)
+prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_constant__ CUtensorMap q_map,
+                        const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    using T = typename S::T;
+    extern __shared__ char dynamic[];
+    __shared__ Shared<S> sh;
     after_previous();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), i = row / a.q_heads;
-    const int head = (int)(row - i * a.q_heads), kvh = head / (a.q_heads / a.kv_heads);
-    const int32_t *kv_ptr = a.kv_ptr ? a.kv_ptr : a.q_ptr;
-    for (int r = threadIdx.x; blockIdx.x == 0 && r < a.requests; r += 128) {
-        if (a.q_ptr[r] < 0 || a.q_ptr[r + 1] < a.q_ptr[r] || a.q_ptr[r + 1] > a.tokens) atomicOr(a.status, kBadQueries);
-        else if (kv_ptr[r] < 0 || kv_ptr[r + 1] < kv_ptr[r] || kv_ptr[r + 1] > a.keys) atomicOr(a.status, kBadKeys);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int kv_head = blockIdx.x % p.a.kv_heads;
+    if (!find_work<S>(p, blockIdx.x / p.a.kv_heads, &sh.work, sh.warp_sums, &sh.found)) return;  // the whole block
+    const Work w = sh.work;
+    char *smem = dynamic + ((1024 - (tc::smem_u32(dynamic) & 1023)) & 1023);
+    char *q_smem = smem, *kv_smem = smem + S::NQ * S::QBYTES;
+    constexpr int kLoader = S::NQ * 4, kIssuer = kLoader + 1;
+
+    // how many tiles of keys a tile of queries sees, and the first that some of the block's rows see in part
+    const int past = w.nk - w.nq;  // token t of the request stands at key t + past
+    auto keys_of = [&](int token) { return p.a.causal ? min(w.nk, max(0, token + past + 1)) : w.nk; };
+    int tiles[S::NQ], most = 0;
+#pragma unroll
+    for (int t = 0; t < S::NQ; ++t) {
+        const int first = w.t0 + t * p.tile_tokens, last = min(first + p.tile_tokens, w.nq) - 1;
+        tiles[t] = last < first ? 0 : (keys_of(last) + S::KEYS - 1) / S::KEYS;
+        most = max(most, tiles[t]);
     }
-    if (i >= a.tokens) return;
-    int r = 0;
-    while (r < a.requests && !(a.q_ptr[r] <= i && i < a.q_ptr[r + 1])) ++r;
-    if (r == a.requests) return;
-    const int32_t q0 = a.q_ptr[r], q1 = a.q_ptr[r + 1], k0 = kv_ptr[r], k1 = kv_ptr[r + 1];
-    if (q0 < 0 || q1 > a.tokens || k0 < 0 || k1 < k0 || k1 > a.keys) return;
-    int64_t n = k1 - k0;
-    if (a.causal) n = min(n, n - (q1 - q0) + (i - q0) + 1);
-    const T *q = static_cast<const T *>(a.q) + i * a.q_stride[0] + head * a.q_stride[1];
-    float o[8] = {}, m = -INFINITY, l = 0.0f;
-    for (int64_t j0 = 0; j0 < n; j0 += 32) {
-        const bool in = j0 + lane < n;
-        float s = -INFINITY;
-        if (in) {
-            const T *k = static_cast<const T *>(a.k) + (k0 + j0 + lane) * a.k_stride[0] + kvh * a.k_stride[1];
-            s = 0.0f;
-            for (int d = 0; d < a.head_dim; ++d) s = fmaf(to_float(q[d]), to_float(k[d]), s);
-            s *= a.scale;
+    const int first_cut = keys_of(w.t0) / S::KEYS;
+
+    if (threadIdx.x == 0) {
+        tc::bar_init(&sh.q_full, 1);
+        for (int i = 0; i < S::SLOTS; ++i) tc::bar_init(&sh.full[i], 1), tc::bar_init(&sh.empty[i], 1);
+        for (int i = 0; i < 2; ++i) tc::bar_init(&sh.scores[i], 1), tc::bar_init(&sh.weights[i], 128);
+        for (int i = 0; i < S::NQ; ++i) tc::bar_init(&sh.product[i], 1), tc::bar_init(&sh.done[i], 1);
+        for (int i = 0; i < kCut; ++i) tc::bar_init(&sh.clean[i], 1);
+        tc::bar_init(&sh.last, 1);
+        sh.gave_up = sh.not_finite = 0;
+        tc::bar_init_done();
+    }
+    if (warp == kIssuer) tc::alloc(&sh.tmem, 512);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = sh.tmem;
+    volatile int *gave_up = &sh.gave_up;
+    // A row of 128 scores needs more registers than 384 threads have each: three times 168 are 72 + 2 * 216.
+    static_assert(S::NQ == 1 || S::THREADS == 384, "the registers of the launch");
+    if (warp >= kLoader) {
+        if constexpr (S::NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == kLoader) {
+            int issued = 0;
+            bool ok = true;
+            if (lane == 0 && most > 0) {
+                const uint32_t box = (uint32_t)(p.tile_tokens * p.group * 128 * S::HALVES);
+                const int n = S::NQ == 2 && tiles[S::NQ - 1] > 0 ? 2 : 1;
+                tma::mbar_expect_tx(&sh.q_full, n * box);
+                for (int t = 0; t < n; ++t)
+                    for (int h = 0; h < S::HALVES; ++h)
+                        tc::load_3d(q_smem + t * S::QBYTES + h * S::QHALF, &q_map, 64 * h, kv_head * p.group,
+                                    w.q0 + w.t0 + t * p.tile_tokens, &sh.q_full);
+            }
+            auto load = [&](const CUtensorMap *map, int j) {
+                const int slot = issued % S::SLOTS, round = issued / S::SLOTS;
+                if (round > 0) ok = ok && tc::bar_wait(&sh.empty[slot], (round - 1) & 1, gave_up);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                if (lane == 0) {
+                    tma::mbar_expect_tx(&sh.full[slot], S::KVBYTES);
+                    for (int h = 0; h < S::HALVES; ++h)
+                        tc::load_3d(kv_smem + slot * S::KVBYTES + h * S::KHALF, map, 64 * h, kv_head, w.k0 + j * S::KEYS, &sh.full[slot]);
+                }
+                ++issued;
+            };
+            // looks the values of tile j over (their slot is 2 j + 1 in the order of loads)
+            auto look_over = [&](int j) {
+                if (j < first_cut) return;
+                const int at = 2 * j + 1, slot = at % S::SLOTS;
+                ok = ok && tc::bar_wait(&sh.full[slot], (at / S::SLOTS) & 1, gave_up);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                constexpr uint32_t EXPONENT = S::BF16 ? 0x7f807f80u : 0x7c007c00u, UNIT = S::BF16 ? 0x00800080u : 0x04000400u;
+                uint4 *v = reinterpret_cast<uint4 *>(kv_smem + slot * S::KVBYTES);
+                auto bad = [&](uint32_t x) { return ((x & EXPONENT) + UNIT) & 0x80008000u; };  // its halves that are not finite
+                uint32_t any = 0;
+    #pragma unroll 8
+                for (int i = lane; i < S::KVBYTES / 16; i += 32) {
+                    const uint4 x = v[i];
+                    any |= bad(x.x) | bad(x.y) | bad(x.z) | bad(x.w);
+                }
+                if (any) {
+                    auto zeroed = [&](uint32_t x) {
+                        const uint32_t b = bad(x);
+                        return x & ~((b >> 15) * 0xffffu);
+                    };
+                    for (int i = lane; i < S::KVBYTES / 16; i += 32) {
+                        const uint4 x = v[i];
+                        v[i] = make_uint4(zeroed(x.x), zeroed(x.y), zeroed(x.z), zeroed(x.w));
+                    }
+                    sh.not_finite = 1;
+                    tc::shared_to_async();
+                }
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(&sh.clean[j - first_cut]);
+            };
+            for (int j = 0; j < most && ok; ++j) {
+                load(&k_map, j);
+                if (ok) load(&v_map, j);
+                if (ok && j > 0) look_over(j - 1);
+            }
+            if (ok && most > 0) look_over(most - 1);
+            // nothing may be on its way into shared memory when the block ends
+            if (!ok) {
+                int none = 0;
+                if (most > 0) tc::bar_wait(&sh.q_full, 0, &none);
+                for (int i = std::max(0, issued - S::SLOTS); i < issued; ++i)
+                    tc::bar_wait(&sh.full[i % S::SLOTS], (i / S::SLOTS) & 1, &none);
+            }
+        } else if (warp == kIssuer) {
+            if (lane == 0 && most > 0) {
+                const uint32_t scores_of = tc::product(S::BF16, kRows, S::KEYS, false, p.negate != 0);
+                const int n16 = (p.a.head_dim + 15) / 16;
+                const uint32_t output_of = tc::product(S::BF16, kRows, 16 * n16, true, false);
+                const uint32_t q_at = tc::smem_u32(q_smem), kv_at = tc::smem_u32(kv_smem);
+                bool ok = tc::bar_wait(&sh.q_full, 0, gave_up);
+                auto wait_slot = [&](int at) { return tc::bar_wait(&sh.full[at % S::SLOTS], (at / S::SLOTS) & 1, gave_up); };
+                auto free_slot = [&](int at) { tc::commit(&sh.empty[at % S::SLOTS]); };
+                // S at column s = Q of tile t times K of tile j
+                auto scores = [&](int t, int j, uint32_t s) {
+                    const uint32_t k = kv_at + 2 * j % S::SLOTS * S::KVBYTES, q = q_at + t * S::QBYTES;
+                    for (int i = 0; i < n16; ++i)
+                        tc::mma(tmem + s, tc::operand(q + (i >> 2) * S::QHALF + (i & 3) * 32, 1024, 0),
+                                tc::operand(k + (i >> 2) * S::KHALF + (i & 3) * 32, 1024, 0), scores_of, i > 0);
+                };
+                auto output = [&](int t, int j, uint32_t s) {
+                    const uint32_t v = kv_at + (2 * j + 1) % S::SLOTS * S::KVBYTES;
+    #pragma unroll
+                    for (int i = 0; i < S::KEYS / 16; ++i)
+                        tc::mma_ts(tmem + S::O + t * S::DP, tmem + s + i * 8, tc::operand(v + i * 2048, 1024, S::KHALF), output_of,
+                                   j > 0 || i > 0);
+                };
+                auto values = [&](int j) {  // V of tile j is there, and looked over if need be
+                    return wait_slot(2 * j + 1) && (j < first_cut || tc::bar_wait(&sh.clean[j - first_cut], 0, gave_up));
+                };
+                if constexpr (S::NQ == 2) {
+                    ok = ok && wait_slot(0);
+                    if (ok) tc::fence_after();
+                    for (int t = 0; t < 2 && ok; ++t)
+                        if (tiles[t] > 0) scores(t, 0, t * S::KEYS), tc::commit(&sh.scores[t]);
+                    if (ok) free_slot(0);
+                    for (int j = 0; j < most && ok; ++j) {
+                        ok = values(j) && (j + 1 >= most || wait_slot(2 * j + 2));
+    #pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (!ok || j >= tiles[t]) continue;
+                            ok = tc::bar_wait(&sh.weights[t], j & 1, gave_up);
+                            if (!ok) continue;
+                            tc::fence_after();
+                            output(t, j, t * S::KEYS);
+                            if (j + 1 < tiles[t]) scores(t, j + 1, t * S::KEYS), tc::commit(&sh.scores[t]);
+                            else tc::commit(&sh.done[t]);
+                        }
+                        if (!ok) break;
+                        free_slot(2 * j + 1);
+                        if (j + 1 < most) free_slot(2 * j + 2);
+                    }
+                } else {
+                    for (int j = 0; j < 2 && j < most && ok; ++j) {
+                        ok = wait_slot(2 * j);
+                        if (!ok) break;
+                        tc::fence_after();
+                        scores(0, j, j * S::KEYS), tc::commit(&sh.scores[j]);
+                        free_slot(2 * j);
+                    }
+                    for (int j = 0; j < most && ok; ++j) {
+                        ok = values(j) && tc::bar_wait(&sh.weights[j & 1], (j >> 1) & 1, gave_up);
+                        if (!ok) break;
+                        tc::fence_after();
+                        output(0, j, (j & 1) * S::KEYS);
+                        tc::commit(&sh.product[0]);
+                        free_slot(2 * j + 1);
+                        if (j + 2 < most) {
+                            ok = wait_slot(2 * j + 4);
+                            if (!ok) break;
+                            tc::fence_after();
+                            scores(0, j + 2, (j & 1) * S::KEYS), tc::commit(&sh.scores[j & 1]);
+                            free_slot(2 * j + 4);
+                        }
+                    }
+                    if (ok) tc::commit(&sh.done[0]);
+                }
+                if (!ok) {  // no product may be under way when its memory is given back
+                    int none = 0;
+                    tc::commit(&sh.last);
+                    tc::bar_wait(&sh.last, 0, &none);
+                }
+            }
+            __syncwarp();
         }
-        float top = s;
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        top = fmaxf(top, m);
-        const float base = top == -INFINITY ? 0.0f : top, keep = m == -INFINITY ? 0.0f : expf(m - base);
-        const float w = in ? expf(s - base) : 0.0f;
-        float sum = w;
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        l = l * keep + sum;
-        m = top;
-        for (int e = 0; e < 8; ++e) o[e] *= keep;
-        for (int j = 0; j < 32 && j0 + j < n; ++j) {
-            const float wj = __shfl_sync(0xffffffffu, w, j);
-            const T *v = static_cast<const T *>(a.v) + (k0 + j0 + j) * a.v_stride[0] + kvh * a.v_stride[1];
-            for (int e = 0; e < 8; ++e)
-                if (lane + 32 * e < a.head_dim) o[e] = fmaf(wj, to_float(v[lane + 32 * e]), o[e]);
+    } else {
+        if constexpr (S::NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int t = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+        const int in_tile = (int)((__umulhi((uint32_t)row, p.group_mul) + (uint32_t)row) >> p.group_shift);
+        const int token = w.t0 + t * p.tile_tokens + in_tile, head = kv_head * p.group + row - in_tile * p.group;
+        const bool real = in_tile < p.tile_tokens && token < w.nq;
+        const int seen = keys_of(token), n = tiles[t];
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            const int buffer = S::NQ == 2 ? t : j & 1;
+            const uint32_t at = lanes + buffer * S::KEYS;
+            ok = tc::bar_wait(&sh.scores[buffer], S::NQ == 2 ? j & 1 : (j >> 1) & 1, gave_up);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc::fence_after();
+            float s[S::KEYS];
+#pragma unroll
+            for (int c = 0; c < S::KEYS; c += 32) tc::load32(at + c, reinterpret_cast<uint32_t *>(s + c));
+            tc::load_wait();
+            const int left = seen - j * S::KEYS;  // keys that the row sees here
+            const bool cut = j >= first_cut;
+            if (cut) {
+#pragma unroll
+                for (int c = 0; c < S::KEYS; ++c)
+                    if (c >= left) s[c] = -INFINITY;
+            }
+            float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < S::KEYS; c += 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], s[c + i]);
+            }
+            const float high = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+            const bool raise = real && (high - m) * p.scale2 > S::RAISE;
+            if (__any_sync(0xffffffffu, raise)) {
+                const float keep = raise ? (m == -INFINITY ? 0.0f : pow2((m - high) * p.scale2)) : 1.0f;
+                if (raise) m = high;
+                l *= keep;
+                if (j > 0) {
+                    if constexpr (S::NQ == 1) {  // with two tiles the barrier of S says it
+                        ok = tc::bar_wait(&sh.product[0], (j - 1) & 1, gave_up);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc::fence_after();
+                    }
+                    const uint32_t o_at = lanes + S::O + t * S::DP;
+                    for (int c = 0; c < p.a.head_dim; c += 32) {
+                        uint32_t o[32];
+                        tc::load32(o_at + c, o);
+                        tc::load_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                        tc::store32(o_at + c, o);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.0f : m;
+            const uint64_t minus = tc::pair(-base, -base), by = tc::pair(p.scale2, p.scale2), lift = tc::pair(S::LIFT, S::LIFT);
+            uint64_t sum[2] = {0, 0};
+            uint32_t weights[S::KEYS / 2];
+#pragma unroll
+            for (int c = 0; c < S::KEYS; c += 2) {
+                float x, y;
+                tc::unpair(tc::fma2(tc::add2(tc::pair(s[c], s[c + 1]), minus), by, lift), x, y);
+                x = pow2(x), y = pow2(y);
+                sum[c / 2 % 2] = tc::add2(sum[c / 2 % 2], tc::pair(x, y));
+                weights[c / 2] = pack<T>(x, y);
+            }
+            float a, b;
+            tc::unpair(tc::add2(sum[0], sum[1]), a, b);
+            l += a + b;
+#pragma unroll
+            for (int c = 0; c < S::KEYS / 2; c += 32) tc::store32(at + c, weights + c);
+            tc::store_wait();
+            tc::fence_before();
+            tc::bar_arrive(&sh.weights[buffer]);
+        }
+        if (n > 0 && ok) {
+            ok = tc::bar_wait(&sh.done[t], 0, gave_up);
+            ok = __all_sync(0xffffffffu, ok);
+            tc::fence_after();
+            if (first_cut < most) ok = ok && tc::bar_wait(&sh.clean[most - first_cut - 1], 0, gave_up);  // not_finite
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        if (ok && w.t0 + t * p.tile_tokens < w.nq) {
+            T *out = static_cast<T *>(p.a.out) + (int64_t)(w.q0 + token) * p.a.out_stride[0] + head * p.a.out_stride[1];
+            const T *v = static_cast<const T *>(p.a.v) + (int64_t)w.k0 * p.a.v_stride[0] + kv_head * p.a.v_stride[1];
+            const float inverse = l == 0.0f ? 0.0f : 1.0f / l;
+            for (int c = 0; c < p.a.head_dim; c += 32) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tc::load32(lanes + S::O + t * S::DP + c, o);
+                    tc::load_wait();
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = n > 0 ? __float_as_uint(__uint_as_float(o[i]) * inverse) : 0u;
+                if (!real) continue;
+                if (sh.not_finite) {  // values that are not finite and seen by this row
+                    for (int k = first_cut * S::KEYS; k < seen; ++k)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < p.a.head_dim) {
+                                const float x = to_float(v[k * p.a.v_stride[0] + c + i]);
+                                if (!(fabsf(x) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+                            }
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 8)
+                    if (c + i < p.a.head_dim)
+                        *reinterpret_cast<uint4 *>(out + c + i) =
+                            make_uint4(pack<T>(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), pack<T>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3])),
+                                       pack<T>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5])), pack<T>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
+            }
+            if (real && p.a.lse)
+                p.a.lse[(int64_t)(w.q0 + token) * p.a.q_heads + head] =
+                    l == 0.0f ? -INFINITY : fmaf(m == -INFINITY ? 0.0f : m, p.scale2, log2f(l) - S::LIFT) * kLn2;
         }
     }
-    T *out = static_cast<T *>(a.out) + i * a.out_stride[0] + head * a.out_stride[1];
-    for (int e = 0; e < 8; ++e)
-        if (lane + 32 * e < a.head_dim) out[lane + 32 * e] = from_float<T>(l == 0.0f ? 0.0f : o[e] / l);
-    if (lane == 0 && a.lse) a.lse[i * a.q_heads + head] = l == 0.0f ? -INFINITY : m + logf(l);
+    tc::fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && sh.gave_up) atomicOr(p.a.status, kGaveUp);
+    if (warp == kIssuer) {
+        tc::fence_after();
+        tc::dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- launch
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+// rows x heads x head_dim elements at `at`; a copy takes 64 elements of box_heads heads of box_rows rows
+bool make_map(CUtensorMap *map, bool bf16, const void *at, int head_dim, int heads, int rows, const int64_t *stride, int box_heads,
+              int box_rows) {
+    const auto encode = map_encoder();
+    if (!encode) return false;
+    // the stride of a dimension of one element is never used, but checked
+    const int64_t head_stride = heads > 1 ? stride[1] : head_dim, row_stride = rows > 1 ? stride[0] : (int64_t)heads * head_dim;
+    const cuuint64_t sizes[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)row_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows}, step[3] = {1, 1, 1};
+    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(at), sizes,
+                  strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class S>
+spmv_status_t launch_prompt(const spmv_prompt_attention_t &a, cudaStream_t stream) {
+    PromptArgs p;
+    p.a = a;
+    p.group = a.q_heads / a.kv_heads;
+    p.tile_tokens = kRows / p.group;
+    set_divisor((uint32_t)p.group, &p.group_mul, &p.group_shift);
+    // weights of masked scores, minus infinity, have to be 0: a scale of 0 is taken as one that no score feels
+    p.scale2 = std::max(std::fabs(a.scale) * kLog2e, FLT_MIN);
+    p.negate = a.scale < 0.0f;
+    CUtensorMap maps[3];
+    const bool keys = a.keys > 0;  // without keys nothing is loaded
+    if (!make_map(&maps[0], S::BF16, a.q, a.head_dim, a.q_heads, a.tokens, a.q_stride, p.group, p.tile_tokens) ||
+        !make_map(&maps[1], S::BF16, keys ? a.k : a.q, a.head_dim, a.kv_heads, std::max(a.keys, 1), a.k_stride, 1, S::KEYS) ||
+        !make_map(&maps[2], S::BF16, keys ? a.v : a.q, a.head_dim, a.kv_heads, std::max(a.keys, 1), a.v_stride, 1, S::KEYS))
+        return llm_fail(SPMV_ERR_CUDA, "spmv_prompt_attention: the driver refused a tensor map");
+    const int64_t blocks = ((int64_t)a.tokens / (S::NQ * p.tile_tokens) + std::min(a.requests, a.tokens)) * a.kv_heads;
+    cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e == cudaSuccess)
+        e = launch_chained(prompt_attention_kernel<S>, (unsigned)blocks, S::THREADS, S::SMEM, 0, stream, p, maps[0], maps[1], maps[2]);
+    return llm_launched("spmv_prompt_attention launch", e);
+}
+template <typename T>
+spmv_status_t launch_prompt_of(const spmv_prompt_attention_t &a, cudaStream_t stream) {
+    if (a.head_dim <= 64) return launch_prompt<Shape<T, 64, 2>>(a, stream);
+    if (a.head_dim <= 128) return launch_prompt<Shape<T, 128, 2>>(a, stream);
+    if (a.head_dim <= 192) return launch_prompt<Shape<T, 192, 1>>(a, stream);
+    return launch_prompt<Shape<T, 256, 1>>(a, stream);
 }
 
 const char *prompt_bad(const spmv_prompt_attention_t &a) {
@@ -85,6 +556,11 @@ const char *prompt_bad(const spmv_prompt_attention_t &a) {
     for (int i = 0; i < 2; ++i)
         if (a.q_stride[i] % 8 || a.k_stride[i] % 8 || a.v_stride[i] % 8 || a.out_stride[i] % 8)
             return "strides must be multiples of 16 bytes";
+    const int sizes[2] = {a.tokens, a.q_heads}, kv_sizes[2] = {a.keys, a.kv_heads};
+    for (int i = 0; i < 2; ++i)  // as tensor copies take them
+        if ((sizes[i] > 1 && (a.q_stride[i] < 1 || a.q_stride[i] >= (1LL << 38))) ||
+            (kv_sizes[i] > 1 && (a.k_stride[i] < 1 || a.k_stride[i] >= (1LL << 38) || a.v_stride[i] < 1 || a.v_stride[i] >= (1LL << 38))))
+            return "strides of q, k and v must be positive and less than 2^38";
     return nullptr;
 }
 
@@ -102,10 +578,7 @@ spmv_status_t spmv_prompt_attention(const spmv_prompt_attention_t *args, spmv_st
     if (const char *bad = prompt_bad(a)) return llm_bad(bad);
     if (a.requests == 0 || a.tokens == 0 || a.q_heads == 0) return SPMV_OK;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
-    const unsigned grid = (unsigned)(((int64_t)a.tokens * a.q_heads + 3) / 4);
-    return llm_launched("spmv_prompt_attention launch",
-                        a.elem == SPMV_ELEM_BF16 ? launch_chained(prompt_attention_kernel<__nv_bfloat16>, grid, 128, 0, 0, stream, a)
-                                                 : launch_chained(prompt_attention_kernel<__half>, grid, 128, 0, 0, stream, a));
+    return a.elem == SPMV_ELEM_BF16 ? launch_prompt_of<__nv_bfloat16>(a, stream) : launch_prompt_of<__half>(a, stream);
 }
 
 }  // extern "C"
