@@ -62,12 +62,13 @@ struct Shape {
     static constexpr int THREADS = NQ * 128 + 128;  // two of the last four warps have nothing to do
     static constexpr int QHALF = kRows * 128, QBYTES = HALVES * QHALF;    // 64 elements of a tile's rows; the tile
     static constexpr int KHALF = KEYS * 128, KVBYTES = HALVES * KHALF;
-    static constexpr int SLOTS = DP == 64 ? 8 : DP == 192 ? 6 : 5;        // K and V tiles in shared memory
-    static constexpr int SMEM = 1024 + NQ * QBYTES + SLOTS * KVBYTES;
+    // A stage holds the tiles that a step takes: V of tile j and K of tile j + 1.  Stage 0 begins with K of tile 0 alone.
+    static constexpr int STAGES = DP == 64 ? 4 : DP == 192 ? 3 : 2, STAGE = 2 * KVBYTES;
+    static constexpr int SMEM = 1024 + NQ * QBYTES + STAGES * STAGE;
     static constexpr uint32_t O = NQ == 2 ? 256 : 128;                    // columns of tensor memory: S at 0 and KEYS, then O
     // Weights are 2^LIFT times as large, and up to 2^RAISE times that before the maximum is raised.  bf16 has the
     // range of 32 bits; in f16 the largest stay below 2^15, and the smallest step is 2^-35 of a row's largest.
-    static constexpr float LIFT = BF16 ? 0.0f : 11.0f, RAISE = BF16 ? 8.0f : 4.0f;
+    static constexpr float LIFT = BF16 ? 0.0f : 11.0f, RAISE = BF16 ? 8.0f : 4.0f, LIMIT = BF16 ? 256.0f : 32768.0f;
 };
 
 struct PromptArgs {
@@ -148,7 +149,7 @@ __device__ __forceinline__ bool find_work(const PromptArgs &p, int block, Work *
 
 template <class S>
 struct Shared {
-    uint64_t q_full, full[S::SLOTS], empty[S::SLOTS], scores[2], weights[2], clean[kCut], product[S::NQ], done[S::NQ], last;
+    uint64_t q_full, full[S::STAGES], empty[S::STAGES], scores[2], weights[2], clean[kCut], product[S::NQ], done[S::NQ], last;
     uint32_t tmem;
     int gave_up, not_finite, found, warp_sums[S::THREADS / 32];
     Work work;
@@ -184,11 +185,11 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
 
     if (threadIdx.x == 0) {
         tc::bar_init(&sh.q_full, 1);
-        for (int i = 0; i < S::SLOTS; ++i) tc::bar_init(&sh.full[i], 1), tc::bar_init(&sh.empty[i], 1);
+        for (int i = 0; i < S::STAGES; ++i) tc::bar_init(&sh.full[i], 1), tc::bar_init(&sh.empty[i], 1);
         for (int i = 0; i < 2; ++i) tc::bar_init(&sh.scores[i], 1), tc::bar_init(&sh.weights[i], 128);
         for (int i = 0; i < S::NQ; ++i) tc::bar_init(&sh.product[i], 1), tc::bar_init(&sh.done[i], 1);
-        for (int i = 0; i < kCut; ++i) tc::bar_init(&sh.clean[i], 1);
         tc::bar_init(&sh.last, 1);
+        for (int i = 0; i < kCut; ++i) tc::bar_init(&sh.clean[i], 1);
         sh.gave_up = sh.not_finite = 0;
         tc::bar_init_done();
     }
@@ -214,27 +215,31 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                         tc::load_3d(q_smem + t * S::QBYTES + h * S::QHALF, &q_map, 64 * h, kv_head * p.group,
                                     w.q0 + w.t0 + t * p.tile_tokens, &sh.q_full);
             }
-            auto load = [&](const CUtensorMap *map, int j) {
-                const int slot = issued % S::SLOTS, round = issued / S::SLOTS;
-                if (round > 0) ok = ok && tc::bar_wait(&sh.empty[slot], (round - 1) & 1, gave_up);
+            // pair i: K of tile i, if there is one, and V of the tile before
+            auto load = [&](int i) {
+                const int stage = i % S::STAGES, round = i / S::STAGES;
+                if (round > 0) ok = tc::bar_wait(&sh.empty[stage], (round - 1) & 1, gave_up);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
                 if (lane == 0) {
-                    tma::mbar_expect_tx(&sh.full[slot], S::KVBYTES);
-                    for (int h = 0; h < S::HALVES; ++h)
-                        tc::load_3d(kv_smem + slot * S::KVBYTES + h * S::KHALF, map, 64 * h, kv_head, w.k0 + j * S::KEYS, &sh.full[slot]);
+                    tma::mbar_expect_tx(&sh.full[stage], ((i < most) + (i > 0)) * S::KVBYTES);
+                    for (int h = 0; h < S::HALVES; ++h) {
+                        char *at = kv_smem + stage * S::STAGE + h * S::KHALF;
+                        if (i < most) tc::load_3d(at, &k_map, 64 * h, kv_head, w.k0 + i * S::KEYS, &sh.full[stage]);
+                        if (i > 0) tc::load_3d(at + S::KVBYTES, &v_map, 64 * h, kv_head, w.k0 + (i - 1) * S::KEYS, &sh.full[stage]);
+                    }
                 }
                 ++issued;
             };
-            // looks the values of tile j over (their slot is 2 j + 1 in the order of loads)
+            // looks the values of tile j over
             auto look_over = [&](int j) {
                 if (j < first_cut) return;
-                const int at = 2 * j + 1, slot = at % S::SLOTS;
-                ok = ok && tc::bar_wait(&sh.full[slot], (at / S::SLOTS) & 1, gave_up);
+                const int stage = (j + 1) % S::STAGES;
+                ok = tc::bar_wait(&sh.full[stage], (j + 1) / S::STAGES & 1, gave_up);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
                 constexpr uint32_t EXPONENT = S::BF16 ? 0x7f807f80u : 0x7c007c00u, UNIT = S::BF16 ? 0x00800080u : 0x04000400u;
-                uint4 *v = reinterpret_cast<uint4 *>(kv_smem + slot * S::KVBYTES);
+                uint4 *v = reinterpret_cast<uint4 *>(kv_smem + stage * S::STAGE + S::KVBYTES);
                 auto bad = [&](uint32_t x) { return ((x & EXPONENT) + UNIT) & 0x80008000u; };  // its halves that are not finite
                 uint32_t any = 0;
     #pragma unroll 8
@@ -257,99 +262,114 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(&sh.clean[j - first_cut]);
             };
-            for (int j = 0; j < most && ok; ++j) {
-                load(&k_map, j);
-                if (ok) load(&v_map, j);
-                if (ok && j > 0) look_over(j - 1);
+            // values are looked over once the next load is under way: what frees its stage does not wait for them
+            for (int i = 0; i <= most && most > 0 && ok; ++i) {
+                load(i);
+                if (ok && i > 1) look_over(i - 2);
             }
             if (ok && most > 0) look_over(most - 1);
             // nothing may be on its way into shared memory when the block ends
             if (!ok) {
                 int none = 0;
                 if (most > 0) tc::bar_wait(&sh.q_full, 0, &none);
-                for (int i = std::max(0, issued - S::SLOTS); i < issued; ++i)
-                    tc::bar_wait(&sh.full[i % S::SLOTS], (i / S::SLOTS) & 1, &none);
+                for (int i = std::max(0, issued - S::STAGES); i < issued; ++i)
+                    tc::bar_wait(&sh.full[i % S::STAGES], i / S::STAGES & 1, &none);
             }
         } else if (warp == kIssuer) {
-            if (lane == 0 && most > 0) {
-                const uint32_t scores_of = tc::product(S::BF16, kRows, S::KEYS, false, p.negate != 0);
-                const int n16 = (p.a.head_dim + 15) / 16;
-                const uint32_t output_of = tc::product(S::BF16, kRows, 16 * n16, true, false);
-                const uint32_t q_at = tc::smem_u32(q_smem), kv_at = tc::smem_u32(kv_smem);
-                bool ok = tc::bar_wait(&sh.q_full, 0, gave_up);
-                auto wait_slot = [&](int at) { return tc::bar_wait(&sh.full[at % S::SLOTS], (at / S::SLOTS) & 1, gave_up); };
-                auto free_slot = [&](int at) { tc::commit(&sh.empty[at % S::SLOTS]); };
-                // S at column s = Q of tile t times K of tile j
-                auto scores = [&](int t, int j, uint32_t s) {
-                    const uint32_t k = kv_at + 2 * j % S::SLOTS * S::KVBYTES, q = q_at + t * S::QBYTES;
-                    for (int i = 0; i < n16; ++i)
-                        tc::mma(tmem + s, tc::operand(q + (i >> 2) * S::QHALF + (i & 3) * 32, 1024, 0),
-                                tc::operand(k + (i >> 2) * S::KHALF + (i & 3) * 32, 1024, 0), scores_of, i > 0);
-                };
-                auto output = [&](int t, int j, uint32_t s) {
-                    const uint32_t v = kv_at + (2 * j + 1) % S::SLOTS * S::KVBYTES;
-    #pragma unroll
-                    for (int i = 0; i < S::KEYS / 16; ++i)
-                        tc::mma_ts(tmem + S::O + t * S::DP, tmem + s + i * 8, tc::operand(v + i * 2048, 1024, S::KHALF), output_of,
-                                   j > 0 || i > 0);
-                };
-                auto values = [&](int j) {  // V of tile j is there, and looked over if need be
-                    return wait_slot(2 * j + 1) && (j < first_cut || tc::bar_wait(&sh.clean[j - first_cut], 0, gave_up));
-                };
-                if constexpr (S::NQ == 2) {
-                    ok = ok && wait_slot(0);
-                    if (ok) tc::fence_after();
-                    for (int t = 0; t < 2 && ok; ++t)
-                        if (tiles[t] > 0) scores(t, 0, t * S::KEYS), tc::commit(&sh.scores[t]);
-                    if (ok) free_slot(0);
-                    for (int j = 0; j < most && ok; ++j) {
-                        ok = values(j) && (j + 1 >= most || wait_slot(2 * j + 2));
-    #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (!ok || j >= tiles[t]) continue;
-                            ok = tc::bar_wait(&sh.weights[t], j & 1, gave_up);
-                            if (!ok) continue;
-                            tc::fence_after();
-                            output(t, j, t * S::KEYS);
-                            if (j + 1 < tiles[t]) scores(t, j + 1, t * S::KEYS), tc::commit(&sh.scores[t]);
-                            else tc::commit(&sh.done[t]);
-                        }
-                        if (!ok) break;
-                        free_slot(2 * j + 1);
-                        if (j + 1 < most) free_slot(2 * j + 2);
+            // the whole warp goes through this, one lane issues
+            const int rounds = tc::uniform(most), cut_from = tc::uniform(first_cut), n16 = (p.a.head_dim + 15) / 16;
+            const uint32_t to = tc::uniform(tmem);
+            const uint32_t scores_of = tc::product(S::BF16, kRows, S::KEYS, false, p.negate != 0);
+            const uint32_t output_of = tc::product(S::BF16, kRows, 16 * n16, true, false);
+            const uint32_t smem_at = tc::uniform(tc::smem_u32(smem));
+            const tc::Operand q_at = tc::operand(smem_at, 1024, 0), k_at = tc::operand(smem_at + S::NQ * S::QBYTES, 1024, 0),
+                              v_at = tc::operand(smem_at + S::NQ * S::QBYTES, 1024, S::KHALF);
+            auto wait = [&](uint64_t *bar, int parity) { return __all_sync(0xffffffffu, tc::bar_wait(bar, parity, gave_up)) != 0; };
+            auto wait_pair = [&](int i) { return wait(&sh.full[i % S::STAGES], i / S::STAGES & 1); };
+            auto clean = [&](int j) { return j < cut_from || wait(&sh.clean[j - cut_from], 0); };  // V of tile j
+            auto free_pair = [&](int i) { tc::commit(&sh.empty[i % S::STAGES]); };
+            auto wait_weights = [&](int buffer, int parity) {
+                const bool there = wait(&sh.weights[buffer], parity);
+                tc::fence_after();
+                return there;
+            };
+            // S at column s = Q of tile t times K of tile j
+            auto scores = [&](int t, int j, uint32_t s) {
+                const tc::Operand k = k_at.at(j % S::STAGES * S::STAGE), q = q_at.at(t * S::QBYTES);
+#pragma unroll
+                for (int i = 0; i < S::DP / 16; ++i)
+                    if (i < n16)
+                        tc::mma(to + s, q.at((i >> 2) * S::QHALF + (i & 3) * 32), k.at((i >> 2) * S::KHALF + (i & 3) * 32), scores_of,
+                                i > 0);
+            };
+            auto output = [&](int t, int j, uint32_t s) {
+                const tc::Operand v = v_at.at((j + 1) % S::STAGES * S::STAGE + S::KVBYTES);
+#pragma unroll
+                for (int i = 0; i < S::KEYS / 16; ++i)
+                    tc::mma_ts(to + S::O + t * S::DP, to + s + i * 8, v.at(i * 2048), output_of, i > 0 || j > 0);
+            };
+            // A wait takes this warp 150 clocks and more even where nothing is waited for, and the products in the queue
+            // last about 400: so there are two waits for weights and one for a stage in a step, each behind products.
+            bool ok = rounds == 0 || (wait(&sh.q_full, 0) && wait_pair(0));
+            if constexpr (S::NQ == 2) {
+                const int own[2] = {tc::uniform(tiles[0]), tc::uniform(tiles[1])};
+                if (ok && rounds > 0) {
+                    if (tc::elect()) {
+                        for (int t = 0; t < 2; ++t)
+                            if (own[t] > 0) scores(t, 0, t * S::KEYS), tc::commit(&sh.scores[t]);
+                        free_pair(0);
                     }
-                } else {
-                    for (int j = 0; j < 2 && j < most && ok; ++j) {
-                        ok = wait_slot(2 * j);
+                    __syncwarp();
+                }
+                for (int j = 0; j < rounds && ok; ++j) {
+                    ok = wait_pair(j + 1) && clean(j);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
                         if (!ok) break;
-                        tc::fence_after();
+                        if (j < own[t]) ok = wait_weights(t, j & 1);
+                        if (!ok) break;
+                        if (tc::elect()) {
+                            if (j < own[t]) {
+                                output(t, j, t * S::KEYS);
+                                if (j + 1 < own[t]) scores(t, j + 1, t * S::KEYS), tc::commit(&sh.scores[t]);
+                                else tc::commit(&sh.done[t]);
+                            }
+                            if (t == 1) free_pair(j + 1);
+                        }
+                        __syncwarp();
+                    }
+                }
+            } else {
+                for (int j = 0; j < 2 && j < rounds && ok; ++j) {
+                    if (j > 0) ok = wait_pair(1);
+                    if (ok && tc::elect()) {
                         scores(0, j, j * S::KEYS), tc::commit(&sh.scores[j]);
-                        free_slot(2 * j);
+                        if (j == 0) free_pair(0);
                     }
-                    for (int j = 0; j < most && ok; ++j) {
-                        ok = values(j) && tc::bar_wait(&sh.weights[j & 1], (j >> 1) & 1, gave_up);
-                        if (!ok) break;
-                        tc::fence_after();
-                        output(0, j, (j & 1) * S::KEYS);
-                        tc::commit(&sh.product[0]);
-                        free_slot(2 * j + 1);
-                        if (j + 2 < most) {
-                            ok = wait_slot(2 * j + 4);
-                            if (!ok) break;
-                            tc::fence_after();
-                            scores(0, j + 2, (j & 1) * S::KEYS), tc::commit(&sh.scores[j & 1]);
-                            free_slot(2 * j + 4);
-                        }
+                    __syncwarp();
+                }
+                for (int j = 0; j < rounds && ok; ++j) {
+                    // the scores after next, of the pair after this, follow the products of these weights in their place
+                    ok = (j > 0 || rounds > 1 || wait_pair(1)) && clean(j) && wait_weights(j & 1, j >> 1 & 1);
+                    if (!ok) break;
+                    if (tc::elect()) output(0, j, (j & 1) * S::KEYS), tc::commit(&sh.product[0]), free_pair(j + 1);
+                    __syncwarp();
+                    if (j + 2 > rounds) continue;
+                    ok = wait_pair(j + 2);
+                    if (!ok) break;
+                    if (j + 2 < rounds) {
+                        if (tc::elect()) scores(0, j + 2, (j & 1) * S::KEYS), tc::commit(&sh.scores[j & 1]);
+                        __syncwarp();
                     }
-                    if (ok) tc::commit(&sh.done[0]);
                 }
-                if (!ok) {  // no product may be under way when its memory is given back
-                    int none = 0;
-                    tc::commit(&sh.last);
-                    tc::bar_wait(&sh.last, 0, &none);
-                }
+                if (rounds > 0 && ok && tc::elect()) tc::commit(&sh.done[0]);
+                __syncwarp();
             }
-            __syncwarp();
+            if (!ok) {  // no product may be under way when its memory is given back
+                int none = 0;
+                if (tc::elect()) tc::commit(&sh.last);
+                tc::bar_wait(&sh.last, 0, &none);
+            }
         }
     } else {
         if constexpr (S::NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -368,62 +388,92 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc::fence_after();
-            float s[S::KEYS];
-#pragma unroll
-            for (int c = 0; c < S::KEYS; c += 32) tc::load32(at + c, reinterpret_cast<uint32_t *>(s + c));
-            tc::load_wait();
             const int left = seen - j * S::KEYS;  // keys that the row sees here
             const bool cut = j >= first_cut;
+            // Loops that few steps go through are not unrolled: the code of a step has to stay in the caches of
+            // instructions beside that of the warp that issues the products.
             if (cut) {
+#pragma unroll 1
+                for (int c = 0; c < S::KEYS; c += 32) {
+                    float s[32];
+                    tc::load32(at + c, reinterpret_cast<uint32_t *>(s));
+                    tc::load32_wait(reinterpret_cast<uint32_t *>(s));
 #pragma unroll
-                for (int c = 0; c < S::KEYS; ++c)
-                    if (c >= left) s[c] = -INFINITY;
+                    for (int i = 0; i < 32; ++i)
+                        if (c + i >= left) s[i] = -INFINITY;
+                    tc::store32(at + c, reinterpret_cast<uint32_t *>(s));
+                }
+                tc::store_wait();
             }
-            float top[4] = {s[0], s[1], s[2], s[3]};
+            // The weights are taken relative to the maximum so far, and the row's own is looked for only where one of
+            // them comes out too large, or nothing was seen before.
+            bool search = __any_sync(0xffffffffu, real && m == -INFINITY);
+            uint32_t weights[S::KEYS / 2];
+            float sum;
+            for (;;) {
+                if (search) {
+                    float high = m;
+#pragma unroll 1
+                    for (int c = 0; c < S::KEYS; c += 32) {
+                        float s[32];
+                        tc::load32(at + c, reinterpret_cast<uint32_t *>(s));
+                        tc::load32_wait(reinterpret_cast<uint32_t *>(s));
 #pragma unroll
-            for (int c = 4; c < S::KEYS; c += 4) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], s[c + i]);
-            }
-            const float high = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
-            const bool raise = real && (high - m) * p.scale2 > S::RAISE;
-            if (__any_sync(0xffffffffu, raise)) {
-                const float keep = raise ? (m == -INFINITY ? 0.0f : pow2((m - high) * p.scale2)) : 1.0f;
-                if (raise) m = high;
-                l *= keep;
-                if (j > 0) {
-                    if constexpr (S::NQ == 1) {  // with two tiles the barrier of S says it
-                        ok = tc::bar_wait(&sh.product[0], (j - 1) & 1, gave_up);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        tc::fence_after();
+                        for (int i = 0; i < 32; ++i) high = fmaxf(high, s[i]);
                     }
-                    const uint32_t o_at = lanes + S::O + t * S::DP;
-                    for (int c = 0; c < p.a.head_dim; c += 32) {
-                        uint32_t o[32];
-                        tc::load32(o_at + c, o);
-                        tc::load_wait();
+                    const bool raise = real && (high - m) * p.scale2 > S::RAISE;
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float keep = raise ? (m == -INFINITY ? 0.0f : pow2((m - high) * p.scale2)) : 1.0f;
+                        if (raise) m = high;
+                        l *= keep;
+                        if (j > 0) {
+                            if constexpr (S::NQ == 1) {  // with two tiles the barrier of S says it
+                                ok = tc::bar_wait(&sh.product[0], (j - 1) & 1, gave_up);
+                                ok = __all_sync(0xffffffffu, ok);
+                                if (!ok) break;
+                                tc::fence_after();
+                            }
+                            const uint32_t o_at = lanes + S::O + t * S::DP;
+#pragma unroll 1
+                            for (int c = 0; c < p.a.head_dim; c += 32) {
+                                uint32_t o[32];
+                                tc::load32(o_at + c, o);
+                                tc::load32_wait(o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                        tc::store32(o_at + c, o);
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                                tc::store32(o_at + c, o);
+                            }
+                        }
                     }
                 }
-            }
-            const float base = m == -INFINITY ? 0.0f : m;
-            const uint64_t minus = tc::pair(-base, -base), by = tc::pair(p.scale2, p.scale2), lift = tc::pair(S::LIFT, S::LIFT);
-            uint64_t sum[2] = {0, 0};
-            uint32_t weights[S::KEYS / 2];
+                const float base = m == -INFINITY ? 0.0f : m;
+                const uint64_t minus = tc::pair(-base, -base), by = tc::pair(p.scale2, p.scale2), lift = tc::pair(S::LIFT, S::LIFT);
+                uint64_t sums[2] = {0, 0};
+                float top = 0.0f, s[2][32];
+                tc::load32(at, reinterpret_cast<uint32_t *>(s[0]));
 #pragma unroll
-            for (int c = 0; c < S::KEYS; c += 2) {
-                float x, y;
-                tc::unpair(tc::fma2(tc::add2(tc::pair(s[c], s[c + 1]), minus), by, lift), x, y);
-                x = pow2(x), y = pow2(y);
-                sum[c / 2 % 2] = tc::add2(sum[c / 2 % 2], tc::pair(x, y));
-                weights[c / 2] = pack<T>(x, y);
+                for (int c = 0; c < S::KEYS; c += 32) {
+                    float *x = s[c / 32 % 2];
+                    tc::load32_wait(reinterpret_cast<uint32_t *>(x));
+                    if (c + 32 < S::KEYS) tc::load32(at + c + 32, reinterpret_cast<uint32_t *>(s[(c / 32 + 1) % 2]));
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float a, b;
+                        tc::unpair(tc::fma2(tc::add2(tc::pair(x[i], x[i + 1]), minus), by, lift), a, b);
+                        a = pow2(a), b = pow2(b);
+                        top = fmaxf(top, fmaxf(a, b));
+                        sums[i / 2 % 2] = tc::add2(sums[i / 2 % 2], tc::pair(a, b));
+                        weights[(c + i) / 2] = pack<T>(a, b);
+                    }
+                }
+                float a, b;
+                tc::unpair(tc::add2(sums[0], sums[1]), a, b);
+                sum = a + b;
+                if (search || !__any_sync(0xffffffffu, real && top > S::LIMIT)) break;
+                search = true;
             }
-            float a, b;
-            tc::unpair(tc::add2(sum[0], sum[1]), a, b);
-            l += a + b;
+            if (!ok) break;
+            l += sum;
 #pragma unroll
             for (int c = 0; c < S::KEYS / 2; c += 32) tc::store32(at + c, weights + c);
             tc::store_wait();
@@ -445,7 +495,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 uint32_t o[32];
                 if (n > 0) {
                     tc::load32(lanes + S::O + t * S::DP + c, o);
-                    tc::load_wait();
+                    tc::load32_wait(o);
                 }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = n > 0 ? __float_as_uint(__uint_as_float(o[i]) * inverse) : 0u;

@@ -13,6 +13,17 @@ namespace tc {
 
 using tma::smem_u32;
 
+// One lane of a whole warp.  What it issues takes its operands from the warp's
+// uniform registers, so they are computed by the whole warp, from values that
+// the compiler can see to be the same on every lane (uniform() makes one).
+__device__ __forceinline__ bool elect() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+template <typename T>
+__device__ __forceinline__ T uniform(T v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // ---------------------------------------------------------------- barriers
 __device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t arrivals) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(arrivals) : "memory");
@@ -73,7 +84,16 @@ __device__ __forceinline__ void load32(uint32_t tmem, uint32_t *r) {
           "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(tmem));
 }
-__device__ __forceinline__ void load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the loads issued so far; what they gave (r) is not used before.
+__device__ __forceinline__ void load32_wait(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+          "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+          "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]),
+          "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+        :
+        : "memory");
+}
 __device__ __forceinline__ void store32(uint32_t tmem, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
@@ -92,9 +112,14 @@ __device__ __forceinline__ void store_wait() { asm volatile("tcgen05.wait::st.sy
 //   rows along the product's K (K-major): `eights` bytes from eight rows to the next eight; `lead` unused;
 //   rows along M or N (MN-major): a row holds 64 of these; `eights` bytes from eight k to the next eight, `lead`
 //   bytes from 64 of M or N to the next 64.
-__device__ __forceinline__ uint64_t operand(uint32_t smem, uint32_t eights, uint32_t lead) {
-    return (uint64_t)(smem >> 4 & 0x3fff) | (uint64_t)(lead >> 4 & 0x3fff) << 16 | (uint64_t)(eights >> 4 & 0x3fff) << 32 |
-           1ull << 46 | 2ull << 61;
+// Its address is in the low word, in units of 16 bytes: another place in shared
+// memory is a 32-bit addition away.
+struct Operand {
+    uint32_t low, high;
+    __device__ __forceinline__ Operand at(uint32_t bytes) const { return {low + (bytes >> 4), high}; }
+};
+__device__ __forceinline__ Operand operand(uint32_t smem, uint32_t eights, uint32_t lead) {
+    return {(smem >> 4 & 0x3fff) | (lead >> 4 & 0x3fff) << 16, (eights >> 4 & 0x3fff) | 1u << 14 | 2u << 29};
 }
 // kind::f16 with 32-bit sums: bf16 or f16 operands, m x n, B's rows along N; A negated.
 __host__ __device__ constexpr uint32_t product(bool bf16, int m, int n, bool b_mn_major, bool negate_a) {
@@ -102,19 +127,19 @@ __host__ __device__ constexpr uint32_t product(bool bf16, int m, int n, bool b_m
            (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
 // d (+)= A B, 16 of K; by one thread, in the order of issue
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add) {
+__device__ __forceinline__ void mma(uint32_t d, Operand a, Operand b, uint32_t what, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a.low), "r"(a.high), "r"(b.low), "r"(b.high), "r"(what), "r"((uint32_t)add)
         : "memory");
 }
 // A from tensor memory: two 16-bit elements a column
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Operand b, uint32_t what, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b.low), "r"(b.high), "r"(what), "r"((uint32_t)add)
         : "memory");
 }
 // arrives on the barrier when everything this thread issued so far is done
@@ -139,11 +164,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
