@@ -51,7 +51,6 @@ enum { kBadQueries = 1, kBadKeys = 2, kGaveUp = 4 };
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 128;
-constexpr int kCut = 4;  // tiles of keys that a block's rows see in part: its tokens span at most two tiles
 
 // DP: the head's elements rounded up to 64; NQ: tiles of a block.
 template <typename T_, int DP_, int NQ_>
@@ -149,7 +148,7 @@ __device__ __forceinline__ bool find_work(const PromptArgs &p, int block, Work *
 
 template <class S>
 struct Shared {
-    uint64_t q_full, full[S::STAGES], empty[S::STAGES], scores[2], weights[2], clean[kCut], product[S::NQ], done[S::NQ], last;
+    uint64_t q_full, full[S::STAGES], empty[S::STAGES], scores[2], weights[2], product[S::NQ], done[S::NQ], last;
     uint32_t tmem;
     int gave_up, not_finite, found, warp_sums[S::THREADS / 32];
     Work work;
@@ -186,10 +185,9 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     if (threadIdx.x == 0) {
         tc::bar_init(&sh.q_full, 1);
         for (int i = 0; i < S::STAGES; ++i) tc::bar_init(&sh.full[i], 1), tc::bar_init(&sh.empty[i], 1);
-        for (int i = 0; i < 2; ++i) tc::bar_init(&sh.scores[i], 1), tc::bar_init(&sh.weights[i], 128);
+        for (int i = 0; i < 2; ++i) tc::bar_init(&sh.scores[i], 1), tc::bar_init(&sh.weights[i], 129);
         for (int i = 0; i < S::NQ; ++i) tc::bar_init(&sh.product[i], 1), tc::bar_init(&sh.done[i], 1);
         tc::bar_init(&sh.last, 1);
-        for (int i = 0; i < kCut; ++i) tc::bar_init(&sh.clean[i], 1);
         sh.gave_up = sh.not_finite = 0;
         tc::bar_init_done();
     }
@@ -218,8 +216,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             // pair i: K of tile i, if there is one, and V of the tile before
             auto load = [&](int i) {
                 const int stage = i % S::STAGES, round = i / S::STAGES;
-                if (round > 0) ok = tc::bar_wait(&sh.empty[stage], (round - 1) & 1, gave_up);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = round == 0 || tc::bar_wait(&sh.empty[stage], (round - 1) & 1, gave_up);
                 if (!ok) return;
                 if (lane == 0) {
                     tma::mbar_expect_tx(&sh.full[stage], ((i < most) + (i > 0)) * S::KVBYTES);
@@ -231,18 +228,13 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 }
                 ++issued;
             };
-            // looks the values of tile j over
-            auto look_over = [&](int j) {
-                if (j < first_cut) return;
-                const int stage = (j + 1) % S::STAGES;
-                ok = tc::bar_wait(&sh.full[stage], (j + 1) / S::STAGES & 1, gave_up);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) return;
+            // puts zeros in the place of what is not finite among a stage's values
+            auto look_over = [&](int stage) {
                 constexpr uint32_t EXPONENT = S::BF16 ? 0x7f807f80u : 0x7c007c00u, UNIT = S::BF16 ? 0x00800080u : 0x04000400u;
                 uint4 *v = reinterpret_cast<uint4 *>(kv_smem + stage * S::STAGE + S::KVBYTES);
                 auto bad = [&](uint32_t x) { return ((x & EXPONENT) + UNIT) & 0x80008000u; };  // its halves that are not finite
                 uint32_t any = 0;
-    #pragma unroll 8
+#pragma unroll 8
                 for (int i = lane; i < S::KVBYTES / 16; i += 32) {
                     const uint4 x = v[i];
                     any |= bad(x.x) | bad(x.y) | bad(x.z) | bad(x.w);
@@ -260,36 +252,46 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     tc::shared_to_async();
                 }
                 __syncwarp();
-                if (lane == 0) tc::bar_arrive(&sh.clean[j - first_cut]);
             };
-            // values are looked over once the next load is under way: what frees its stage does not wait for them
-            for (int i = 0; i <= most && most > 0 && ok; ++i) {
-                load(i);
-                if (ok && i > 1) look_over(i - 2);
+            // Tells the issuer, with the weights of step j, that what the step takes is there: V of tile j, looked over
+            // if need be, and the keys behind it.
+            auto announce = [&](int j) {
+                const int last = S::NQ == 2 ? j + 1 : min(j + 2, most), stage = (j + 1) % S::STAGES;
+                for (int i = j + 1; i <= last && ok; ++i) ok = tc::bar_wait(&sh.full[i % S::STAGES], i / S::STAGES & 1, gave_up);
+                if (ok && j >= first_cut) look_over(stage);
+                for (int b = 0; b < 2 && ok; ++b) {  // once a phase: the one before has to be over
+                    if (S::NQ == 2 ? j >= tiles[b % S::NQ] : b != (j & 1)) continue;
+                    if (j >= 3 - S::NQ) ok = tc::bar_wait(&sh.weights[b], (S::NQ == 2 ? j - 1 : (j >> 1) - 1) & 1, gave_up);
+                    if (ok && lane == 0) tc::bar_arrive(&sh.weights[b]);
+                }
+            };
+            if (most > 0) load(0);
+            for (int j = 0; j < most && ok; ++j) {
+                load(j + 1);
+                if (S::NQ == 1 && ok && j > 0) announce(j - 1);
+                if (S::NQ == 2 && ok) announce(j);
             }
-            if (ok && most > 0) look_over(most - 1);
+            if (S::NQ == 1 && ok && most > 0) announce(most - 1);
             // nothing may be on its way into shared memory when the block ends
             if (!ok) {
-                int none = 0;
-                if (most > 0) tc::bar_wait(&sh.q_full, 0, &none);
+                if (most > 0) tc::bar_wait(&sh.q_full, 0, nullptr);
                 for (int i = std::max(0, issued - S::STAGES); i < issued; ++i)
-                    tc::bar_wait(&sh.full[i % S::STAGES], i / S::STAGES & 1, &none);
+                    tc::bar_wait(&sh.full[i % S::STAGES], i / S::STAGES & 1, nullptr);
             }
         } else if (warp == kIssuer) {
             // the whole warp goes through this, one lane issues
-            const int rounds = tc::uniform(most), cut_from = tc::uniform(first_cut), n16 = (p.a.head_dim + 15) / 16;
+            const int rounds = tc::uniform(most), n16 = (p.a.head_dim + 15) / 16;
             const uint32_t to = tc::uniform(tmem);
             const uint32_t scores_of = tc::product(S::BF16, kRows, S::KEYS, false, p.negate != 0);
             const uint32_t output_of = tc::product(S::BF16, kRows, 16 * n16, true, false);
             const uint32_t smem_at = tc::uniform(tc::smem_u32(smem));
             const tc::Operand q_at = tc::operand(smem_at, 1024, 0), k_at = tc::operand(smem_at + S::NQ * S::QBYTES, 1024, 0),
                               v_at = tc::operand(smem_at + S::NQ * S::QBYTES, 1024, S::KHALF);
-            auto wait = [&](uint64_t *bar, int parity) { return __all_sync(0xffffffffu, tc::bar_wait(bar, parity, gave_up)) != 0; };
-            auto wait_pair = [&](int i) { return wait(&sh.full[i % S::STAGES], i / S::STAGES & 1); };
-            auto clean = [&](int j) { return j < cut_from || wait(&sh.clean[j - cut_from], 0); };  // V of tile j
+            auto wait_pair = [&](int i) { return tc::bar_wait(&sh.full[i % S::STAGES], i / S::STAGES & 1, gave_up); };
             auto free_pair = [&](int i) { tc::commit(&sh.empty[i % S::STAGES]); };
+            // the weights, and all that their step takes
             auto wait_weights = [&](int buffer, int parity) {
-                const bool there = wait(&sh.weights[buffer], parity);
+                const bool there = tc::bar_wait(&sh.weights[buffer], parity, gave_up);
                 tc::fence_after();
                 return there;
             };
@@ -308,9 +310,9 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 for (int i = 0; i < S::KEYS / 16; ++i)
                     tc::mma_ts(to + S::O + t * S::DP, to + s + i * 8, v.at(i * 2048), output_of, i > 0 || j > 0);
             };
-            // A wait takes this warp 150 clocks and more even where nothing is waited for, and the products in the queue
-            // last about 400: so there are two waits for weights and one for a stage in a step, each behind products.
-            bool ok = rounds == 0 || (wait(&sh.q_full, 0) && wait_pair(0));
+            // The queue of products is short, and every wait takes this warp 150 clocks and more even where nothing is waited
+            // for: it waits once a tile and step.
+            bool ok = rounds == 0 || (tc::bar_wait(&sh.q_full, 0, gave_up) && wait_pair(0));
             if constexpr (S::NQ == 2) {
                 const int own[2] = {tc::uniform(tiles[0]), tc::uniform(tiles[1])};
                 if (ok && rounds > 0) {
@@ -322,10 +324,8 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     __syncwarp();
                 }
                 for (int j = 0; j < rounds && ok; ++j) {
-                    ok = wait_pair(j + 1) && clean(j);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        if (!ok) break;
                         if (j < own[t]) ok = wait_weights(t, j & 1);
                         if (!ok) break;
                         if (tc::elect()) {
@@ -349,26 +349,21 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     __syncwarp();
                 }
                 for (int j = 0; j < rounds && ok; ++j) {
-                    // the scores after next, of the pair after this, follow the products of these weights in their place
-                    ok = (j > 0 || rounds > 1 || wait_pair(1)) && clean(j) && wait_weights(j & 1, j >> 1 & 1);
+                    ok = wait_weights(j & 1, j >> 1 & 1);
                     if (!ok) break;
-                    if (tc::elect()) output(0, j, (j & 1) * S::KEYS), tc::commit(&sh.product[0]), free_pair(j + 1);
-                    __syncwarp();
-                    if (j + 2 > rounds) continue;
-                    ok = wait_pair(j + 2);
-                    if (!ok) break;
-                    if (j + 2 < rounds) {
-                        if (tc::elect()) scores(0, j + 2, (j & 1) * S::KEYS), tc::commit(&sh.scores[j & 1]);
-                        __syncwarp();
+                    if (tc::elect()) {
+                        output(0, j, (j & 1) * S::KEYS), tc::commit(&sh.product[0]), free_pair(j + 1);
+                        if (j + 2 < rounds) scores(0, j + 2, (j & 1) * S::KEYS), tc::commit(&sh.scores[j & 1]);
                     }
+                    __syncwarp();
                 }
                 if (rounds > 0 && ok && tc::elect()) tc::commit(&sh.done[0]);
                 __syncwarp();
             }
             if (!ok) {  // no product may be under way when its memory is given back
-                int none = 0;
                 if (tc::elect()) tc::commit(&sh.last);
-                tc::bar_wait(&sh.last, 0, &none);
+                __syncwarp();
+                tc::bar_wait(&sh.last, 0, nullptr);
             }
         }
     } else {
@@ -385,7 +380,6 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             const int buffer = S::NQ == 2 ? t : j & 1;
             const uint32_t at = lanes + buffer * S::KEYS;
             ok = tc::bar_wait(&sh.scores[buffer], S::NQ == 2 ? j & 1 : (j >> 1) & 1, gave_up);
-            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc::fence_after();
             const int left = seen - j * S::KEYS;  // keys that the row sees here
@@ -429,7 +423,6 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                         if (j > 0) {
                             if constexpr (S::NQ == 1) {  // with two tiles the barrier of S says it
                                 ok = tc::bar_wait(&sh.product[0], (j - 1) & 1, gave_up);
-                                ok = __all_sync(0xffffffffu, ok);
                                 if (!ok) break;
                                 tc::fence_after();
                             }
@@ -482,10 +475,9 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         }
         if (n > 0 && ok) {
             ok = tc::bar_wait(&sh.done[t], 0, gave_up);
-            ok = __all_sync(0xffffffffu, ok);
             tc::fence_after();
-            if (first_cut < most) ok = ok && tc::bar_wait(&sh.clean[most - first_cut - 1], 0, gave_up);  // not_finite
-            ok = __all_sync(0xffffffffu, ok);
+            // over long since; what the loading warp noted before it arrived here is read below
+            ok = ok && tc::bar_wait(&sh.weights[S::NQ == 2 ? t : (n - 1) & 1], (S::NQ == 2 ? n - 1 : (n - 1) >> 1) & 1, gave_up);
         }
         if (ok && w.t0 + t * p.tile_tokens < w.nq) {
             T *out = static_cast<T *>(p.a.out) + (int64_t)(w.q0 + token) * p.a.out_stride[0] + head * p.a.out_stride[1];
