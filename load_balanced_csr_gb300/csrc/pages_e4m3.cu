@@ -67,17 +67,27 @@ struct Raw {
     __device__ __forceinline__ float operator[](int i) const { return to_float(part[i / N].v[i % N]); }
 };
 
-__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
-
-// the bits of the largest finite |x|, at least `so_far`
+// What the first pass over some elements finds: the bits of the largest finite |x|, and whether one is not finite.
+struct Size {
+    uint32_t bits;
+    bool odd;
+};
 template <typename T, int V>
-__device__ __forceinline__ uint32_t largest(const Raw<T, V> &x, uint32_t so_far) {
+__device__ __forceinline__ void look(const Raw<T, V> &x, Size &s) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const uint32_t bits = __float_as_uint(x[i]) & 0x7fffffffu;
-        so_far = max(so_far, bits < 0x7f800000u ? bits : 0u);
+        if (bits < 0x7f800000u) s.bits = max(s.bits, bits);
+        else s.odd = true;
     }
-    return so_far;
+}
+// 16-bit elements in pairs: their bits without the sign are in the order of their sizes
+template <typename T>
+__device__ __forceinline__ void look_pairs(const Raw<T, 8> &x, uint32_t &top) {
+    static_assert(sizeof(T) == 2, "");
+    uint4 w;
+    memcpy(&w, &x, 16);
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
 }
 // the least power of two p >= 2^-126 with size <= 448 p = 1.75 * 2^8 p
 __device__ __forceinline__ float scale_for(uint32_t size_bits) {
@@ -87,17 +97,17 @@ __device__ __forceinline__ float scale_for(uint32_t size_bits) {
 // x / scale; a power of two's reciprocal is exact, and a NaN stands for what is not finite
 struct Divide {
     float scale, inverse;
-    bool exact;
+    bool exact, odd;  // odd: there may be values that are not finite
     __device__ __forceinline__ float operator()(float x) const {
         const float q = exact ? x * inverse : x / scale;
-        return finite(x) ? q : __int_as_float(0x7fffffff);
+        return !odd || (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u ? q : __int_as_float(0x7fffffff);
     }
 };
-__device__ __forceinline__ Divide divide_by(float scale) {
-    return {scale, 1.0f / scale, (__float_as_uint(scale) & 0x7fffffu) == 0 && scale <= __uint_as_float(253u << 23)};
+__device__ __forceinline__ Divide divide_by(float scale, bool odd) {
+    return {scale, 1.0f / scale, (__float_as_uint(scale) & 0x7fffffu) == 0 && scale <= __uint_as_float(253u << 23), odd};
 }
 template <typename T, int V>
-__device__ __forceinline__ void write_codes(unsigned char *to, const Raw<T, V> &x, const Divide &by) {
+__device__ __forceinline__ void write_codes_by(unsigned char *to, const Raw<T, V> &x, const Divide &by) {
     if constexpr (V == 1) {
         *to = (unsigned char)to_e4m3x2(by(x[0]), 0.0f);
     } else {
@@ -106,6 +116,15 @@ __device__ __forceinline__ void write_codes(unsigned char *to, const Raw<T, V> &
         c.x = to_e4m3x2(by(x[0]), by(x[1])) | to_e4m3x2(by(x[2]), by(x[3])) << 16;
         c.y = to_e4m3x2(by(x[4]), by(x[5])) | to_e4m3x2(by(x[6]), by(x[7])) << 16;
         *reinterpret_cast<uint2 *>(to) = c;
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void write_codes(unsigned char *to, const Raw<T, V> &x, const Divide &by) {
+    if (by.exact && !by.odd) {  // nearly always
+        const Divide plain = {by.scale, by.inverse, true, false};
+        write_codes_by(to, x, plain);
+    } else {
+        write_codes_by(to, x, by);
     }
 }
 template <int V>
@@ -124,47 +143,74 @@ __device__ __forceinline__ void rescale_codes(unsigned char *at, float by) {
 }
 
 // ---------------------------------------------------------------- store, blocks of tokens
+// A run of a tile: its tokens are entries first .. first + count - 1 of the tile's list.
+struct Run {
+    int32_t block, first, count;
+};
+constexpr int kListed = kMaxTile + kMaxBlock;  // the tile's tokens, and those behind it of its last run
+
 // L lanes take a row, 32 / L rows go at once; HELD batches of these stay in
 // registers between the two passes.
 template <typename T, int V, int L>
-__global__ void __launch_bounds__(kCodeThreads) paged_store_blocks_kernel(StoreCodesArgs a) {
-    constexpr int G = 32 / L, HELD = sizeof(T) == 4 ? 4 : 8;
-    __shared__ int32_t first_of[kMaxTile];                 // the tile's runs: their first tokens
+__global__ void __launch_bounds__(kCodeThreads, 4) paged_store_blocks_kernel(StoreCodesArgs a) {
+    constexpr int G = 32 / L, HELD = sizeof(T) == 4 ? 2 : 8;
+    __shared__ Run runs[kMaxTile];
     __shared__ int num_runs;
-    __shared__ int32_t token_of[kCodeWarps][kMaxBlock];    // a run's tokens
-    __shared__ uint8_t place_of[kCodeWarps][kMaxBlock];    // their places in the block
+    __shared__ int32_t token_of[kListed];
+    __shared__ uint8_t place_of[kListed];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     after_previous();
     const uint32_t cache_slots = (uint32_t)a.num_pages * (uint32_t)a.page;
-    // the block of tokens that token i goes to, or none
-    auto block_of = [&](int64_t i) {
-        if (i < 0 || i >= a.tokens) return -1;
-        const int32_t s = a.slots[i];
-        return (uint32_t)s < cache_slots ? (int32_t)over((uint32_t)s, a.block_mul, a.block_shift) : -1;
-    };
     const int64_t t0 = (int64_t)(blockIdx.x / a.slices) * a.tile;
     const int slice = blockIdx.x % a.slices;
     if (warp == 0) {
+        // a token's slot and the block of tokens that it goes to, or -1
+        auto read = [&](int64_t i, int32_t &slot) {
+            slot = i >= 0 && i < a.tokens ? a.slots[i] : -1;
+            return (uint32_t)slot < cache_slots ? (int32_t)over((uint32_t)slot, a.block_mul, a.block_shift) : -1;
+        };
         int before = -1;  // of the last token before these that goes anywhere
         int64_t before_at = 0;
+        int32_t slot;
         for (int64_t i = t0 - 1; i >= t0 - kMaxGap && before < 0; i -= 32) {
-            const int b = block_of(i - lane);
+            const int b = read(i - lane, slot);
             const uint32_t any = __ballot_sync(0xffffffffu, b >= 0);
             if (any) before = __shfl_sync(0xffffffffu, b, __ffs(any) - 1), before_at = i - (__ffs(any) - 1);
         }
-        int n = 0;
-        for (int j = 0; j < a.tile; j += 32) {
-            const int64_t i = t0 + j + lane;
-            const int b = j + lane < a.tile ? block_of(i) : -1;
-            const uint32_t there = __ballot_sync(0xffffffffu, b >= 0), under = there & ((1u << lane) - 1);
+        int n = 0, listed = 0;  // runs; tokens of them
+        const uint32_t under_me = (1u << lane) - 1;
+        for (int64_t i0 = t0;; i0 += 32) {
+            const bool inside = i0 < t0 + a.tile;  // behind the tile: the last run's tokens alone
+            const int64_t i = i0 + lane;
+            const int b = inside && i >= t0 + a.tile ? -1 : read(i, slot);
+            const uint32_t there = __ballot_sync(0xffffffffu, b >= 0), under = there & under_me;
             const int last = __shfl_sync(0xffffffffu, b, under ? 31 - __clz(under) : 0);
             const bool opens = b >= 0 && (under ? b != last : b != before || i - before_at > kMaxGap);
-            const uint32_t all = __ballot_sync(0xffffffffu, opens);
-            if (opens) first_of[n + __popc(all & ((1u << lane) - 1))] = (int32_t)i;
-            n += __popc(all);
-            const int top = __shfl_sync(0xffffffffu, b, there ? 31 - __clz(there) : 0);
-            if (there) before = top, before_at = t0 + j + 31 - __clz(there);
+            uint32_t opened = __ballot_sync(0xffffffffu, opens), mine = there;
+            if (!inside) {
+                if (n == 0) break;
+                mine &= opened ? (1u << (__ffs(opened) - 1)) - 1 : 0xffffffffu;
+            } else if (n == 0) {  // tokens before the first run are of the tile's before
+                mine &= opened ? ~((1u << (__ffs(opened) - 1)) - 1) : 0u;
+            }
+            const int at = listed + __popc(mine & under_me);
+            if ((mine >> lane & 1) && at < kListed) {  // slots that tokens share could be more
+                token_of[at] = (int32_t)i, place_of[at] = (uint8_t)(slot - b * a.block);
+                if (inside && opens) runs[n + __popc(opened & under_me)] = Run{b, at, 0};
+            }
+            if (inside) n += __popc(opened);
+            listed = min(listed + __popc(mine), kListed);
+            if (!inside && (opened || (there ? false : i0 + 31 - before_at >= kMaxGap) || i0 + 32 >= a.tokens || listed == kListed)) break;
+            if (there) {
+                before = __shfl_sync(0xffffffffu, b, 31 - __clz(there));
+                before_at = i0 + 31 - __clz(there);
+            } else if (inside && i0 + 32 >= t0 + a.tile && i0 + 31 - before_at >= kMaxGap) {
+                break;
+            }
+            if (i0 + 32 >= a.tokens) break;
         }
+        __syncwarp();
+        for (int r = lane; r < n; r += 32) runs[r].count = min((r + 1 < n ? runs[r + 1].first : listed) - runs[r].first, a.block);
         if (lane == 0) num_runs = n;
     }
     __syncthreads();
@@ -172,41 +218,17 @@ __global__ void __launch_bounds__(kCodeThreads) paged_store_blocks_kernel(StoreC
     const bool one = vecs <= L;  // a row is one vector a lane
     const int tasks = num_runs * 2 * a.heads;
     for (int task = slice * kCodeWarps + warp; task < tasks; task += a.slices * kCodeWarps) {
-        const int run = task / (2 * a.heads), rest = task - run * 2 * a.heads, head = rest >> 1;
-        const Side &side = a.side[rest & 1];
-        // the run: tokens of one block, skipped ones left out
-        const int64_t i0 = first_of[run];
-        const int mine = block_of(i0);
-        int n = 0;
-        int64_t last_at = i0;
-        uint32_t low = 0, high = 0;  // the places written
-        for (int64_t i = i0; i < a.tokens && n < a.block; i += 32) {
-            const int b = block_of(i + lane);
-            const uint32_t there = __ballot_sync(0xffffffffu, b >= 0);
-            if (there ? i + __ffs(there) - 1 - last_at > kMaxGap : i + 31 - last_at >= kMaxGap) break;
-            const uint32_t others = __ballot_sync(0xffffffffu, b >= 0 && b != mine);
-            const uint32_t until = others ? (1u << (__ffs(others) - 1)) - 1 : 0xffffffffu;
-            const bool in = b == mine && ((until >> lane) & 1);
-            const uint32_t all = __ballot_sync(0xffffffffu, in);
-            const int at = n + __popc(all & ((1u << lane) - 1));
-            if (in && at < a.block) {  // tokens that share a slot could be more
-                const int place = a.slots[i + lane] - mine * a.block;
-                token_of[warp][at] = (int32_t)(i + lane), place_of[warp][at] = (uint8_t)place;
-                if (place < 32) low |= 1u << place;
-                else high |= 1u << (place - 32);
-            }
-            n = min(n + __popc(all), a.block);
-            if (others) break;
-            if (there) last_at = i + 31 - __clz(there);
-        }
-        low = __reduce_or_sync(0xffffffffu, low), high = __reduce_or_sync(0xffffffffu, high);
-        __syncwarp();
-        const uint32_t slot0 = (uint32_t)mine * a.block, page = over(slot0, a.page_mul, a.page_shift), in0 = slot0 - page * a.page;
+        const int of = (int)over((uint32_t)task >> 1, a.heads_mul, a.heads_shift), head = (task >> 1) - of * a.heads;
+        const Side &side = a.side[task & 1];
+        const Run run = runs[of];
+        const int n = run.count;
+        const uint32_t slot0 = (uint32_t)run.block * a.block, page = over(slot0, a.page_mul, a.page_shift), in0 = slot0 - page * a.page;
         float *scale = side.scales + page * side.ss[0] + over(in0, a.block_mul, a.block_shift) * side.ss[1] + head * side.ss[2];
         unsigned char *codes = side.codes + page * side.cs[0] + (int64_t)in0 * side.cs[1] + head * side.cs[2];
         const T *x = static_cast<const T *>(side.x) + head * side.xs[1];
         const float old = *scale;
-        uint32_t size = 0;
+        Size size = {0, false};
+        uint32_t pairs = 0;
         Raw<T, V> held[HELD];
         for (int r = 0; r < n; r += HELD * G) {
             for (int c = col; c < vecs || c == col; c += L) {  // once where a row is one vector a lane
@@ -214,28 +236,60 @@ __global__ void __launch_bounds__(kCodeThreads) paged_store_blocks_kernel(StoreC
                 for (int u = 0; u < HELD; ++u) {
                     const int row = r + u * G + sub;
                     held[u].clear();
-                    if (row < n && c < vecs) held[u].read(x + token_of[warp][row] * side.xs[0] + c * V);
+                    if (row < n && c < vecs) held[u].read(x + token_of[run.first + row] * side.xs[0] + c * V);
                 }
 #pragma unroll
-                for (int u = 0; u < HELD; ++u) size = largest(held[u], size);
+                for (int u = 0; u < HELD; ++u) {
+                    if constexpr (sizeof(T) == 2 && V == 8) look_pairs(held[u], pairs);
+                    else look(held[u], size);
+                }
             }
         }
-        size = __reduce_max_sync(0xffffffffu, size);
+        if constexpr (sizeof(T) == 2 && V == 8) {
+            pairs = __vmaxu2(pairs, pairs >> 16) & 0xffffu;
+            pairs = __reduce_max_sync(0xffffffffu, pairs);
+            T top;
+            const uint16_t bits = (uint16_t)pairs;
+            memcpy(&top, &bits, 2);
+            size.bits = __float_as_uint(to_float(top));
+            if (size.bits >= 0x7f800000u) {  // one of them is not finite: once more, leaving such out
+                size = {0, true};
+                for (int r = sub; r < n; r += G)
+                    for (int c = col; c < vecs; c += L) {
+                        Raw<T, V> again;
+                        again.read(x + token_of[run.first + r] * side.xs[0] + c * V);
+                        look(again, size);
+                    }
+                size.odd = true;
+                size.bits = __reduce_max_sync(0xffffffffu, size.bits);
+            }
+        } else {
+            size.bits = __reduce_max_sync(0xffffffffu, size.bits);
+            size.odd = __any_sync(0xffffffffu, size.odd);
+        }
+        uint32_t low = 0, high = 0;  // the places written
+        for (int r = lane; r < n; r += 32) {
+            const int place = place_of[run.first + r];
+            if (place < 32) low |= 1u << place;
+            else high |= 1u << (place - 32);
+        }
+        low = __reduce_or_sync(0xffffffffu, low);
         const bool begun = low & 1;
-        const float need = scale_for(size), now = begun ? need : fmaxf(old, need);
-        const Divide by = divide_by(now);
+        const float need = scale_for(size.bits), now = begun ? need : fmaxf(old, need);
+        const Divide by = divide_by(now, size.odd);
         for (int r = 0; r < n; r += HELD * G) {
             for (int c = col; c < vecs; c += L) {
 #pragma unroll
                 for (int u = 0; u < HELD; ++u) {
                     const int row = r + u * G + sub;
                     if (row >= n) continue;
-                    if (!(one && n <= HELD * G)) held[u].read(x + token_of[warp][row] * side.xs[0] + c * V);
-                    write_codes(codes + place_of[warp][row] * side.cs[1] + c * V, held[u], by);
+                    if (!(one && n <= HELD * G)) held[u].read(x + token_of[run.first + row] * side.xs[0] + c * V);
+                    write_codes(codes + place_of[run.first + row] * side.cs[1] + c * V, held[u], by);
                 }
             }
         }
         if (!begun && now > old) {
+            high = __reduce_or_sync(0xffffffffu, high);
             const float ratio = old / now;
             for (int r = sub; r < a.block; r += G) {
                 if (((r < 32 ? low >> r : high >> (r - 32)) & 1)) continue;
@@ -243,7 +297,6 @@ __global__ void __launch_bounds__(kCodeThreads) paged_store_blocks_kernel(StoreC
             }
         }
         if (lane == 0) *scale = now;
-        __syncwarp();
     }
 }
 
@@ -258,7 +311,7 @@ __global__ void __launch_bounds__(kCodeThreads) paged_store_tokens_kernel(StoreC
     int32_t slot[U], head[U];
     int64_t token[U];
     Raw<T, V> held[U][2];
-    uint32_t size[U][2];
+    Size size[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         // past the last row: the block's first token, not stored
@@ -280,14 +333,20 @@ __global__ void __launch_bounds__(kCodeThreads) paged_store_tokens_kernel(StoreC
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            size[u][s] = largest(held[u][s], 0);
+            size[u][s] = {0, false};
+            look(held[u][s], size[u][s]);
             for (int c = lane + L; c < vecs; c += L) {
                 Raw<T, V> more;
                 more.read(source(u, s) + c * V);
-                size[u][s] = largest(more, size[u][s]);
+                look(more, size[u][s]);
             }
+            uint32_t all = size[u][s].bits | (size[u][s].odd ? 0x80000000u : 0u);
 #pragma unroll
-            for (int d = L / 2; d > 0; d >>= 1) size[u][s] = max(size[u][s], __shfl_xor_sync(0xffffffffu, size[u][s], d));
+            for (int d = L / 2; d > 0; d >>= 1) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, all, d);
+                all = max(all & 0x7fffffffu, other & 0x7fffffffu) | ((all | other) & 0x80000000u);
+            }
+            size[u][s] = {all & 0x7fffffffu, (all >> 31) != 0};
         }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -297,8 +356,8 @@ __global__ void __launch_bounds__(kCodeThreads) paged_store_tokens_kernel(StoreC
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const Side &side = a.side[s];
-            const float now = scale_for(size[u][s]);
-            const Divide by = divide_by(now);
+            const float now = scale_for(size[u][s].bits);
+            const Divide by = divide_by(now, size[u][s].odd);
             unsigned char *codes = side.codes + page * side.cs[0] + in * side.cs[1] + head[u] * side.cs[2];
             if (lane < vecs) write_codes(codes + lane * V, held[u][s], by);
             for (int c = lane + L; c < vecs; c += L) {
@@ -320,7 +379,7 @@ cudaError_t launch_store_codes(StoreCodesArgs &a, cudaStream_t stream) {
     }
     // Few tokens: small tiles, and a tile's runs and heads go to several blocks.
     const int sms = std::max(1, device_sm_count());
-    a.tile = a.tokens <= 16 * sms ? 16 : kMaxTile;
+    a.tile = a.tokens <= 16 * sms ? 32 : kMaxTile;
     const int64_t tiles = ((int64_t)a.tokens + a.tile - 1) / a.tile;
     const int64_t most = (std::min(a.tile, a.tokens) * 2ll * a.heads + kCodeWarps - 1) / kCodeWarps;  // blocks that a tile could fill
     a.slices = (int)std::max<int64_t>(1, std::min<int64_t>(most, (2 * sms + tiles - 1) / tiles));
@@ -389,50 +448,56 @@ __global__ void __launch_bounds__(kLoadThreads) paged_load_kernel(LoadArgs a) {
     }
     for (int i = threadIdx.x; i < here; i += kLoadThreads) shared[i] = slot_of_row(a, ptr, token0 + i);
     __syncthreads();
+    // keys and values, all of a thread's, before any is stored
+    Vec<C, N> in[2][U];
+    float scale[2][U];
+    int32_t slot[U];
+    uint32_t token[U], head[U], at[U];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const LoadSide &side = a.side[s];
-        Vec<C, N> in[U];
-        float scale[U];
-        int32_t slot[U];
-        T *to[U];
+    for (int u = 0; u < U; ++u) {
+        const uint32_t e = skip + threadIdx.x + u * kLoadThreads, t = over(e, a.row_mul, a.row_shift), in_row = e - t * a.row;
+        token[u] = t, head[u] = over(in_row, a.vecs_mul, a.vecs_shift), at[u] = (in_row - head[u] * a.vecs) * N;
+        slot[u] = first + threadIdx.x + u * kLoadThreads < a.items ? shared[t] : -1;
+        const bool there = slot[u] >= 0;
+        const uint32_t page = there ? over((uint32_t)slot[u], a.page_mul, a.page_shift) : 0, inside = there ? (uint32_t)slot[u] - page * a.page : 0;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t e = skip + threadIdx.x + u * kLoadThreads, t = over(e, a.row_mul, a.row_shift), in_row = e - t * a.row;
-            const uint32_t head = over(in_row, a.vecs_mul, a.vecs_shift), at = (in_row - head * a.vecs) * N;
-            slot[u] = first + threadIdx.x + u * kLoadThreads < a.items ? shared[t] : -1;
-            to[u] = reinterpret_cast<T *>(side.out) + (token0 + t) * side.os[0] + head * side.os[1] + at;
-            scale[u] = 0.0f;
+        for (int s = 0; s < 2; ++s) {
+            const LoadSide &side = a.side[s];
+            scale[s][u] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) in[u].v[i] = C{};
-            if (slot[u] < 0) continue;
-            const uint32_t page = over((uint32_t)slot[u], a.page_mul, a.page_shift), inside = (uint32_t)slot[u] - page * a.page;
-            in[u] = *reinterpret_cast<const Vec<C, N> *>(reinterpret_cast<const C *>(side.cache) + page * side.cs[0] +
-                                                         inside * side.cs[1] + head * side.cs[2] + at);
+            for (int i = 0; i < N; ++i) in[s][u].v[i] = C{};
+            if (!there) continue;
+            in[s][u] = *reinterpret_cast<const Vec<C, N> *>(reinterpret_cast<const C *>(side.cache) + page * side.cs[0] +
+                                                            inside * side.cs[1] + head[u] * side.cs[2] + at[u]);
             if (CODES)
-                scale[u] = side.scales[page * side.ss[0] + over(inside, a.block_mul, a.block_shift) * side.ss[1] + head * side.ss[2]];
+                scale[s][u] = side.scales[page * side.ss[0] + over(inside, a.block_mul, a.block_shift) * side.ss[1] + head[u] * side.ss[2]];
         }
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (slot[u] == -1) continue;
-            if constexpr (CODES) {
-                if constexpr (N == 1) {
-                    *to[u] = from_float<T>(from_e4m3x2(in[u].v[0]).x * scale[u]);
-                } else {
-                    constexpr int W = 16 / sizeof(T);  // elements of a store
+    for (int u = 0; u < U; ++u) {
+        if (slot[u] == -1) continue;
 #pragma unroll
-                    for (int i = 0; i < N; i += W) {
-                        Vec<T, W> out;
+        for (int s = 0; s < 2; ++s) {
+            const LoadSide &side = a.side[s];
+            T *to = reinterpret_cast<T *>(side.out) + (token0 + token[u]) * side.os[0] + head[u] * side.os[1] + at[u];
+            if constexpr (CODES && N == 1) {
+                *to = from_float<T>(from_e4m3x2(in[s][u].v[0]).x * scale[s][u]);
+            } else if constexpr (CODES) {
+                constexpr int W = 16 / sizeof(T);  // elements of a store
+                uint32_t words[N / 4];
+                memcpy(words, &in[s][u], N);
 #pragma unroll
-                        for (int j = 0; j < W; j += 2) {
-                            const float2 x = from_e4m3x2((uint32_t)in[u].v[i + j] | (uint32_t)in[u].v[i + j + 1] << 8);
-                            out.v[j] = from_float<T>(x.x * scale[u]), out.v[j + 1] = from_float<T>(x.y * scale[u]);
-                        }
-                        *reinterpret_cast<Vec<T, W> *>(to[u] + i) = out;
+                for (int i = 0; i < N; i += W) {
+                    Vec<T, W> out;
+#pragma unroll
+                    for (int j = 0; j < W; j += 2) {
+                        const float2 x = from_e4m3x2(words[(i + j) / 4] >> ((i + j) % 4 * 8) & 0xffffu);
+                        out.v[j] = from_float<T>(x.x * scale[s][u]), out.v[j + 1] = from_float<T>(x.y * scale[s][u]);
                     }
+                    *reinterpret_cast<Vec<T, W> *>(to + i) = out;
                 }
             } else {
-                *reinterpret_cast<Vec<T, N> *>(to[u]) = in[u];
+                *reinterpret_cast<Vec<T, N> *>(to) = in[s][u];
             }
         }
     }
@@ -440,11 +505,16 @@ __global__ void __launch_bounds__(kLoadThreads) paged_load_kernel(LoadArgs a) {
 
 template <typename T, bool CODES, int N>
 cudaError_t launch_load(const LoadArgs &a, cudaStream_t stream) {
-    constexpr int U = N == 1 ? 8 : 4;
+    constexpr int U = N == 1 ? 4 : 2;
     const int64_t per_block = kLoadThreads * U;
     const size_t smem = 4 * ((per_block - 1) / a.row + 2 + (a.requests <= kLoadRequests ? a.requests + 1 : 0));
     return launch_chained(paged_load_kernel<T, CODES, N, U>, (unsigned)((a.items + per_block - 1) / per_block), kLoadThreads,
                           smem, 0, stream, a);
+}
+
+template <typename T>
+cudaError_t launch_load_codes(const LoadArgs &a, int n, cudaStream_t stream) {
+    return n == 16 ? launch_load<T, true, 16>(a, stream) : n == 8 ? launch_load<T, true, 8>(a, stream) : launch_load<T, true, 1>(a, stream);
 }
 
 bool strides_on(const void *p, const int64_t *strides, int n, int size, int bytes) {
@@ -539,11 +609,14 @@ spmv_status_t spmv_paged_load(int32_t requests, int32_t tokens, int32_t heads, i
     std::copy(k_stride, k_stride + 2, a.side[0].os), std::copy(v_stride, v_stride + 2, a.side[1].os);
     std::copy(c.k_stride, c.k_stride + 3, a.side[0].cs), std::copy(c.v_stride, c.v_stride + 3, a.side[1].cs);
     std::copy(c.k_scale_stride, c.k_scale_stride + 3, a.side[0].ss), std::copy(c.v_scale_stride, c.v_scale_stride + 3, a.side[1].ss);
-    // 8 codes are one load of 8 bytes and one or two stores of 16
-    const int n = c.block ? 8 : 16 / size;
-    bool wide = head_dim % n == 0;
-    for (const LoadSide &s : a.side)
-        wide = wide && strides_on(s.cache, s.cs, 3, held, n * held) && strides_on(s.out, s.os, 2, size, 16);
+    // 16 codes are one load of 16 bytes and two or four stores; 8 where heads or strides allow no more
+    auto fits = [&](int n) {
+        bool wide = head_dim % n == 0;
+        for (const LoadSide &s : a.side) wide = wide && strides_on(s.cache, s.cs, 3, held, n * held) && strides_on(s.out, s.os, 2, size, 16);
+        return wide;
+    };
+    const int n = c.block ? (fits(16) ? 16 : 8) : 16 / size;
+    const bool wide = fits(n);
     a.vecs = wide ? head_dim / n : head_dim;
     a.row = heads * a.vecs;
     a.items = (int64_t)tokens * a.row;
@@ -556,9 +629,9 @@ spmv_status_t spmv_paged_load(int32_t requests, int32_t tokens, int32_t heads, i
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
     cudaError_t e;
     if (c.block)
-        e = elem == SPMV_ELEM_F32    ? (wide ? launch_load<float, true, 8>(a, stream) : launch_load<float, true, 1>(a, stream))
-            : elem == SPMV_ELEM_BF16 ? (wide ? launch_load<__nv_bfloat16, true, 8>(a, stream) : launch_load<__nv_bfloat16, true, 1>(a, stream))
-                                     : (wide ? launch_load<__half, true, 8>(a, stream) : launch_load<__half, true, 1>(a, stream));
+        e = elem == SPMV_ELEM_F32    ? launch_load_codes<float>(a, wide ? n : 1, stream)
+            : elem == SPMV_ELEM_BF16 ? launch_load_codes<__nv_bfloat16>(a, wide ? n : 1, stream)
+                                     : launch_load_codes<__half>(a, wide ? n : 1, stream);
     else
         e = size == 4 ? (wide ? launch_load<float, false, 4>(a, stream) : launch_load<float, false, 1>(a, stream))
                       : (wide ? launch_load<__half, false, 8>(a, stream) : launch_load<__half, false, 1>(a, stream));
