@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kMaxBlock = 64;  // tokens of a scale: a run's slots are 64 bits
 constexpr int kCodeThreads = 256, kCodeWarps = kCodeThreads / 32;
-constexpr int kMaxTile = 64;   // tokens of a tile
+constexpr int kTile = 32;      // tokens of a tile (64: 73 us instead of 72 below)
 // Tokens of one block that are further apart in `slots` are not looked for: a
 // long tail of skipped ones would be read to its end.
 constexpr int kMaxGap = 64;
@@ -45,7 +45,7 @@ struct Side {  // of keys, or of values
 
 struct StoreCodesArgs {
     Side side[2];
-    int32_t tokens, heads, dim, num_pages, page, block, tile, slices;
+    int32_t tokens, heads, dim, num_pages, page, block, slices;
     uint32_t page_mul, page_shift, block_mul, block_shift, heads_mul, heads_shift;
     const int32_t *slots;
 };
@@ -94,37 +94,31 @@ __device__ __forceinline__ float scale_for(uint32_t size_bits) {
     const int e = (int)(size_bits >> 23) - 8 + ((size_bits & 0x7fffffu) > 0x600000u);  // biased
     return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
-// x / scale; a power of two's reciprocal is exact, and a NaN stands for what is not finite
+// x / scale; a NaN stands for what is not finite.  PLAIN: the scale is a power of two, whose reciprocal is exact, and x
+// is finite.
 struct Divide {
     float scale, inverse;
-    bool exact, odd;  // odd: there may be values that are not finite
-    __device__ __forceinline__ float operator()(float x) const {
-        const float q = exact ? x * inverse : x / scale;
-        return !odd || (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u ? q : __int_as_float(0x7fffffff);
-    }
+    bool plain;
 };
 __device__ __forceinline__ Divide divide_by(float scale, bool odd) {
-    return {scale, 1.0f / scale, (__float_as_uint(scale) & 0x7fffffu) == 0 && scale <= __uint_as_float(253u << 23), odd};
+    return {scale, 1.0f / scale, !odd && (__float_as_uint(scale) & 0x7fffffu) == 0 && scale <= __uint_as_float(253u << 23)};
 }
-template <typename T, int V>
-__device__ __forceinline__ void write_codes_by(unsigned char *to, const Raw<T, V> &x, const Divide &by) {
+template <bool PLAIN>
+__device__ __forceinline__ float divided(float x, const Divide &by) {
+    if (PLAIN) return x * by.inverse;
+    return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u ? x / by.scale : __int_as_float(0x7fffffff);
+}
+template <bool PLAIN, typename T, int V>
+__device__ __forceinline__ void write_codes(unsigned char *to, const Raw<T, V> &x, const Divide &by) {
+    auto q = [&](int i) { return divided<PLAIN>(x[i], by); };
     if constexpr (V == 1) {
-        *to = (unsigned char)to_e4m3x2(by(x[0]), 0.0f);
+        *to = (unsigned char)to_e4m3x2(q(0), 0.0f);
     } else {
         static_assert(V == 8, "");
         uint2 c;
-        c.x = to_e4m3x2(by(x[0]), by(x[1])) | to_e4m3x2(by(x[2]), by(x[3])) << 16;
-        c.y = to_e4m3x2(by(x[4]), by(x[5])) | to_e4m3x2(by(x[6]), by(x[7])) << 16;
+        c.x = to_e4m3x2(q(0), q(1)) | to_e4m3x2(q(2), q(3)) << 16;
+        c.y = to_e4m3x2(q(4), q(5)) | to_e4m3x2(q(6), q(7)) << 16;
         *reinterpret_cast<uint2 *>(to) = c;
-    }
-}
-template <typename T, int V>
-__device__ __forceinline__ void write_codes(unsigned char *to, const Raw<T, V> &x, const Divide &by) {
-    if (by.exact && !by.odd) {  // nearly always
-        const Divide plain = {by.scale, by.inverse, true, false};
-        write_codes_by(to, x, plain);
-    } else {
-        write_codes_by(to, x, by);
     }
 }
 template <int V>
@@ -147,21 +141,21 @@ __device__ __forceinline__ void rescale_codes(unsigned char *at, float by) {
 struct Run {
     int32_t block, first, count;
 };
-constexpr int kListed = kMaxTile + kMaxBlock;  // the tile's tokens, and those behind it of its last run
+constexpr int kListed = kTile + kMaxBlock;  // the tile's tokens, and those behind it of its last run
 
 // L lanes take a row, 32 / L rows go at once; HELD batches of these stay in
 // registers between the two passes.
 template <typename T, int V, int L>
 __global__ void __launch_bounds__(kCodeThreads, 4) paged_store_blocks_kernel(StoreCodesArgs a) {
     constexpr int G = 32 / L, HELD = sizeof(T) == 4 ? 2 : 8;
-    __shared__ Run runs[kMaxTile];
+    __shared__ Run runs[kTile];
     __shared__ int num_runs;
     __shared__ int32_t token_of[kListed];
     __shared__ uint8_t place_of[kListed];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     after_previous();
     const uint32_t cache_slots = (uint32_t)a.num_pages * (uint32_t)a.page;
-    const int64_t t0 = (int64_t)(blockIdx.x / a.slices) * a.tile;
+    const int64_t t0 = (int64_t)(blockIdx.x / a.slices) * kTile;
     const int slice = blockIdx.x % a.slices;
     if (warp == 0) {
         // a token's slot and the block of tokens that it goes to, or -1
@@ -180,9 +174,9 @@ __global__ void __launch_bounds__(kCodeThreads, 4) paged_store_blocks_kernel(Sto
         int n = 0, listed = 0;  // runs; tokens of them
         const uint32_t under_me = (1u << lane) - 1;
         for (int64_t i0 = t0;; i0 += 32) {
-            const bool inside = i0 < t0 + a.tile;  // behind the tile: the last run's tokens alone
+            const bool inside = i0 < t0 + kTile;  // behind the tile: the last run's tokens alone
             const int64_t i = i0 + lane;
-            const int b = inside && i >= t0 + a.tile ? -1 : read(i, slot);
+            const int b = inside && i >= t0 + kTile ? -1 : read(i, slot);
             const uint32_t there = __ballot_sync(0xffffffffu, b >= 0), under = there & under_me;
             const int last = __shfl_sync(0xffffffffu, b, under ? 31 - __clz(under) : 0);
             const bool opens = b >= 0 && (under ? b != last : b != before || i - before_at > kMaxGap);
@@ -204,7 +198,7 @@ __global__ void __launch_bounds__(kCodeThreads, 4) paged_store_blocks_kernel(Sto
             if (there) {
                 before = __shfl_sync(0xffffffffu, b, 31 - __clz(there));
                 before_at = i0 + 31 - __clz(there);
-            } else if (inside && i0 + 32 >= t0 + a.tile && i0 + 31 - before_at >= kMaxGap) {
+            } else if (inside && i0 + 32 >= t0 + kTile && i0 + 31 - before_at >= kMaxGap) {
                 break;
             }
             if (i0 + 32 >= a.tokens) break;
@@ -215,7 +209,6 @@ __global__ void __launch_bounds__(kCodeThreads, 4) paged_store_blocks_kernel(Sto
     }
     __syncthreads();
     const int vecs = a.dim / V, sub = lane / L, col = lane % L;
-    const bool one = vecs <= L;  // a row is one vector a lane
     const int tasks = num_runs * 2 * a.heads;
     for (int task = slice * kCodeWarps + warp; task < tasks; task += a.slices * kCodeWarps) {
         const int of = (int)over((uint32_t)task >> 1, a.heads_mul, a.heads_shift), head = (task >> 1) - of * a.heads;
@@ -229,21 +222,33 @@ __global__ void __launch_bounds__(kCodeThreads, 4) paged_store_blocks_kernel(Sto
         const float old = *scale;
         Size size = {0, false};
         uint32_t pairs = 0;
+        auto look_at = [&](const Raw<T, V> &row) {
+            if constexpr (sizeof(T) == 2 && V == 8) look_pairs(row, pairs);
+            else look(row, size);
+        };
+        // one vector of row r
+        auto read = [&](Raw<T, V> &to, int r, int c) { to.read(x + token_of[run.first + r] * side.xs[0] + c * V); };
+        const bool whole = vecs <= L && n <= HELD * G;  // the registers hold the run
         Raw<T, V> held[HELD];
-        for (int r = 0; r < n; r += HELD * G) {
-            for (int c = col; c < vecs || c == col; c += L) {  // once where a row is one vector a lane
+        if (whole) {
 #pragma unroll
-                for (int u = 0; u < HELD; ++u) {
-                    const int row = r + u * G + sub;
-                    held[u].clear();
-                    if (row < n && c < vecs) held[u].read(x + token_of[run.first + row] * side.xs[0] + c * V);
-                }
-#pragma unroll
-                for (int u = 0; u < HELD; ++u) {
-                    if constexpr (sizeof(T) == 2 && V == 8) look_pairs(held[u], pairs);
-                    else look(held[u], size);
-                }
+            for (int u = 0; u < HELD; ++u) {
+                held[u].clear();
+                if (u * G + sub < n && col < vecs) read(held[u], u * G + sub, col);
             }
+#pragma unroll
+            for (int u = 0; u < HELD; ++u) look_at(held[u]);
+        } else {
+            for (int r = sub; r < n; r += HELD * G)
+                for (int c = col; c < vecs; c += L) {
+#pragma unroll
+                    for (int u = 0; u < HELD; ++u) {
+                        held[u].clear();
+                        if (r + u * G < n) read(held[u], r + u * G, c);
+                    }
+#pragma unroll
+                    for (int u = 0; u < HELD; ++u) look_at(held[u]);
+                }
         }
         if constexpr (sizeof(T) == 2 && V == 8) {
             pairs = __vmaxu2(pairs, pairs >> 16) & 0xffffu;
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kCodeThreads, 4) paged_store_blocks_kernel(Sto
                 for (int r = sub; r < n; r += G)
                     for (int c = col; c < vecs; c += L) {
                         Raw<T, V> again;
-                        again.read(x + token_of[run.first + r] * side.xs[0] + c * V);
+                        read(again, r, c);
                         look(again, size);
                     }
                 size.odd = true;
@@ -277,16 +282,20 @@ __global__ void __launch_bounds__(kCodeThreads, 4) paged_store_blocks_kernel(Sto
         const bool begun = low & 1;
         const float need = scale_for(size.bits), now = begun ? need : fmaxf(old, need);
         const Divide by = divide_by(now, size.odd);
-        for (int r = 0; r < n; r += HELD * G) {
-            for (int c = col; c < vecs; c += L) {
+        if (whole && by.plain) {  // nearly always
 #pragma unroll
-                for (int u = 0; u < HELD; ++u) {
-                    const int row = r + u * G + sub;
-                    if (row >= n) continue;
-                    if (!(one && n <= HELD * G)) held[u].read(x + token_of[run.first + row] * side.xs[0] + c * V);
-                    write_codes(codes + place_of[run.first + row] * side.cs[1] + c * V, held[u], by);
+            for (int u = 0; u < HELD; ++u)
+                if (u * G + sub < n && col < vecs)
+                    write_codes<true>(codes + place_of[run.first + u * G + sub] * side.cs[1] + col * V, held[u], by);
+        } else {
+            for (int r = sub; r < n; r += G)
+                for (int c = col; c < vecs; c += L) {
+                    Raw<T, V> again;
+                    read(again, r, c);
+                    unsigned char *to = codes + place_of[run.first + r] * side.cs[1] + c * V;
+                    if (by.plain) write_codes<true>(to, again, by);
+                    else write_codes<false>(to, again, by);
                 }
-            }
         }
         if (!begun && now > old) {
             high = __reduce_or_sync(0xffffffffu, high);
@@ -359,11 +368,14 @@ __global__ void __launch_bounds__(kCodeThreads) paged_store_tokens_kernel(StoreC
             const float now = scale_for(size[u][s].bits);
             const Divide by = divide_by(now, size[u][s].odd);
             unsigned char *codes = side.codes + page * side.cs[0] + in * side.cs[1] + head[u] * side.cs[2];
-            if (lane < vecs) write_codes(codes + lane * V, held[u][s], by);
+            if (lane < vecs) {
+                if (by.plain) write_codes<true>(codes + lane * V, held[u][s], by);
+                else write_codes<false>(codes + lane * V, held[u][s], by);
+            }
             for (int c = lane + L; c < vecs; c += L) {
                 Raw<T, V> more;
                 more.read(source(u, s) + c * V);
-                write_codes(codes + c * V, more, by);
+                write_codes<false>(codes + c * V, more, by);
             }
             if (lane == 0) side.scales[page * side.ss[0] + in * side.ss[1] + head[u] * side.ss[2]] = now;
         }
@@ -377,11 +389,10 @@ cudaError_t launch_store_codes(StoreCodesArgs &a, cudaStream_t stream) {
         const int64_t blocks = ((int64_t)a.tokens * a.heads + ROWS - 1) / ROWS;
         return launch_chained(paged_store_tokens_kernel<T, V, L>, (unsigned)blocks, kCodeThreads, 0, 0, stream, a);
     }
-    // Few tokens: small tiles, and a tile's runs and heads go to several blocks.
+    // few tokens: a tile's runs and heads go to several blocks
     const int sms = std::max(1, device_sm_count());
-    a.tile = a.tokens <= 16 * sms ? 32 : kMaxTile;
-    const int64_t tiles = ((int64_t)a.tokens + a.tile - 1) / a.tile;
-    const int64_t most = (std::min(a.tile, a.tokens) * 2ll * a.heads + kCodeWarps - 1) / kCodeWarps;  // blocks that a tile could fill
+    const int64_t tiles = ((int64_t)a.tokens + kTile - 1) / kTile;
+    const int64_t most = (std::min<int64_t>(kTile, a.tokens) * 2ll * a.heads + kCodeWarps - 1) / kCodeWarps;  // blocks that a tile could fill
     a.slices = (int)std::max<int64_t>(1, std::min<int64_t>(most, (2 * sms + tiles - 1) / tiles));
     return launch_chained(paged_store_blocks_kernel<T, V, L>, (unsigned)(tiles * a.slices), kCodeThreads, 0, 0, stream, a);
 }
@@ -505,7 +516,7 @@ __global__ void __launch_bounds__(kLoadThreads) paged_load_kernel(LoadArgs a) {
 
 template <typename T, bool CODES, int N>
 cudaError_t launch_load(const LoadArgs &a, cudaStream_t stream) {
-    constexpr int U = N == 1 ? 4 : 2;
+    constexpr int U = N == 1 ? 4 : 1;
     const int64_t per_block = kLoadThreads * U;
     const size_t smem = 4 * ((per_block - 1) / a.row + 2 + (a.requests <= kLoadRequests ? a.requests + 1 : 0));
     return launch_chained(paged_load_kernel<T, CODES, N, U>, (unsigned)((a.items + per_block - 1) / per_block), kLoadThreads,
@@ -573,7 +584,7 @@ spmv_status_t spmv_paged_store_e4m3(int32_t tokens, int32_t heads, int32_t head_
     for (const Side &s : a.side) wide = wide && strides_on(s.x, s.xs, 2, size, 16) && strides_on(s.codes, s.cs, 3, 1, 8);
     a.tokens = tokens, a.heads = heads, a.dim = head_dim;
     a.num_pages = c.num_pages, a.page = c.page_size, a.block = c.block;
-    a.tile = a.slices = 0;
+    a.slices = 0;
     a.slots = slots;
     set_divisor((uint32_t)c.page_size, &a.page_mul, &a.page_shift);
     set_divisor((uint32_t)c.block, &a.block_mul, &a.block_shift);
