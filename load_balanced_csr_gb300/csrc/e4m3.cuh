@@ -21,6 +21,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t codes) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
     return r;
 }
+// Four codes.
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
+}
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
     const uint32_t pair = e4m3x2_to_half2(codes);
     __half2 h;

@@ -37,6 +37,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -1075,6 +1076,7 @@ cudaError_t launch_attention(const spmv_paged_attention_t &a, int sms, cudaStrea
     p.tiles = (p.group + P::GT - 1) / P::GT;
     p.rows = a.kv_heads * p.tiles;
     p.scale2 = std::fabs(a.scale) * kLog2e;
+    if constexpr (P::SCALES) p.scale2 = std::max(p.scale2, FLT_MIN);  // minus infinity times it has no weight
     p.flip = a.scale < 0.0f ? 0x80008000u : 0u;
     const int size = sizeof(T);
     auto pairs = [&](const void *at, const int64_t *strides) {  // pairs of elements are aligned

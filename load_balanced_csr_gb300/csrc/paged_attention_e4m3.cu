@@ -20,6 +20,8 @@
 //   Weights are taken 2^14 times as large, times vs / ref with ref the power of
 // two below the largest value scale so far, as hi + lo; the sums, relative to
 // ref, are rescaled when a larger scale comes.
+#include <cfloat>
+
 #include "e4m3.cuh"
 #include "paged_attention.cuh"
 
@@ -49,7 +51,8 @@ struct TileE4m3 {
     uint32_t q[DP / 16][2 * H], next[AHEAD ? DP / 16 : 1][2 * H];
     float o[DP / 8][4];  // [32 elements][16 of them][even, odd]
     float m[H], l[H];
-    float qf[H];         // what q was divided by
+    float scale2[H];     // the scores' scale for q as it was multiplied, and what it was divided by
+    float qf[H];
     float ref;           // of o: the same on every lane
 
     __device__ __forceinline__ static void load(const AttendArgs &p, uint32_t (*to)[2 * H], int b, int h0, int heads, int lane) {
@@ -87,7 +90,7 @@ struct TileE4m3 {
             for (int r = 0; r < 2 * H; ++r) q[s][r] ^= p.flip;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-            qf[h] = 1.0f;
+            qf[h] = 1.0f, scale2[h] = p.scale2;
             if (!BF16) continue;
             uint32_t top = 0;  // the largest element's bits
 #pragma unroll
@@ -100,6 +103,7 @@ struct TileE4m3 {
             const int shift = min(max(14 - ((int)(top >> 7) - 127), -114), 126);
             const float up = __int_as_float((127 + shift) << 23);
             qf[h] = __int_as_float((127 - shift) << 23);
+            scale2[h] = fmaxf(p.scale2 * qf[h], FLT_MIN);
 #pragma unroll
             for (int s = 0; s < DP / 16; ++s)
 #pragma unroll
@@ -133,48 +137,51 @@ struct TileE4m3 {
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t(&qs)[2 * H] = q[2 * i + j];
                         const uint32_t qa[4] = {qs[0], H == 2 ? qs[H - 1] : 0u, qs[H], H == 2 ? qs[2 * H - 1] : 0u};
-                        mma16816<__half>(sums[n], qa, e4m3x2_to_half2(kb[j] & 0xffffu), e4m3x2_to_half2(kb[j] >> 16));
-                        mma16816<__half>(sums[n + 1], qa, e4m3x2_to_half2(kb[2 + j] & 0xffffu), e4m3x2_to_half2(kb[2 + j] >> 16));
+                        uint32_t b0, b1;
+                        e4m3x4_to_half2(kb[j], b0, b1);
+                        mma16816<__half>(sums[n], qa, b0, b1);
+                        e4m3x4_to_half2(kb[2 + j], b0, b1);
+                        mma16816<__half>(sums[n + 1], qa, b0, b1);
                     }
                 }
         }
-        const bool whole = mask == FULL_MASK<CH>;
-        // value scales are positive; a larger one than any so far
-        const uint32_t top_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(v_scale[lane % CH]) & 0x7fffffffu);
-        const float ref_now = __uint_as_float(max(top_bits & 0x7f800000u, __float_as_uint(ref)));
+        // a value scale of twice ref, or more
+        const uint32_t v_bits = __float_as_uint(v_scale[lane % CH]) & 0x7f800000u;
+        bool higher = v_bits > __float_as_uint(ref);
         uint32_t hi[NT * H], lo[NT * H];
         float s[NT][H][2], top[H];
-        bool higher = ref_now > ref;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float2 scale = *reinterpret_cast<const float2 *>(k_scale + n * 8 + (lane & 3) * 2);
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                s[n][h][0] = sums[n][2 * h] * scale.x, s[n][h][1] = sums[n][2 * h + 1] * scale.y;
-                if (BF16) s[n][h][0] *= qf[h], s[n][h][1] *= qf[h];
-            }
+            for (int h = 0; h < H; ++h) s[n][h][0] = sums[n][2 * h] * scale.x, s[n][h][1] = sums[n][2 * h + 1] * scale.y;
+        }
+        if (mask != FULL_MASK<CH>) {  // their weights are 0: scale2 is not
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (!((mask >> (n * 8 + (lane & 3) * 2 + c)) & 1))
+#pragma unroll
+                        for (int h = 0; h < H; ++h) s[n][h][c] = -INFINITY;
         }
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             float raw = -INFINITY;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (!whole && !((mask >> (n * 8 + (lane & 3) * 2 + c)) & 1)) s[n][h][c] = -INFINITY;
-                    raw = fmaxf(raw, s[n][h][c]);
-                }
+            for (int n = 0; n < NT; ++n) raw = fmaxf(raw, fmaxf(s[n][h][0], s[n][h][1]));
             raw = fmaxf(raw, __shfl_xor_sync(0xffffffffu, raw, 1));
             raw = fmaxf(raw, __shfl_xor_sync(0xffffffffu, raw, 2));
             top[h] = fmaxf(m[h], raw);
             higher |= top[h] > m[h];
         }
         if (__any_sync(0xffffffffu, higher)) {
+            const float ref_now = __uint_as_float(max(__reduce_max_sync(0xffffffffu, v_bits), __float_as_uint(ref)));
             const float down = ref / ref_now;
             ref = ref_now;
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                const float keep = worth(m[h], top[h], p.scale2), keep_o = keep * down;
+                const float keep = worth(m[h], top[h], scale2[h]), keep_o = keep * down;
                 l[h] *= keep;
                 m[h] = top[h];
 #pragma unroll
@@ -184,7 +191,7 @@ struct TileE4m3 {
                 }
             }
         }
-        const float by_ref = 1.0f / ref;
+        const float by_ref = __uint_as_float((254u << 23) - __float_as_uint(ref));  // ref is a power of two
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float2 scale = *reinterpret_cast<const float2 *>(v_scale + n * 8 + (lane & 3) * 2);
@@ -192,19 +199,14 @@ struct TileE4m3 {
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const float base = base_of(m[h]);
-                float w[2];
-                __half high[2];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    w[c] = pow2(fmaf(s[n][h][c] - base, p.scale2, UP));
-                    if (!whole && !((mask >> (n * 8 + (lane & 3) * 2 + c)) & 1)) w[c] = 0.0f;
-                }
-                l[h] += w[0] + w[1];
-                w[0] *= scale.x, w[1] *= scale.y;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) high[c] = from_float<__half>(w[c]);
-                hi[n * H + h] = pack2(high[0], high[1]);
-                lo[n * H + h] = pack2(from_float<__half>(w[0] - to_float(high[0])), from_float<__half>(w[1] - to_float(high[1])));
+                float x = pow2(fmaf(s[n][h][0] - base, scale2[h], UP)), y = pow2(fmaf(s[n][h][1] - base, scale2[h], UP));
+                l[h] += x + y;
+                x *= scale.x, y *= scale.y;
+                const __half2 high = __floats2half2_rn(x, y);
+                const float2 back = __half22float2(high);
+                const __half2 low = __floats2half2_rn(x - back.x, y - back.y);
+                memcpy(&hi[n * H + h], &high, 4);
+                memcpy(&lo[n * H + h], &low, 4);
             }
         }
         const uint32_t at = vs + (r8 + (mat & 1) * 8) * PITCH + (mat >> 1) * 16;
@@ -220,14 +222,16 @@ struct TileE4m3 {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) vb[j] = __byte_perm(vb[j], 0, 0x3120);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t b0[2], b1[2];  // even elements, odd ones
+                    e4m3x4_to_half2(vb[2 * j], b0[0], b0[1]);
+                    e4m3x4_to_half2(vb[2 * j + 1], b1[0], b1[1]);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t b0 = e4m3x2_to_half2(e ? vb[2 * j] >> 16 : vb[2 * j] & 0xffffu);
-                        const uint32_t b1 = e4m3x2_to_half2(e ? vb[2 * j + 1] >> 16 : vb[2 * j + 1] & 0xffffu);
-                        mma16816<__half>(o[4 * i + 2 * j + e], pa, b0, b1);
-                        if (H == 2) mma16816<__half>(o[4 * i + 2 * j + e], pl, b0, b1);
+                        mma16816<__half>(o[4 * i + 2 * j + e], pa, b0[e], b1[e]);
+                        if (H == 2) mma16816<__half>(o[4 * i + 2 * j + e], pl, b0[e], b1[e]);
                     }
+                }
             }
         }
     }
@@ -239,6 +243,7 @@ struct TileE4m3 {
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
             l[h] *= down;
+            if (BF16) m[h] *= qf[h];
         }
 #pragma unroll
         for (int n = 0; n < DP / 8; ++n)
