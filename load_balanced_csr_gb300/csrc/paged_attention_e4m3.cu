@@ -273,14 +273,24 @@ struct TileE4m3 {
     }
 };
 
+// Positions of a chunk, warps and stages: what an SM's registers and shared
+// memory hold, of the ways measured (64 requests, their lengths even up to
+// 4,000, 4 kv heads, 16 positions a page, bf16; us with 4 and with 16 heads
+// each).  64 elements: 8 warps of 4 stages 32.8 / 46.2, 12 of 3 31.4 / 46.2, 16
+// of 2 32.3 / 42.7, but four requests of up to 300 positions take 10.3 with 8
+// warps and 12.4 with more; 96: 8 of 3 42.3 / 54.8, 10 of 3 45.9; 128: 8 of 2
+// chunks of 32 (one request of 131,071, 8 heads each: 65 us, 7 of 3 79, 10 of
+// 2 80, 16 positions a chunk 83 and more); 192: 8 of 2 62.9 / 83.9, 16
+// positions a chunk 65.2 / 137; 256: with 4 heads each 8 of 2 chunks of 16
+// 74.0, 6 of 3 86, 6 of 2 of 32 87; with 16 6 of 2 of 32 142, 4 of 4 of 16 176.
 template <typename T, int GT, typename F>
 auto with_codes(int dim, F f) {
     constexpr bool small = GT == 8;
-    if (dim <= 64) return f(TileE4m3<T, GT, 64, 32, 12, 3>());
-    if (dim <= 96) return f(TileE4m3<T, GT, 96, 32, small ? 10 : 8, 3>());
-    if (dim <= 128) return f(TileE4m3<T, GT, 128, 32, 8, small ? 2 : 2>());
-    if (dim <= 192) return f(TileE4m3<T, GT, 192, 16, small ? 8 : 4, small ? 3 : 4>());
-    return f(TileE4m3<T, GT, 256, 16, small ? 6 : 4, small ? 3 : 4>());
+    if (dim <= 64) return f(TileE4m3<T, GT, 64, 32, small ? 8 : 16, small ? 4 : 2>());
+    if (dim <= 96) return f(TileE4m3<T, GT, 96, 32, 8, 3>());
+    if (dim <= 128) return f(TileE4m3<T, GT, 128, 32, 8, 2>());
+    if (dim <= 192) return f(TileE4m3<T, GT, 192, 32, 8, 2>());
+    return f(TileE4m3<T, GT, 256, small ? 16 : 32, small ? 8 : 6, 2>());
 }
 template <typename T, typename F>
 auto with_codes(int dim, int group, F f) {
