@@ -98,60 +98,112 @@ __device__ __forceinline__ uint32_t pack<__half>(float lo, float hi) {
     return r;
 }
 
-// The request and the place in it of a block, counted from the last request's last tokens, whose rows have most keys.
+// Queries of a request and a kv head that a block works on at a time.  They
+// are counted from the last request's last tokens, whose rows have most keys.
 struct Work {
     int q0, nq, k0, nk;  // the request's rows
-    int t0;              // the block's first token in it
+    int t0;              // the first token in it
+    int kv_head;
+    int more;            // 0: there is no more, and the rest says nothing
 };
 
+// Finds the requests of work numbers, which mostly rise: a warp's place in the requests.
 template <class S>
-__device__ __forceinline__ bool find_work(const PromptArgs &p, int block, Work *work, int *warp_sums, int *found) {
-    const int block_tokens = S::NQ * p.tile_tokens;
-    const int32_t *kv_ptr = p.a.kv_ptr ? p.a.kv_ptr : p.a.q_ptr;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int carry = 0;
-    if (threadIdx.x == 0) *found = 0;
-    for (int base = 0; base < p.a.requests; base += S::THREADS) {
-        const int r = p.a.requests - 1 - base - (int)threadIdx.x;
-        Work w{};
-        int n = 0, flag = 0;
-        if (r >= 0) {
-            const int q0 = p.a.q_ptr[r], q1 = p.a.q_ptr[r + 1], k0 = kv_ptr[r], k1 = kv_ptr[r + 1];
-            if (q0 < 0 || q1 < q0 || q1 > p.a.tokens) flag = kBadQueries;
-            else if (k0 < 0 || k1 < k0 || k1 > p.a.keys) flag = kBadKeys;
-            else w = Work{q0, q1 - q0, k0, k1 - k0, 0}, n = (w.nq + block_tokens - 1) / block_tokens;
-        }
-        if (flag && blockIdx.x == 0) atomicOr(p.a.status, flag);
-        int scan = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, scan, d);
-            if (lane >= d) scan += up;
-        }
-        if (lane == 31) warp_sums[warp] = scan;
-        __syncthreads();
-        int before = carry + scan - n;
-        for (int i = 0; i < S::THREADS / 32; ++i) {
-            if (i < warp) before += warp_sums[i];
-            carry += warp_sums[i];
-        }
-        if (block >= before && block < before + n) {
-            w.t0 = (n - 1 - (block - before)) * block_tokens;
-            *work = w;
-            *found = 1;
-        }
-        __syncthreads();
-        if (carry > block && blockIdx.x != 0) break;  // the first block looks all requests over
-    }
-    return *found;
-}
+struct Finder {
+    static constexpr int EACH = 4;  // requests of a lane
+    int base = 0, before = 0;       // requests passed, counted from the last, and their blocks
 
+    // request r's rows; what is wrong with them
+    __device__ __forceinline__ static int read(const PromptArgs &p, int r, Work &w) {
+        const int32_t *kv_ptr = p.a.kv_ptr ? p.a.kv_ptr : p.a.q_ptr;
+        const int q0 = p.a.q_ptr[r], q1 = p.a.q_ptr[r + 1], k0 = kv_ptr[r], k1 = kv_ptr[r + 1];
+        w = Work{};
+        if (q0 < 0 || q1 < q0 || q1 > p.a.tokens) return kBadQueries;
+        if (k0 < 0 || k1 < k0 || k1 > p.a.keys) return kBadKeys;
+        w.q0 = q0, w.nq = q1 - q0, w.k0 = k0, w.nk = k1 - k0;
+        return 0;
+    }
+    // by a whole warp
+    __device__ __forceinline__ bool find(const PromptArgs &p, int number, int lane, Work &work) {
+        const int block_tokens = S::NQ * p.tile_tokens, block = number / p.a.kv_heads;
+        if (block < before) base = before = 0;
+        for (; base < p.a.requests; base += 32 * EACH) {
+            Work w[EACH];
+            int n[EACH], sum = 0;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) {
+                const int r = p.a.requests - 1 - base - lane * EACH - i;
+                w[i] = Work{};
+                if (r >= 0) read(p, r, w[i]);
+                n[i] = (w[i].nq + block_tokens - 1) / block_tokens;
+                sum += n[i];
+            }
+            int scan = sum;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, scan, d);
+                if (lane >= d) scan += up;
+            }
+            const int total = __shfl_sync(0xffffffffu, scan, 31);
+            int at = before + scan - sum;
+            bool mine = false;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) {
+                if (block >= at && block < at + n[i]) {
+                    mine = true;
+                    work = w[i];
+                    work.t0 = (n[i] - 1 - (block - at)) * block_tokens;
+                }
+                at += n[i];
+            }
+            const uint32_t who = __ballot_sync(0xffffffffu, mine);
+            if (who) {
+                const int from = __ffs(who) - 1;
+                work.q0 = __shfl_sync(0xffffffffu, work.q0, from), work.nq = __shfl_sync(0xffffffffu, work.nq, from);
+                work.k0 = __shfl_sync(0xffffffffu, work.k0, from), work.nk = __shfl_sync(0xffffffffu, work.nk, from);
+                work.t0 = __shfl_sync(0xffffffffu, work.t0, from);
+                work.kv_head = number - block * p.a.kv_heads;
+                work.more = 1;
+                return true;
+            }
+            before += total;
+        }
+        return false;
+    }
+};
+
+// What a piece of work is to a block.
+template <class S>
+struct Item {
+    int tiles[S::NQ];  // tiles of keys that a tile of queries sees
+    int most;          // of them all
+    int first_cut;     // the first that some of the rows see in part
+
+    __device__ __forceinline__ static int keys_of(const PromptArgs &p, const Work &w, int token) {  // that a token sees
+        return p.a.causal ? min(w.nk, max(0, token + w.nk - w.nq + 1)) : w.nk;
+    }
+    __device__ __forceinline__ Item(const PromptArgs &p, const Work &w) {
+        most = 0;
+#pragma unroll
+        for (int t = 0; t < S::NQ; ++t) {
+            const int first = w.t0 + t * p.tile_tokens, last = min(first + p.tile_tokens, w.nq) - 1;
+            tiles[t] = last < first ? 0 : (keys_of(p, w, last) + S::KEYS - 1) / S::KEYS;
+            most = max(most, tiles[t]);
+        }
+        first_cut = keys_of(p, w, w.t0) / S::KEYS;
+    }
+};
+
+// Barriers' phases are counted over all work of a block: steps of a tile (scores, weights, and product with one tile),
+// stages (full, empty), pieces of work (the others).
 template <class S>
 struct Shared {
-    uint64_t q_full, full[S::STAGES], empty[S::STAGES], scores[2], weights[2], product[S::NQ], done[S::NQ], last;
+    uint64_t q_full, q_empty, full[S::STAGES], empty[S::STAGES], scores[2], weights[2], product, done[S::NQ], last;
+    uint64_t planned[2], taken[2], nearly, answered;
+    uint4 answer;
     uint32_t tmem;
-    int gave_up, not_finite, found, warp_sums[S::THREADS / 32];
-    Work work;
+    int gave_up, not_finite[2];
+    Work plan[2];
 };
 
 template <class S>
@@ -163,32 +215,20 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     __shared__ Shared<S> sh;
     after_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int kv_head = blockIdx.x % p.a.kv_heads;
-    if (!find_work<S>(p, blockIdx.x / p.a.kv_heads, &sh.work, sh.warp_sums, &sh.found)) return;  // the whole block
-    const Work w = sh.work;
     char *smem = dynamic + ((1024 - (tc::smem_u32(dynamic) & 1023)) & 1023);
     char *q_smem = smem, *kv_smem = smem + S::NQ * S::QBYTES;
-    constexpr int kLoader = S::NQ * 4, kIssuer = kLoader + 1;
-
-    // how many tiles of keys a tile of queries sees, and the first that some of the block's rows see in part
-    const int past = w.nk - w.nq;  // token t of the request stands at key t + past
-    auto keys_of = [&](int token) { return p.a.causal ? min(w.nk, max(0, token + past + 1)) : w.nk; };
-    int tiles[S::NQ], most = 0;
-#pragma unroll
-    for (int t = 0; t < S::NQ; ++t) {
-        const int first = w.t0 + t * p.tile_tokens, last = min(first + p.tile_tokens, w.nq) - 1;
-        tiles[t] = last < first ? 0 : (keys_of(last) + S::KEYS - 1) / S::KEYS;
-        most = max(most, tiles[t]);
-    }
-    const int first_cut = keys_of(w.t0) / S::KEYS;
+    constexpr int kLoader = S::NQ * 4, kIssuer = kLoader + 1, kPlanner = kLoader + 2;
 
     if (threadIdx.x == 0) {
-        tc::bar_init(&sh.q_full, 1);
+        tc::bar_init(&sh.q_full, 1), tc::bar_init(&sh.q_empty, 1), tc::bar_init(&sh.product, 1), tc::bar_init(&sh.last, 1);
         for (int i = 0; i < S::STAGES; ++i) tc::bar_init(&sh.full[i], 1), tc::bar_init(&sh.empty[i], 1);
-        for (int i = 0; i < 2; ++i) tc::bar_init(&sh.scores[i], 1), tc::bar_init(&sh.weights[i], 129);
-        for (int i = 0; i < S::NQ; ++i) tc::bar_init(&sh.product[i], 1), tc::bar_init(&sh.done[i], 1);
-        tc::bar_init(&sh.last, 1);
-        sh.gave_up = sh.not_finite = 0;
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(&sh.scores[i], 1), tc::bar_init(&sh.weights[i], 129);
+            tc::bar_init(&sh.planned[i], 1), tc::bar_init(&sh.taken[i], S::NQ * 4 + 2);
+        }
+        for (int i = 0; i < S::NQ; ++i) tc::bar_init(&sh.done[i], 1);
+        tc::bar_init(&sh.answered, 1), tc::bar_init(&sh.nearly, 1);
+        sh.gave_up = 0;
         tc::bar_init_done();
     }
     if (warp == kIssuer) tc::alloc(&sh.tmem, 512);
@@ -197,320 +237,435 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     tc::fence_after();
     const uint32_t tmem = sh.tmem;
     volatile int *gave_up = &sh.gave_up;
+    // The next piece of work; the planner is one ahead of the last warp at work.
+    auto next = [&](int item, Work &w) {
+        if (!tc::bar_wait(&sh.planned[item & 1], item >> 1 & 1, gave_up)) return false;
+        w = sh.plan[item & 1];
+        return w.more != 0;
+    };
+    auto finished = [&](int item) {
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(&sh.taken[item & 1]);
+    };
     // A row of 128 scores needs more registers than 384 threads have each: three times 168 are 72 + 2 * 216.
     static_assert(S::NQ == 1 || S::THREADS == 384, "the registers of the launch");
     if (warp >= kLoader) {
         if constexpr (S::NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kLoader) {
-            int issued = 0;
             bool ok = true;
-            if (lane == 0 && most > 0) {
-                const uint32_t box = (uint32_t)(p.tile_tokens * p.group * 128 * S::HALVES);
-                const int n = S::NQ == 2 && tiles[S::NQ - 1] > 0 ? 2 : 1;
-                tma::mbar_expect_tx(&sh.q_full, n * box);
-                for (int t = 0; t < n; ++t)
-                    for (int h = 0; h < S::HALVES; ++h)
-                        tc::load_3d(q_smem + t * S::QBYTES + h * S::QHALF, &q_map, 64 * h, kv_head * p.group,
-                                    w.q0 + w.t0 + t * p.tile_tokens, &sh.q_full);
-            }
-            // pair i: K of tile i, if there is one, and V of the tile before
-            auto load = [&](int i) {
-                const int stage = i % S::STAGES, round = i / S::STAGES;
-                ok = round == 0 || tc::bar_wait(&sh.empty[stage], (round - 1) & 1, gave_up);
-                if (!ok) return;
-                if (lane == 0) {
-                    tma::mbar_expect_tx(&sh.full[stage], ((i < most) + (i > 0)) * S::KVBYTES);
-                    for (int h = 0; h < S::HALVES; ++h) {
-                        char *at = kv_smem + stage * S::STAGE + h * S::KHALF;
-                        if (i < most) tc::load_3d(at, &k_map, 64 * h, kv_head, w.k0 + i * S::KEYS, &sh.full[stage]);
-                        if (i > 0) tc::load_3d(at + S::KVBYTES, &v_map, 64 * h, kv_head, w.k0 + (i - 1) * S::KEYS, &sh.full[stage]);
+            Work w;
+            int pairs = 0, queries = 0;      // loaded so far
+            int steps[2] = {0, 0};           // announced so far, of a tile (with one tile the first counts)
+            for (int item = 0; ok && next(item, w); ++item) {
+                const Item<S> of(p, w);
+                const int most = of.most;
+                if (lane == 0) sh.not_finite[item & 1] = 0;
+                __syncwarp();
+                if (most > 0) {
+                    if (queries > 0) ok = tc::bar_wait(&sh.q_empty, (queries - 1) & 1, gave_up);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const uint32_t box = (uint32_t)(p.tile_tokens * p.group * 128 * S::HALVES);
+                        const int n = S::NQ == 2 && of.tiles[S::NQ - 1] > 0 ? 2 : 1;
+                        tma::mbar_expect_tx(&sh.q_full, n * box);
+                        for (int t = 0; t < n; ++t)
+                            for (int h = 0; h < S::HALVES; ++h)
+                                tc::load_3d(q_smem + t * S::QBYTES + h * S::QHALF, &q_map, 64 * h, w.kv_head * p.group,
+                                            w.q0 + w.t0 + t * p.tile_tokens, &sh.q_full);
                     }
+                    ++queries;
                 }
-                ++issued;
-            };
-            // puts zeros in the place of what is not finite among a stage's values
-            auto look_over = [&](int stage) {
-                constexpr uint32_t EXPONENT = S::BF16 ? 0x7f807f80u : 0x7c007c00u, UNIT = S::BF16 ? 0x00800080u : 0x04000400u;
-                uint4 *v = reinterpret_cast<uint4 *>(kv_smem + stage * S::STAGE + S::KVBYTES);
-                auto bad = [&](uint32_t x) { return ((x & EXPONENT) + UNIT) & 0x80008000u; };  // its halves that are not finite
-                uint32_t any = 0;
+                const int pairs0 = pairs;  // pair i of this work is pair pairs0 + i
+                // pair i: K of tile i, if there is one, and V of the tile before
+                auto load = [&](int i) {
+                    const int stage = pairs % S::STAGES, round = pairs / S::STAGES;
+                    ok = round == 0 || tc::bar_wait(&sh.empty[stage], (round - 1) & 1, gave_up);
+                    if (!ok) return;
+                    if (lane == 0) {
+                        tma::mbar_expect_tx(&sh.full[stage], ((i < most) + (i > 0)) * S::KVBYTES);
+                        for (int h = 0; h < S::HALVES; ++h) {
+                            char *at = kv_smem + stage * S::STAGE + h * S::KHALF;
+                            if (i < most) tc::load_3d(at, &k_map, 64 * h, w.kv_head, w.k0 + i * S::KEYS, &sh.full[stage]);
+                            if (i > 0) tc::load_3d(at + S::KVBYTES, &v_map, 64 * h, w.kv_head, w.k0 + (i - 1) * S::KEYS, &sh.full[stage]);
+                        }
+                    }
+                    ++pairs;
+                };
+                auto wait_pair = [&](int i) {
+                    return tc::bar_wait(&sh.full[(pairs0 + i) % S::STAGES], (pairs0 + i) / S::STAGES & 1, gave_up);
+                };
+                // puts zeros in the place of what is not finite among a stage's values
+                auto look_over = [&](int stage) {
+                    constexpr uint32_t EXPONENT = S::BF16 ? 0x7f807f80u : 0x7c007c00u, UNIT = S::BF16 ? 0x00800080u : 0x04000400u;
+                    uint4 *v = reinterpret_cast<uint4 *>(kv_smem + stage * S::STAGE + S::KVBYTES);
+                    auto bad = [&](uint32_t x) { return ((x & EXPONENT) + UNIT) & 0x80008000u; };  // its halves that are not finite
+                    uint32_t any = 0;
 #pragma unroll 8
-                for (int i = lane; i < S::KVBYTES / 16; i += 32) {
-                    const uint4 x = v[i];
-                    any |= bad(x.x) | bad(x.y) | bad(x.z) | bad(x.w);
-                }
-                if (any) {
-                    auto zeroed = [&](uint32_t x) {
-                        const uint32_t b = bad(x);
-                        return x & ~((b >> 15) * 0xffffu);
-                    };
                     for (int i = lane; i < S::KVBYTES / 16; i += 32) {
                         const uint4 x = v[i];
-                        v[i] = make_uint4(zeroed(x.x), zeroed(x.y), zeroed(x.z), zeroed(x.w));
+                        any |= bad(x.x) | bad(x.y) | bad(x.z) | bad(x.w);
                     }
-                    sh.not_finite = 1;
-                    tc::shared_to_async();
-                }
-                __syncwarp();
-            };
+                    if (any) {
+                        auto zeroed = [&](uint32_t x) {
+                            const uint32_t b = bad(x);
+                            return x & ~((b >> 15) * 0xffffu);
+                        };
+                        for (int i = lane; i < S::KVBYTES / 16; i += 32) {
+                            const uint4 x = v[i];
+                            v[i] = make_uint4(zeroed(x.x), zeroed(x.y), zeroed(x.z), zeroed(x.w));
+                        }
+                        sh.not_finite[item & 1] = 1;
+                        tc::shared_to_async();
+                    }
+                    __syncwarp();
+                };
             // Tells the issuer, with the weights of step j, that what the step takes is there: V of tile j, looked over
-            // if need be, and the keys behind it.
-            auto announce = [&](int j) {
-                const int last = S::NQ == 2 ? j + 1 : min(j + 2, most), stage = (j + 1) % S::STAGES;
-                for (int i = j + 1; i <= last && ok; ++i) ok = tc::bar_wait(&sh.full[i % S::STAGES], i / S::STAGES & 1, gave_up);
-                if (ok && j >= first_cut) look_over(stage);
-                for (int b = 0; b < 2 && ok; ++b) {  // once a phase: the one before has to be over
-                    if (S::NQ == 2 ? j >= tiles[b % S::NQ] : b != (j & 1)) continue;
-                    if (j >= 3 - S::NQ) ok = tc::bar_wait(&sh.weights[b], (S::NQ == 2 ? j - 1 : (j >> 1) - 1) & 1, gave_up);
-                    if (ok && lane == 0) tc::bar_arrive(&sh.weights[b]);
+                // if need be, and the keys behind it.
+                auto announce = [&](int j) {
+                    const int last = S::NQ == 2 ? j + 1 : min(j + 2, most);
+                    for (int i = j + 1; i <= last && ok; ++i) ok = wait_pair(i);
+                    if (ok && j >= of.first_cut) look_over((pairs0 + j + 1) % S::STAGES);
+                    for (int t = 0; t < S::NQ && ok; ++t) {  // once a phase: the one before has to be over
+                        if (j >= of.tiles[t]) continue;
+                        const int step = steps[t]++, b = S::NQ == 2 ? t : step & 1, phase = S::NQ == 2 ? step : step >> 1;
+                        if (phase > 0) ok = tc::bar_wait(&sh.weights[b], (phase - 1) & 1, gave_up);
+                        if (ok && lane == 0) tc::bar_arrive(&sh.weights[b]);
+                    }
+                };
+                if (most > 0) load(0);
+                if (most == 0 && lane == 0) tc::bar_arrive(&sh.nearly);
+                for (int j = 0; j < most && ok; ++j) {
+                    load(j + 1);
+                    if (j + 1 == most && ok && lane == 0) tc::bar_arrive(&sh.nearly);
+                    if (S::NQ == 1 && ok && j > 0) announce(j - 1);
+                    if (S::NQ == 2 && ok) announce(j);
                 }
-            };
-            if (most > 0) load(0);
-            for (int j = 0; j < most && ok; ++j) {
-                load(j + 1);
-                if (S::NQ == 1 && ok && j > 0) announce(j - 1);
-                if (S::NQ == 2 && ok) announce(j);
+                if (S::NQ == 1 && ok && most > 0) announce(most - 1);
+                if (ok) finished(item);
             }
-            if (S::NQ == 1 && ok && most > 0) announce(most - 1);
             // nothing may be on its way into shared memory when the block ends
-            if (!ok) {
-                if (most > 0) tc::bar_wait(&sh.q_full, 0, nullptr);
-                for (int i = std::max(0, issued - S::STAGES); i < issued; ++i)
+            if (*gave_up) {
+                if (queries > 0) tc::bar_wait(&sh.q_full, (queries - 1) & 1, nullptr);
+                for (int i = std::max(0, pairs - S::STAGES); i < pairs; ++i)
                     tc::bar_wait(&sh.full[i % S::STAGES], i / S::STAGES & 1, nullptr);
             }
         } else if (warp == kIssuer) {
             // the whole warp goes through this, one lane issues
-            const int rounds = tc::uniform(most), n16 = (p.a.head_dim + 15) / 16;
+            const int n16 = (p.a.head_dim + 15) / 16;
             const uint32_t to = tc::uniform(tmem);
             const uint32_t scores_of = tc::product(S::BF16, kRows, S::KEYS, false, p.negate != 0);
             const uint32_t output_of = tc::product(S::BF16, kRows, 16 * n16, true, false);
             const uint32_t smem_at = tc::uniform(tc::smem_u32(smem));
             const tc::Operand q_at = tc::operand(smem_at, 1024, 0), k_at = tc::operand(smem_at + S::NQ * S::QBYTES, 1024, 0),
                               v_at = tc::operand(smem_at + S::NQ * S::QBYTES, 1024, S::KHALF);
-            auto wait_pair = [&](int i) { return tc::bar_wait(&sh.full[i % S::STAGES], i / S::STAGES & 1, gave_up); };
-            auto free_pair = [&](int i) { tc::commit(&sh.empty[i % S::STAGES]); };
-            // the weights, and all that their step takes
-            auto wait_weights = [&](int buffer, int parity) {
-                const bool there = tc::bar_wait(&sh.weights[buffer], parity, gave_up);
-                tc::fence_after();
-                return there;
-            };
-            // S at column s = Q of tile t times K of tile j
-            auto scores = [&](int t, int j, uint32_t s) {
-                const tc::Operand k = k_at.at(j % S::STAGES * S::STAGE), q = q_at.at(t * S::QBYTES);
+            // The operands' places are constants apart, so that a product of 16 takes its thread a few instructions: with
+            // descriptors made for each the products waited for that thread (about 130 clocks each, where they take 64).
+            // S at column s = Q of tile t times a stage's K
+            auto scores = [&](int t, int stage, uint32_t s) {
+                const tc::Operand k = k_at.at(stage * S::STAGE), q = q_at.at(t * S::QBYTES);
 #pragma unroll
                 for (int i = 0; i < S::DP / 16; ++i)
                     if (i < n16)
                         tc::mma(to + s, q.at((i >> 2) * S::QHALF + (i & 3) * 32), k.at((i >> 2) * S::KHALF + (i & 3) * 32), scores_of,
                                 i > 0);
             };
-            auto output = [&](int t, int j, uint32_t s) {
-                const tc::Operand v = v_at.at((j + 1) % S::STAGES * S::STAGE + S::KVBYTES);
+            // O of tile t (+)= the weights at column s times a stage's V
+            auto output = [&](int t, int stage, uint32_t s, bool add) {
+                const tc::Operand v = v_at.at(stage * S::STAGE + S::KVBYTES);
 #pragma unroll
                 for (int i = 0; i < S::KEYS / 16; ++i)
-                    tc::mma_ts(to + S::O + t * S::DP, to + s + i * 8, v.at(i * 2048), output_of, i > 0 || j > 0);
+                    tc::mma_ts(to + S::O + t * S::DP, to + s + i * 8, v.at(i * 2048), output_of, i > 0 || add);
+            };
+            // the weights, and all that their step takes
+            auto wait_weights = [&](int buffer, int parity) {
+                const bool there = tc::bar_wait(&sh.weights[buffer], parity, gave_up);
+                tc::fence_after();
+                return there;
+            };
+            bool ok = true;
+            Work w;
+            int stage = 0, stage_phase = 0;   // of the next pair
+            int queries = 0, steps[2] = {0, 0};
+            auto pass_stage = [&] {
+                if (++stage == S::STAGES) stage = 0, stage_phase ^= 1;
             };
             // The queue of products is short, and every wait takes this warp 150 clocks and more even where nothing is waited
             // for: it waits once a tile and step.
-            bool ok = rounds == 0 || (tc::bar_wait(&sh.q_full, 0, gave_up) && wait_pair(0));
-            if constexpr (S::NQ == 2) {
-                const int own[2] = {tc::uniform(tiles[0]), tc::uniform(tiles[1])};
-                if (ok && rounds > 0) {
+            for (int item = 0; ok && next(item, w); ++item) {
+                const Item<S> of(p, w);
+                const int rounds = tc::uniform(of.most);
+                if (rounds == 0) {
+                    finished(item);
+                    continue;
+                }
+                ok = tc::bar_wait(&sh.q_full, queries++ & 1, gave_up) && tc::bar_wait(&sh.full[stage], stage_phase, gave_up);
+                if (!ok) break;
+                if constexpr (S::NQ == 2) {
+                    const int own[2] = {tc::uniform(of.tiles[0]), tc::uniform(of.tiles[1])};
                     if (tc::elect()) {
                         for (int t = 0; t < 2; ++t)
-                            if (own[t] > 0) scores(t, 0, t * S::KEYS), tc::commit(&sh.scores[t]);
-                        free_pair(0);
+                            if (own[t] > 0) scores(t, stage, t * S::KEYS), tc::commit(&sh.scores[t]);
+                        tc::commit(&sh.empty[stage]);
+                        if (rounds == 1) tc::commit(&sh.q_empty);
                     }
                     __syncwarp();
-                }
-                for (int j = 0; j < rounds && ok; ++j) {
+                    pass_stage();
+                    for (int j = 0; j < rounds && ok; ++j) {
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (j < own[t]) ok = wait_weights(t, j & 1);
-                        if (!ok) break;
-                        if (tc::elect()) {
-                            if (j < own[t]) {
-                                output(t, j, t * S::KEYS);
-                                if (j + 1 < own[t]) scores(t, j + 1, t * S::KEYS), tc::commit(&sh.scores[t]);
-                                else tc::commit(&sh.done[t]);
+                        for (int t = 0; t < 2; ++t) {
+                            if (j < own[t]) ok = wait_weights(t, (steps[t] + j) & 1);
+                            if (!ok) break;
+                            if (tc::elect()) {
+                                if (j < own[t]) {
+                                    output(t, stage, t * S::KEYS, j > 0);
+                                    if (j + 1 < own[t]) scores(t, stage, t * S::KEYS), tc::commit(&sh.scores[t]);
+                                    else tc::commit(&sh.done[t]);
+                                }
+                                if (t == 1) {
+                                    tc::commit(&sh.empty[stage]);
+                                    if (j + 2 == rounds) tc::commit(&sh.q_empty);
+                                }
                             }
-                            if (t == 1) free_pair(j + 1);
+                            __syncwarp();
+                        }
+                        pass_stage();
+                    }
+                    steps[0] += own[0], steps[1] += own[1];
+                } else {
+                    const int step0 = steps[0];  // step j is step step0 + j of the block, in buffer (step0 + j) % 2
+                    auto buffer = [&](int j) { return (uint32_t)((step0 + j) & 1); };
+                    const int stage0 = stage;
+                    if (tc::elect()) {
+                        scores(0, stage0, buffer(0) * S::KEYS), tc::commit(&sh.scores[buffer(0)]);
+                        tc::commit(&sh.empty[stage0]);
+                        if (rounds == 1) tc::commit(&sh.q_empty);
+                    }
+                    __syncwarp();
+                    pass_stage();
+                    if (rounds > 1) {
+                        ok = tc::bar_wait(&sh.full[stage], stage_phase, gave_up);
+                        if (ok && tc::elect()) {
+                            scores(0, stage, buffer(1) * S::KEYS), tc::commit(&sh.scores[buffer(1)]);
+                            if (rounds == 2) tc::commit(&sh.q_empty);
                         }
                         __syncwarp();
                     }
-                }
-            } else {
-                for (int j = 0; j < 2 && j < rounds && ok; ++j) {
-                    if (j > 0) ok = wait_pair(1);
-                    if (ok && tc::elect()) {
-                        scores(0, j, j * S::KEYS), tc::commit(&sh.scores[j]);
-                        if (j == 0) free_pair(0);
+                    for (int j = 0; j < rounds && ok; ++j) {
+                        ok = wait_weights(buffer(j), (step0 + j) >> 1 & 1);
+                        if (!ok) break;
+                        const int after = stage + 1 == S::STAGES ? 0 : stage + 1;
+                        if (tc::elect()) {
+                            output(0, stage, buffer(j) * S::KEYS, j > 0), tc::commit(&sh.product), tc::commit(&sh.empty[stage]);
+                            if (j + 2 < rounds) scores(0, after, buffer(j) * S::KEYS), tc::commit(&sh.scores[buffer(j)]);
+                            if (j + 3 == rounds) tc::commit(&sh.q_empty);
+                            if (j + 1 == rounds) tc::commit(&sh.done[0]);
+                        }
+                        __syncwarp();
+                        pass_stage();
                     }
-                    __syncwarp();
+                    steps[0] += rounds;
                 }
-                for (int j = 0; j < rounds && ok; ++j) {
-                    ok = wait_weights(j & 1, j >> 1 & 1);
-                    if (!ok) break;
-                    if (tc::elect()) {
-                        output(0, j, (j & 1) * S::KEYS), tc::commit(&sh.product[0]), free_pair(j + 1);
-                        if (j + 2 < rounds) scores(0, j + 2, (j & 1) * S::KEYS), tc::commit(&sh.scores[j & 1]);
-                    }
-                    __syncwarp();
-                }
-                if (rounds > 0 && ok && tc::elect()) tc::commit(&sh.done[0]);
-                __syncwarp();
+                if (ok) finished(item);
             }
-            if (!ok) {  // no product may be under way when its memory is given back
+            if (*gave_up) {  // no product may be under way when its memory is given back
                 if (tc::elect()) tc::commit(&sh.last);
                 __syncwarp();
                 tc::bar_wait(&sh.last, 0, nullptr);
             }
+        } else if (warp == kPlanner) {
+            // Work for the other warps: this block's own, then that of blocks that have not begun, so that loads and first
+            // scores run during the last piece's end.
+            Finder<S> finder;
+            int item = 0, asked = 0;
+            bool ok = true;
+            auto publish = [&](const Work &w) {
+                if (lane == 0) sh.plan[item & 1] = w;
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(&sh.planned[item & 1]);
+                ++item;
+            };
+            for (int number = blockIdx.x; number >= 0 && ok;) {
+                Work w;
+                if (finder.find(p, number, lane, w)) {
+                    if (item >= 2) ok = tc::bar_wait(&sh.taken[item & 1], (item - 2) >> 1 & 1, gave_up);
+                    if (!ok) break;
+                    publish(w);
+                    // No more is taken over before this piece is nearly done: what waits here another block could do
+                    // (asking when a piece begins: 263 us instead of 243 for eight chunks of 512 behind 3,500 to 7,000).
+                    ok = tc::bar_wait(&sh.nearly, (item - 1) & 1, gave_up);
+                    if (!ok) break;
+                }
+                if (lane == 0) tc::ask_block(&sh.answer, &sh.answered);
+                __syncwarp();
+                // waited for by its own time alone: an answer must not come behind the block's end
+                const bool there = tc::bar_wait(&sh.answered, asked++ & 1, nullptr);
+                if (!there) *gave_up = 1, ok = false;
+                number = there ? tc::answered_block(&sh.answer) : -1;
+                tc::shared_to_async();  // read before it is written again
+                __syncwarp();
+            }
+            if (ok && item >= 2) ok = tc::bar_wait(&sh.taken[item & 1], (item - 2) >> 1 & 1, gave_up);
+            if (ok) publish(Work{});
+            if (blockIdx.x == 0)  // the first block looks all requests over
+                for (int r = lane; r < p.a.requests; r += 32) {
+                    Work w;
+                    if (const int flag = Finder<S>::read(p, r, w)) atomicOr(p.a.status, flag);
+                }
         }
     } else {
         if constexpr (S::NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int t = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
         const int in_tile = (int)((__umulhi((uint32_t)row, p.group_mul) + (uint32_t)row) >> p.group_shift);
-        const int token = w.t0 + t * p.tile_tokens + in_tile, head = kv_head * p.group + row - in_tile * p.group;
-        const bool real = in_tile < p.tile_tokens && token < w.nq;
-        const int seen = keys_of(token), n = tiles[t];
-        float m = -INFINITY, l = 0.0f;
+        int steps = 0, pieces = 0;  // of this tile so far; with one tile step s is in buffer s % 2
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            const int buffer = S::NQ == 2 ? t : j & 1;
-            const uint32_t at = lanes + buffer * S::KEYS;
-            ok = tc::bar_wait(&sh.scores[buffer], S::NQ == 2 ? j & 1 : (j >> 1) & 1, gave_up);
-            if (!ok) break;
-            tc::fence_after();
-            const int left = seen - j * S::KEYS;  // keys that the row sees here
-            const bool cut = j >= first_cut;
-            // Loops that few steps go through are not unrolled: the code of a step has to stay in the caches of
-            // instructions beside that of the warp that issues the products.
-            if (cut) {
-#pragma unroll 1
-                for (int c = 0; c < S::KEYS; c += 32) {
-                    float s[32];
-                    tc::load32(at + c, reinterpret_cast<uint32_t *>(s));
-                    tc::load32_wait(reinterpret_cast<uint32_t *>(s));
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (c + i >= left) s[i] = -INFINITY;
-                    tc::store32(at + c, reinterpret_cast<uint32_t *>(s));
-                }
-                tc::store_wait();
-            }
-            // The weights are taken relative to the maximum so far, and the row's own is looked for only where one of
-            // them comes out too large, or nothing was seen before.
-            bool search = __any_sync(0xffffffffu, real && m == -INFINITY);
-            uint32_t weights[S::KEYS / 2];
-            float sum;
-            for (;;) {
-                if (search) {
-                    float high = m;
+        Work w;
+        for (int item = 0; ok && next(item, w); ++item) {
+            const Item<S> of(p, w);
+            const int n = of.tiles[t], first_cut = of.first_cut;
+            const int token = w.t0 + t * p.tile_tokens + in_tile, head = w.kv_head * p.group + row - in_tile * p.group;
+            const bool real = in_tile < p.tile_tokens && token < w.nq;
+            const int seen = Item<S>::keys_of(p, w, token);
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < n; ++j) {
+                const int step = steps + j, buffer = S::NQ == 2 ? t : step & 1;
+                const uint32_t at = lanes + buffer * S::KEYS;
+                ok = tc::bar_wait(&sh.scores[buffer], S::NQ == 2 ? step & 1 : step >> 1 & 1, gave_up);
+                if (!ok) break;
+                tc::fence_after();
+                const int left = seen - j * S::KEYS;  // keys that the row sees here
+                const bool cut = j >= first_cut;
+                // Loops that few steps go through are not unrolled: the code of a step has to stay in the caches of
+                // instructions beside that of the warp that issues the products.
+                if (cut) {
 #pragma unroll 1
                     for (int c = 0; c < S::KEYS; c += 32) {
                         float s[32];
                         tc::load32(at + c, reinterpret_cast<uint32_t *>(s));
                         tc::load32_wait(reinterpret_cast<uint32_t *>(s));
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) high = fmaxf(high, s[i]);
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i >= left) s[i] = -INFINITY;
+                        tc::store32(at + c, reinterpret_cast<uint32_t *>(s));
                     }
-                    const bool raise = real && (high - m) * p.scale2 > S::RAISE;
-                    if (__any_sync(0xffffffffu, raise)) {
-                        const float keep = raise ? (m == -INFINITY ? 0.0f : pow2((m - high) * p.scale2)) : 1.0f;
-                        if (raise) m = high;
-                        l *= keep;
-                        if (j > 0) {
-                            if constexpr (S::NQ == 1) {  // with two tiles the barrier of S says it
-                                ok = tc::bar_wait(&sh.product[0], (j - 1) & 1, gave_up);
-                                if (!ok) break;
-                                tc::fence_after();
-                            }
-                            const uint32_t o_at = lanes + S::O + t * S::DP;
+                    tc::store_wait();
+                }
+                // The weights are taken relative to the maximum so far, and the row's own is looked for only where one of
+                // them comes out too large, or nothing was seen before.
+                bool search = __any_sync(0xffffffffu, real && m == -INFINITY);
+                uint32_t weights[S::KEYS / 2];
+                float sum;
+                for (;;) {
+                    if (search) {
+                        float high = m;
 #pragma unroll 1
-                            for (int c = 0; c < p.a.head_dim; c += 32) {
-                                uint32_t o[32];
-                                tc::load32(o_at + c, o);
-                                tc::load32_wait(o);
+                        for (int c = 0; c < S::KEYS; c += 32) {
+                            float s[32];
+                            tc::load32(at + c, reinterpret_cast<uint32_t *>(s));
+                            tc::load32_wait(reinterpret_cast<uint32_t *>(s));
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                                tc::store32(o_at + c, o);
+                            for (int i = 0; i < 32; ++i) high = fmaxf(high, s[i]);
+                        }
+                        const bool raise = real && (high - m) * p.scale2 > S::RAISE;
+                        if (__any_sync(0xffffffffu, raise)) {
+                            const float keep = raise ? (m == -INFINITY ? 0.0f : pow2((m - high) * p.scale2)) : 1.0f;
+                            if (raise) m = high;
+                            l *= keep;
+                            if (j > 0) {
+                                if constexpr (S::NQ == 1) {  // with two tiles the barrier of S says it
+                                    ok = tc::bar_wait(&sh.product, (step - 1) & 1, gave_up);
+                                    if (!ok) break;
+                                    tc::fence_after();
+                                }
+                                const uint32_t o_at = lanes + S::O + t * S::DP;
+#pragma unroll 1
+                                for (int c = 0; c < p.a.head_dim; c += 32) {
+                                    uint32_t o[32];
+                                    tc::load32(o_at + c, o);
+                                    tc::load32_wait(o);
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                                    tc::store32(o_at + c, o);
+                                }
                             }
                         }
                     }
-                }
-                const float base = m == -INFINITY ? 0.0f : m;
-                const uint64_t minus = tc::pair(-base, -base), by = tc::pair(p.scale2, p.scale2), lift = tc::pair(S::LIFT, S::LIFT);
-                uint64_t sums[2] = {0, 0};
-                float top = 0.0f, s[2][32];
-                tc::load32(at, reinterpret_cast<uint32_t *>(s[0]));
+                    const float base = m == -INFINITY ? 0.0f : m;
+                    const uint64_t minus = tc::pair(-base, -base), by = tc::pair(p.scale2, p.scale2), lift = tc::pair(S::LIFT, S::LIFT);
+                    uint64_t sums[2] = {0, 0};
+                    float top = 0.0f, s[2][32];
+                    tc::load32(at, reinterpret_cast<uint32_t *>(s[0]));
 #pragma unroll
-                for (int c = 0; c < S::KEYS; c += 32) {
-                    float *x = s[c / 32 % 2];
-                    tc::load32_wait(reinterpret_cast<uint32_t *>(x));
-                    if (c + 32 < S::KEYS) tc::load32(at + c + 32, reinterpret_cast<uint32_t *>(s[(c / 32 + 1) % 2]));
+                    for (int c = 0; c < S::KEYS; c += 32) {
+                        float *x = s[c / 32 % 2];
+                        tc::load32_wait(reinterpret_cast<uint32_t *>(x));
+                        if (c + 32 < S::KEYS) tc::load32(at + c + 32, reinterpret_cast<uint32_t *>(s[(c / 32 + 1) % 2]));
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float a, b;
-                        tc::unpair(tc::fma2(tc::add2(tc::pair(x[i], x[i + 1]), minus), by, lift), a, b);
-                        a = pow2(a), b = pow2(b);
-                        top = fmaxf(top, fmaxf(a, b));
-                        sums[i / 2 % 2] = tc::add2(sums[i / 2 % 2], tc::pair(a, b));
-                        weights[(c + i) / 2] = pack<T>(a, b);
+                        for (int i = 0; i < 32; i += 2) {
+                            float a, b;
+                            tc::unpair(tc::fma2(tc::add2(tc::pair(x[i], x[i + 1]), minus), by, lift), a, b);
+                            a = pow2(a), b = pow2(b);
+                            top = fmaxf(top, fmaxf(a, b));
+                            sums[i / 2 % 2] = tc::add2(sums[i / 2 % 2], tc::pair(a, b));
+                            weights[(c + i) / 2] = pack<T>(a, b);
+                        }
                     }
+                    float a, b;
+                    tc::unpair(tc::add2(sums[0], sums[1]), a, b);
+                    sum = a + b;
+                    if (search || !__any_sync(0xffffffffu, real && top > S::LIMIT)) break;
+                    search = true;
                 }
-                float a, b;
-                tc::unpair(tc::add2(sums[0], sums[1]), a, b);
-                sum = a + b;
-                if (search || !__any_sync(0xffffffffu, real && top > S::LIMIT)) break;
-                search = true;
+                if (!ok) break;
+                l += sum;
+#pragma unroll
+                for (int c = 0; c < S::KEYS / 2; c += 32) tc::store32(at + c, weights + c);
+                tc::store_wait();
+                tc::fence_before();
+                tc::bar_arrive(&sh.weights[buffer]);
             }
-            if (!ok) break;
-            l += sum;
-#pragma unroll
-            for (int c = 0; c < S::KEYS / 2; c += 32) tc::store32(at + c, weights + c);
-            tc::store_wait();
-            tc::fence_before();
-            tc::bar_arrive(&sh.weights[buffer]);
-        }
-        if (n > 0 && ok) {
-            ok = tc::bar_wait(&sh.done[t], 0, gave_up);
-            tc::fence_after();
-            // over long since; what the loading warp noted before it arrived here is read below
-            ok = ok && tc::bar_wait(&sh.weights[S::NQ == 2 ? t : (n - 1) & 1], (S::NQ == 2 ? n - 1 : (n - 1) >> 1) & 1, gave_up);
-        }
-        if (ok && w.t0 + t * p.tile_tokens < w.nq) {
-            T *out = static_cast<T *>(p.a.out) + (int64_t)(w.q0 + token) * p.a.out_stride[0] + head * p.a.out_stride[1];
-            const T *v = static_cast<const T *>(p.a.v) + (int64_t)w.k0 * p.a.v_stride[0] + kv_head * p.a.v_stride[1];
-            const float inverse = l == 0.0f ? 0.0f : 1.0f / l;
-            for (int c = 0; c < p.a.head_dim; c += 32) {
-                uint32_t o[32];
-                if (n > 0) {
-                    tc::load32(lanes + S::O + t * S::DP + c, o);
-                    tc::load32_wait(o);
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = n > 0 ? __float_as_uint(__uint_as_float(o[i]) * inverse) : 0u;
-                if (!real) continue;
-                if (sh.not_finite) {  // values that are not finite and seen by this row
-                    for (int k = first_cut * S::KEYS; k < seen; ++k)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i < p.a.head_dim) {
-                                const float x = to_float(v[k * p.a.v_stride[0] + c + i]);
-                                if (!(fabsf(x) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
-                            }
-                }
-#pragma unroll
-                for (int i = 0; i < 32; i += 8)
-                    if (c + i < p.a.head_dim)
-                        *reinterpret_cast<uint4 *>(out + c + i) =
-                            make_uint4(pack<T>(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), pack<T>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3])),
-                                       pack<T>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5])), pack<T>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
+            if (n > 0 && ok) {
+                ok = tc::bar_wait(&sh.done[t], pieces++ & 1, gave_up);
+                tc::fence_after();
+                // over long since; what the loading warp noted before it arrived here is read below
+                const int step = steps + n - 1;
+                ok = ok && tc::bar_wait(&sh.weights[S::NQ == 2 ? t : step & 1], S::NQ == 2 ? step & 1 : step >> 1 & 1, gave_up);
             }
-            if (real && p.a.lse)
-                p.a.lse[(int64_t)(w.q0 + token) * p.a.q_heads + head] =
-                    l == 0.0f ? -INFINITY : fmaf(m == -INFINITY ? 0.0f : m, p.scale2, log2f(l) - S::LIFT) * kLn2;
+            steps += n;
+            if (ok && w.t0 + t * p.tile_tokens < w.nq) {
+                T *out = static_cast<T *>(p.a.out) + (int64_t)(w.q0 + token) * p.a.out_stride[0] + head * p.a.out_stride[1];
+                const T *v = static_cast<const T *>(p.a.v) + (int64_t)w.k0 * p.a.v_stride[0] + w.kv_head * p.a.v_stride[1];
+                const float inverse = l == 0.0f ? 0.0f : 1.0f / l;
+                for (int c = 0; c < p.a.head_dim; c += 32) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        tc::load32(lanes + S::O + t * S::DP + c, o);
+                        tc::load32_wait(o);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = n > 0 ? __float_as_uint(__uint_as_float(o[i]) * inverse) : 0u;
+                    if (!real) continue;
+                    if (n > 0 && sh.not_finite[item & 1]) {  // values that are not finite and seen by this row
+                        for (int k = first_cut * S::KEYS; k < seen; ++k)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i < p.a.head_dim) {
+                                    const float x = to_float(v[k * p.a.v_stride[0] + c + i]);
+                                    if (!(fabsf(x) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+                                }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        if (c + i < p.a.head_dim)
+                            *reinterpret_cast<uint4 *>(out + c + i) =
+                                make_uint4(pack<T>(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), pack<T>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3])),
+                                           pack<T>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5])), pack<T>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
+                }
+                if (real && p.a.lse)
+                    p.a.lse[(int64_t)(w.q0 + token) * p.a.q_heads + head] =
+                        l == 0.0f ? -INFINITY : fmaf(m == -INFINITY ? 0.0f : m, p.scale2, log2f(l) - S::LIFT) * kLn2;
+            }
+            if (ok) finished(item);
         }
     }
     tc::fence_before();
