@@ -817,8 +817,18 @@ typedef struct {
     float *lse;                     /* [tokens * q_heads], or null */
     int32_t *status;                /* device int32; flags are OR-ed in.  Bit 0: a request's queries are
                                        not rows of q, bit 1: its keys are not rows of k; such a request
-                                       is left out, its rows of out stay as they were */
+                                       is left out, its rows of out stay as they were.  Bit 2: a wait
+                                       inside the kernel ran out (a second), and out is not complete */
+    void *workspace;                /* spmv_prompt_attention_workspace bytes (fewer serve in part), 16-byte
+                                       aligned, or null: where few queries leave SMs without work, their
+                                       keys are cut into shares as far as it goes.  Its contents do not
+                                       matter; calls that may overlap on the GPU need workspaces of their
+                                       own */
+    size_t workspace_bytes;
 } spmv_prompt_attention_t;
+
+/* Bytes of workspace (HOST *bytes) that spmv_prompt_attention has use for, on the current device. */
+spmv_status_t spmv_prompt_attention_workspace(int32_t q_heads, int32_t kv_heads, int32_t head_dim, spmv_elem_t elem, size_t *bytes);
 
 /* args is a HOST structure, read before the call returns.
  * Errors: INVALID_ARG, CUDA.  No requests, tokens or heads: nothing is done. */

@@ -152,6 +152,7 @@ def _load(path: str) -> ctypes.CDLL:
         "spmv_paged_load": [i32, i32, i32, i32, ctypes.c_int, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp],
         "spmv_paged_attention_e4m3_workspace": [i32, i32, i32, i32, ctypes.c_int, ctypes.POINTER(sz)],
         "spmv_paged_attention_e4m3": [vp, i32, vp, vp, vp, vp, vp],
+        "spmv_prompt_attention_workspace": [i32, i32, i32, ctypes.c_int, ctypes.POINTER(sz)],
         "spmv_prompt_attention": [vp, vp],
     }
     for name, args in sigs.items():

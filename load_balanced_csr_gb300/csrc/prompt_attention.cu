@@ -52,10 +52,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 128;
 
-// DP: the head's elements rounded up to 64; NQ: tiles of a block.
-template <typename T_, int DP_, int NQ_>
+// DP: the head's elements rounded up to 64; NQ: tiles of a block; CUT: the keys of its work are cut into shares.
+template <typename T_, int DP_, int NQ_, bool CUT_>
 struct Shape {
     using T = T_;
+    static constexpr bool CUT = CUT_;
     static constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
     static constexpr int DP = DP_, NQ = NQ_, KEYS = NQ == 2 ? 128 : 64, HALVES = DP / 64;
     static constexpr int THREADS = NQ * 128 + 128;  // two of the last four warps have nothing to do
@@ -65,9 +66,10 @@ struct Shape {
     static constexpr int STAGES = DP == 64 ? 4 : DP == 192 ? 3 : 2, STAGE = 2 * KVBYTES;
     static constexpr int SMEM = 1024 + NQ * QBYTES + STAGES * STAGE;
     static constexpr uint32_t O = NQ == 2 ? 256 : 128;                    // columns of tensor memory: S at 0 and KEYS, then O
-    // Weights are 2^LIFT times as large, and up to 2^RAISE times that before the maximum is raised.  bf16 has the
-    // range of 32 bits; in f16 the largest stay below 2^15, and the smallest step is 2^-35 of a row's largest.
-    static constexpr float LIFT = BF16 ? 0.0f : 11.0f, RAISE = BF16 ? 8.0f : 4.0f, LIMIT = BF16 ? 256.0f : 32768.0f;
+    // Weights are 2^LIFT times as large.  The maximum they are relative to is raised where a score is RAISE powers of
+    // two above it, and looked for where a weight (f16), or a step's sum (bf16), is above LIMIT.  bf16 has the range of
+    // 32 bits; f16's weights stay below 2^15, and its smallest step is 2^-35 of a row's largest.
+    static constexpr float LIFT = BF16 ? 0.0f : 11.0f, RAISE = BF16 ? 8.0f : 4.0f, LIMIT = BF16 ? 0x1p40f : 0x1p15f;
 };
 
 struct PromptArgs {
@@ -76,7 +78,12 @@ struct PromptArgs {
     uint32_t group_mul, group_shift;
     float scale2;                // |scale| / ln 2
     uint32_t negate;             // scale < 0
+    int32_t splits;              // shares that each block's keys are cut into
+    int64_t rows;                // tokens * q_heads
+    float *sums, *stats;         // workspace of cut rows: [splits][rows][head_dim] sums, [splits][rows][2] m and l
 };
+constexpr int kLeast = 4;      // tiles of keys that a share has at least
+constexpr int kMostSplits = 32;
 
 __device__ __forceinline__ float pow2(float x) {
     float y;
@@ -103,7 +110,7 @@ __device__ __forceinline__ uint32_t pack<__half>(float lo, float hi) {
 struct Work {
     int q0, nq, k0, nk;  // the request's rows
     int t0;              // the first token in it
-    int kv_head;
+    int kv_head, split;
     int more;            // 0: there is no more, and the rest says nothing
 };
 
@@ -125,7 +132,7 @@ struct Finder {
     }
     // by a whole warp
     __device__ __forceinline__ bool find(const PromptArgs &p, int number, int lane, Work &work) {
-        const int block_tokens = S::NQ * p.tile_tokens, block = number / p.a.kv_heads;
+        const int whole = S::CUT ? number / p.splits : number, block_tokens = S::NQ * p.tile_tokens, block = whole / p.a.kv_heads;
         if (block < before) base = before = 0;
         for (; base < p.a.requests; base += 32 * EACH) {
             Work w[EACH];
@@ -162,7 +169,7 @@ struct Finder {
                 work.q0 = __shfl_sync(0xffffffffu, work.q0, from), work.nq = __shfl_sync(0xffffffffu, work.nq, from);
                 work.k0 = __shfl_sync(0xffffffffu, work.k0, from), work.nk = __shfl_sync(0xffffffffu, work.nk, from);
                 work.t0 = __shfl_sync(0xffffffffu, work.t0, from);
-                work.kv_head = number - block * p.a.kv_heads;
+                work.kv_head = whole - block * p.a.kv_heads, work.split = S::CUT ? number - whole * p.splits : 0;
                 work.more = 1;
                 return true;
             }
@@ -175,6 +182,7 @@ struct Finder {
 // What a piece of work is to a block.
 template <class S>
 struct Item {
+    int begin;         // its first tile of keys; the others are counted from there
     int tiles[S::NQ];  // tiles of keys that a tile of queries sees
     int most;          // of them all
     int first_cut;     // the first that some of the rows see in part
@@ -183,14 +191,24 @@ struct Item {
         return p.a.causal ? min(w.nk, max(0, token + w.nk - w.nq + 1)) : w.nk;
     }
     __device__ __forceinline__ Item(const PromptArgs &p, const Work &w) {
-        most = 0;
+        int all = 0;
 #pragma unroll
         for (int t = 0; t < S::NQ; ++t) {
             const int first = w.t0 + t * p.tile_tokens, last = min(first + p.tile_tokens, w.nq) - 1;
             tiles[t] = last < first ? 0 : (keys_of(p, w, last) + S::KEYS - 1) / S::KEYS;
-            most = max(most, tiles[t]);
+            all = max(all, tiles[t]);
         }
+        begin = 0, most = all;
         first_cut = keys_of(p, w, w.t0) / S::KEYS;
+        if constexpr (S::CUT) {  // the shares that there are tiles for, as equal as they go
+            const int shares = min(p.splits, max(1, all / kLeast));
+            begin = w.split < shares ? (int)((int64_t)all * w.split / shares) : all;
+            const int end = w.split < shares ? (int)((int64_t)all * (w.split + 1) / shares) : all;
+            most = 0;
+#pragma unroll
+            for (int t = 0; t < S::NQ; ++t) tiles[t] = max(0, min(tiles[t], end) - begin), most = max(most, tiles[t]);
+            first_cut = max(0, first_cut - begin);
+        }
     }
 };
 
@@ -285,8 +303,8 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                         tma::mbar_expect_tx(&sh.full[stage], ((i < most) + (i > 0)) * S::KVBYTES);
                         for (int h = 0; h < S::HALVES; ++h) {
                             char *at = kv_smem + stage * S::STAGE + h * S::KHALF;
-                            if (i < most) tc::load_3d(at, &k_map, 64 * h, w.kv_head, w.k0 + i * S::KEYS, &sh.full[stage]);
-                            if (i > 0) tc::load_3d(at + S::KVBYTES, &v_map, 64 * h, w.kv_head, w.k0 + (i - 1) * S::KEYS, &sh.full[stage]);
+                            if (i < most) tc::load_3d(at, &k_map, 64 * h, w.kv_head, w.k0 + (of.begin + i) * S::KEYS, &sh.full[stage]);
+                            if (i > 0) tc::load_3d(at + S::KVBYTES, &v_map, 64 * h, w.kv_head, w.k0 + (of.begin + i - 1) * S::KEYS, &sh.full[stage]);
                         }
                     }
                     ++pairs;
@@ -525,7 +543,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             const int n = of.tiles[t], first_cut = of.first_cut;
             const int token = w.t0 + t * p.tile_tokens + in_tile, head = w.kv_head * p.group + row - in_tile * p.group;
             const bool real = in_tile < p.tile_tokens && token < w.nq;
-            const int seen = Item<S>::keys_of(p, w, token);
+            const int seen = Item<S>::keys_of(p, w, token) - of.begin * S::KEYS;  // of its share's keys and those behind
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < n; ++j) {
                 const int step = steps + j, buffer = S::NQ == 2 ? t : step & 1;
@@ -593,7 +611,8 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     const float base = m == -INFINITY ? 0.0f : m;
                     const uint64_t minus = tc::pair(-base, -base), by = tc::pair(p.scale2, p.scale2), lift = tc::pair(S::LIFT, S::LIFT);
                     uint64_t sums[2] = {0, 0};
-                    float top = 0.0f, s[2][32];
+                    float s[2][32];
+                    __half2 top = __float2half2_rn(0.0f);
                     tc::load32(at, reinterpret_cast<uint32_t *>(s[0]));
 #pragma unroll
                     for (int c = 0; c < S::KEYS; c += 32) {
@@ -605,15 +624,20 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                             float a, b;
                             tc::unpair(tc::fma2(tc::add2(tc::pair(x[i], x[i + 1]), minus), by, lift), a, b);
                             a = pow2(a), b = pow2(b);
-                            top = fmaxf(top, fmaxf(a, b));
                             sums[i / 2 % 2] = tc::add2(sums[i / 2 % 2], tc::pair(a, b));
-                            weights[(c + i) / 2] = pack<T>(a, b);
+                            const uint32_t w = weights[(c + i) / 2] = pack<T>(a, b);
+                            if constexpr (!S::BF16) {
+                                __half2 h;
+                                memcpy(&h, &w, 4);
+                                top = __hmax2(top, h);
+                            }
                         }
                     }
                     float a, b;
                     tc::unpair(tc::add2(sums[0], sums[1]), a, b);
                     sum = a + b;
-                    if (search || !__any_sync(0xffffffffu, real && top > S::LIMIT)) break;
+                    const float largest = S::BF16 ? sum : fmaxf(__low2float(top), __high2float(top));
+                    if (search || !__any_sync(0xffffffffu, real && largest > S::LIMIT)) break;
                     search = true;
                 }
                 if (!ok) break;
@@ -634,9 +658,10 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             steps += n;
             if (ok && w.t0 + t * p.tile_tokens < w.nq) {
                 T *out = static_cast<T *>(p.a.out) + (int64_t)(w.q0 + token) * p.a.out_stride[0] + head * p.a.out_stride[1];
-                const T *v = static_cast<const T *>(p.a.v) + (int64_t)w.k0 * p.a.v_stride[0] + w.kv_head * p.a.v_stride[1];
-                const float inverse = l == 0.0f ? 0.0f : 1.0f / l;
-                for (int c = 0; c < p.a.head_dim; c += 32) {
+                const T *v = static_cast<const T *>(p.a.v) + (int64_t)(w.k0 + of.begin * S::KEYS) * p.a.v_stride[0] + w.kv_head * p.a.v_stride[1];
+                const float inverse = S::CUT ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+                const int64_t part = S::CUT ? w.split * p.rows + (int64_t)(w.q0 + token) * p.a.q_heads + head : 0;
+                for (int c = 0; c < p.a.head_dim && (!S::CUT || n > 0); c += 32) {
                     uint32_t o[32];
                     if (n > 0) {
                         tc::load32(lanes + S::O + t * S::DP + c, o);
@@ -646,13 +671,20 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     for (int i = 0; i < 32; ++i) o[i] = n > 0 ? __float_as_uint(__uint_as_float(o[i]) * inverse) : 0u;
                     if (!real) continue;
                     if (n > 0 && sh.not_finite[item & 1]) {  // values that are not finite and seen by this row
-                        for (int k = first_cut * S::KEYS; k < seen; ++k)
+                        for (int k = first_cut * S::KEYS; k < (S::CUT ? min(seen, n * S::KEYS) : seen); ++k)
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (c + i < p.a.head_dim) {
                                     const float x = to_float(v[k * p.a.v_stride[0] + c + i]);
                                     if (!(fabsf(x) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
                                 }
+                    }
+                    if constexpr (S::CUT) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            if (c + i < p.a.head_dim)
+                                *reinterpret_cast<uint4 *>(p.sums + part * p.a.head_dim + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        continue;
                     }
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
@@ -661,7 +693,9 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                                 make_uint4(pack<T>(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), pack<T>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3])),
                                            pack<T>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5])), pack<T>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
                 }
-                if (real && p.a.lse)
+                if constexpr (S::CUT) {
+                    if (real) *reinterpret_cast<float2 *>(p.stats + 2 * part) = make_float2(m, l);
+                } else if (real && p.a.lse)
                     p.a.lse[(int64_t)(w.q0 + token) * p.a.q_heads + head] =
                         l == 0.0f ? -INFINITY : fmaf(m == -INFINITY ? 0.0f : m, p.scale2, log2f(l) - S::LIFT) * kLn2;
             }
@@ -675,6 +709,62 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         tc::fence_after();
         tc::dealloc(tmem, 512);
     }
+}
+
+// ---------------------------------------------------------------- rows that were cut
+// A warp joins a row's shares in their order, each weighted by its maximum's
+// distance from the largest.
+constexpr int kJoinWarps = 8;
+template <typename T>
+__global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptArgs p, float lift) {
+    after_previous();
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+    if (row >= p.rows) return;
+    const int64_t token = row / p.a.q_heads;
+    const int head = (int)(row - token * p.a.q_heads);
+    bool mine = false;  // the row is some request's
+    for (int r0 = 0; r0 < p.a.requests && !mine; r0 += 32) {
+        const int r = r0 + lane;
+        bool in = false;
+        if (r < p.a.requests) {
+            const int32_t *kv_ptr = p.a.kv_ptr ? p.a.kv_ptr : p.a.q_ptr;
+            const int q0 = p.a.q_ptr[r], q1 = p.a.q_ptr[r + 1], k0 = kv_ptr[r], k1 = kv_ptr[r + 1];
+            in = q0 >= 0 && q0 <= token && token < q1 && q1 <= p.a.tokens && k0 >= 0 && k1 >= k0 && k1 <= p.a.keys;
+        }
+        mine = __any_sync(0xffffffffu, in);
+    }
+    if (!mine) return;
+    float m = -INFINITY, l = 0.0f;
+    if (lane < p.splits) {
+        const float2 stat = *reinterpret_cast<const float2 *>(p.stats + 2 * (lane * p.rows + row));
+        m = stat.x, l = stat.y;
+    }
+    float high = m;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
+    // a share without weights has no sums either
+    const float weight = l == 0.0f ? 0.0f : m == -INFINITY ? 1.0f : pow2((m - high) * p.scale2);
+    float sum = l * weight;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const uint32_t there = __ballot_sync(0xffffffffu, !(l == 0.0f));
+    const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
+    T *out = static_cast<T *>(p.a.out) + token * p.a.out_stride[0] + head * p.a.out_stride[1];
+    for (int c0 = 0; c0 < p.a.head_dim; c0 += 128) {
+        const int c = c0 + lane * 4;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int i = 0; i < p.splits; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, weight, i);
+            if (!(there >> i & 1) || c >= p.a.head_dim) continue;
+            const float4 x = *reinterpret_cast<const float4 *>(p.sums + (i * p.rows + row) * p.a.head_dim + c);
+            o.x = fmaf(wi, x.x, o.x), o.y = fmaf(wi, x.y, o.y), o.z = fmaf(wi, x.z, o.z), o.w = fmaf(wi, x.w, o.w);
+        }
+        if (c < p.a.head_dim)
+            *reinterpret_cast<uint2 *>(out + c) = make_uint2(pack<T>(o.x * inverse, o.y * inverse), pack<T>(o.z * inverse, o.w * inverse));
+    }
+    if (lane == 0 && p.a.lse) p.a.lse[row] = sum == 0.0f ? -INFINITY : fmaf(high == -INFINITY ? 0.0f : high, p.scale2, log2f(sum) - lift) * kLn2;
 }
 
 // ---------------------------------------------------------------- launch
@@ -706,8 +796,9 @@ bool make_map(CUtensorMap *map, bool bf16, const void *at, int head_dim, int hea
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class S>
+template <typename T, int DP, int NQ>
 spmv_status_t launch_prompt(const spmv_prompt_attention_t &a, cudaStream_t stream) {
+    using S = Shape<T, DP, NQ, false>;
     PromptArgs p;
     p.a = a;
     p.group = a.q_heads / a.kv_heads;
@@ -722,18 +813,35 @@ spmv_status_t launch_prompt(const spmv_prompt_attention_t &a, cudaStream_t strea
         !make_map(&maps[1], S::BF16, keys ? a.k : a.q, a.head_dim, a.kv_heads, std::max(a.keys, 1), a.k_stride, 1, S::KEYS) ||
         !make_map(&maps[2], S::BF16, keys ? a.v : a.q, a.head_dim, a.kv_heads, std::max(a.keys, 1), a.v_stride, 1, S::KEYS))
         return llm_fail(SPMV_ERR_CUDA, "spmv_prompt_attention: the driver refused a tensor map");
-    const int64_t blocks = ((int64_t)a.tokens / (S::NQ * p.tile_tokens) + std::min(a.requests, a.tokens)) * a.kv_heads;
-    cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-    if (e == cudaSuccess)
-        e = launch_chained(prompt_attention_kernel<S>, (unsigned)blocks, S::THREADS, S::SMEM, 0, stream, p, maps[0], maps[1], maps[2]);
+    // no more pieces of work than this, whatever the lengths
+    const int64_t block_tokens = S::NQ * p.tile_tokens, requests = std::min(a.requests, a.tokens);
+    const int64_t pieces = (a.tokens + requests * (block_tokens - 1)) / block_tokens * a.kv_heads;
+    // Few pieces leave most SMs without work: each one's keys are cut into shares then, as far as there are SMs, workspace,
+    // keys (a share has four tiles at least) and bits to count them; a second kernel joins them.  64 queries behind 60,000
+    // keys, 32 over 8 heads of 128: 487 us uncut.
+    const int64_t sms = std::max(1, device_sm_count()), row_bytes = 4 * ((int64_t)a.head_dim + 2);
+    p.rows = (int64_t)a.tokens * a.q_heads;
+    const int64_t room = a.workspace ? (int64_t)std::min<uint64_t>(a.workspace_bytes, 1ull << 40) / (row_bytes * p.rows) : 0;
+    p.splits = (int)std::max<int64_t>(1, std::min(std::min(sms / pieces, room), std::min<int64_t>(kMostSplits, a.keys / (kLeast * S::KEYS))));
+    p.sums = static_cast<float *>(a.workspace);
+    p.stats = p.sums + p.splits * p.rows * a.head_dim;
+    auto launch = [&](auto kernel) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        return e != cudaSuccess ? e
+                                : launch_chained(kernel, (unsigned)(pieces * p.splits), S::THREADS, S::SMEM, 0, stream, p, maps[0], maps[1], maps[2]);
+    };
+    cudaError_t e = p.splits == 1 ? launch(prompt_attention_kernel<S>) : launch(prompt_attention_kernel<Shape<T, DP, NQ, true>>);
+    if (e == cudaSuccess && p.splits > 1)
+        e = launch_chained(prompt_join_kernel<T>, (unsigned)((p.rows + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, 0, stream, p,
+                           S::LIFT);
     return llm_launched("spmv_prompt_attention launch", e);
 }
 template <typename T>
 spmv_status_t launch_prompt_of(const spmv_prompt_attention_t &a, cudaStream_t stream) {
-    if (a.head_dim <= 64) return launch_prompt<Shape<T, 64, 2>>(a, stream);
-    if (a.head_dim <= 128) return launch_prompt<Shape<T, 128, 2>>(a, stream);
-    if (a.head_dim <= 192) return launch_prompt<Shape<T, 192, 1>>(a, stream);
-    return launch_prompt<Shape<T, 256, 1>>(a, stream);
+    if (a.head_dim <= 64) return launch_prompt<T, 64, 2>(a, stream);
+    if (a.head_dim <= 128) return launch_prompt<T, 128, 2>(a, stream);
+    if (a.head_dim <= 192) return launch_prompt<T, 192, 1>(a, stream);
+    return launch_prompt<T, 256, 1>(a, stream);
 }
 
 const char *prompt_bad(const spmv_prompt_attention_t &a) {
@@ -748,6 +856,7 @@ const char *prompt_bad(const spmv_prompt_attention_t &a) {
     if (a.keys > 0 && (!a.k || !a.v)) return "k or v is NULL";
     if (!aligned_to(a.q_ptr, 4) || !aligned_to(a.kv_ptr, 4) || !aligned_to(a.lse, 4) || !aligned_to(a.status, 4))
         return "q_ptr, kv_ptr, lse or status is not aligned to its type";
+    if (a.workspace && !aligned_to(a.workspace, 16)) return "the workspace must be 16-byte aligned";
     if (!aligned_to(a.q, 16) || !aligned_to(a.k, 16) || !aligned_to(a.v, 16) || !aligned_to(a.out, 16))
         return "q, k, v and out must be 16-byte aligned";
     for (int i = 0; i < 2; ++i)
@@ -768,6 +877,19 @@ const char *prompt_bad(const spmv_prompt_attention_t &a) {
 using namespace lbcsr;
 
 extern "C" {
+
+spmv_status_t spmv_prompt_attention_workspace(int32_t q_heads, int32_t kv_heads, int32_t head_dim, spmv_elem_t elem, size_t *bytes) {
+    if (!bytes) return llm_bad("bytes is NULL");
+    *bytes = 0;
+    spmv_prompt_attention_t a = {};
+    a.q_heads = q_heads, a.kv_heads = kv_heads, a.head_dim = head_dim, a.elem = elem;
+    if (const char *bad = prompt_bad(a)) return llm_bad(bad);
+    const int sms = device_sm_count();
+    if (sms <= 0) return llm_fail(SPMV_ERR_CUDA, "no CUDA device");
+    // the rows of as many pieces of work as there are SMs
+    *bytes = (size_t)sms * (head_dim <= 128 ? 2 : 1) * kRows * 4 * (head_dim + 2);
+    return SPMV_OK;
+}
 
 spmv_status_t spmv_prompt_attention(const spmv_prompt_attention_t *args, spmv_stream_t stream_handle) {
     if (!args) return llm_bad("args is NULL");

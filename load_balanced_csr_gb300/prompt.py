@@ -26,13 +26,16 @@ class PromptAttentionArgs(ctypes.Structure):
                 ("elem", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
                 ("q_stride", _I64x2), ("k_stride", _I64x2), ("v_stride", _I64x2), ("out_stride", _I64x2),
                 ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_ptr", ctypes.c_void_p),
-                ("kv_ptr", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+                ("kv_ptr", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
 class PromptAttention:
     """Attention of up to ``max_requests`` packed prompts, bfloat16 or
-    float16.  Keep the object until its calls have run; calls of one object
-    may overlap on the GPU, host threads need objects of their own."""
+    float16.  Keeps the workspace that joins the shares of queries whose keys
+    are cut between blocks: calls that may overlap on the GPU (two streams)
+    need objects of their own, and an object is kept until its calls have
+    run."""
 
     def __init__(self, max_requests: int, q_heads: int, kv_heads: int, head_dim: int, dtype, device="cuda"):
         self._L, self.device, self.dtype = lib(), _launch.cuda_device(device), dtype
@@ -43,10 +46,12 @@ class PromptAttention:
         self.max_requests = int(max_requests)
         self.q_heads, self.kv_heads, self.head_dim = int(q_heads), int(kv_heads), int(head_dim)
         a.q_heads, a.kv_heads, a.head_dim = self.q_heads, self.kv_heads, self.head_dim
-        # what no call could be made with is refused here
-        _launch.call(self._L.spmv_prompt_attention, "spmv_prompt_attention", self.device, ctypes.byref(a), 0)
+        size = ctypes.c_size_t()
+        _launch.call(self._L.spmv_prompt_attention_workspace, "spmv_prompt_attention_workspace", self.device, self.q_heads,
+                     self.kv_heads, self.head_dim, a.elem, ctypes.byref(size))
+        self._workspace = torch.empty(size.value, dtype=torch.uint8, device=self.device)
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
-        a.status = self._status.data_ptr()
+        a.status, a.workspace, a.workspace_bytes = self._status.data_ptr(), self._workspace.data_ptr(), size.value
         self._like = self._shape = None
         self._dense, self._scale, self._args_ref = False, self.head_dim ** -0.5, ctypes.byref(a)
         _launch.settle(self.device)
@@ -122,6 +127,7 @@ class PromptAttention:
 
     def device_status(self) -> int:
         """Flags of the calls so far (0 = none); waits for the device.  Bit 0:
-        a request's queries, bit 1: its keys are not rows of the tensors."""
+        a request's queries, bit 1: its keys are not rows of the tensors; bit
+        2: a wait inside the kernel ran out, and an output is not complete."""
         torch.cuda.synchronize(self.device)
         return int(self._status.item())

@@ -131,9 +131,44 @@ def test_one_long_prompt(dtype, causal):
     p.check(*p.run(causal=causal), causal=causal)
 
 
-def test_one_query_over_a_long_past():
-    p = Prompts([1, 3], [70001, 33000], 8, 2, 128, "bf16", seed=2)
-    p.check(*p.run())
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,q_heads,kv_heads", [(128, 8, 2), (64, 1, 1), (256, 4, 1), (80, 7, 1)])
+def test_few_queries_over_a_long_past(dim, q_heads, kv_heads, dtype):
+    """Their keys are cut into shares: more shares than some have keys for, rows that see none, rows of no request."""
+    p = Prompts([1, 3, 0, 40, 5], [70001, 33000, 7, 900, 0], q_heads, kv_heads, dim, dtype, seed=2, before=3)
+    attend = p.attention()
+    given, lse = p.q.new_full(p.q.shape, 3.0), p.q.new_full(p.q.shape[:2], 3.0).float()
+    attend(p.q, p.k, p.v, p.q_ptr, p.kv_ptr, out=given, lse=lse)
+    assert attend.device_status() == 0
+    p.check(given, lse)
+    assert bool((given[:3] == 3).all()) and bool((given[52:] == 3).all()) and bool((lse[:3] == 3).all()) and bool((lse[52:] == 3).all())
+    again, _ = attend(p.q, p.k, p.v, p.q_ptr, p.kv_ptr, causal=False)
+    whole, _ = attend(p.q, p.k, p.v, p.q_ptr, p.kv_ptr, causal=False)
+    assert again[3:52].equal(whole[3:52])
+    out, lse = p.run(causal=False)
+    p.check(out, lse, causal=False)
+
+
+def test_infinities_in_shares():
+    """Values and scores that are not finite in one share of the keys alone."""
+    import torch
+    p = Prompts([2], [9000], 2, 1, 64, "bf16", seed=3)
+    clean, _ = p.run()
+    p.v[4000, 0, 3], p.v[8999, 0, 5], p.v[8998, 0, 6] = float("inf"), float("-inf"), float("nan")
+    out, _ = p.run()
+    want = clean.clone()
+    want[:2, :, 3], want[1, :, 5], want[:2, :, 6] = float("inf"), float("-inf"), float("nan")
+    assert torch.equal(out[:2].nan_to_num(7, 8, 9), want[:2].nan_to_num(7, 8, 9))
+    p.k[:9000, 0, 0] = float("-inf")
+    p.q[:, :, 0] = 1
+    out, lse = p.run()
+    assert bool((lse[:2] == -np.inf).all()) and bool((out[:2, :, 8:] == 0).all())
+    p.k[5000, 0, 0] = 0
+    out, lse = p.run()
+    assert torch.equal(out[:2, :, 8:], p.v[5000, 0, 8:].expand(2, 2, -1)) and bool(torch.isfinite(lse[:2]).all())
+    p.k[6000, 0, 0] = float("inf")
+    out, lse = p.run()
+    assert bool(torch.isnan(out[:2]).all()) and bool(torch.isnan(lse[:2]).all())
 
 
 def test_many_short_prompts():
@@ -304,11 +339,11 @@ def test_repeated_calls_and_streams():
     out, lse = attend(p.q, p.k, p.v, p.q_ptr, p.kv_ptr, stream=stream)
     stream.synchronize()
     assert torch.equal(out[:n], want[:n]) and torch.equal(lse[:n], want_lse[:n])
-    # calls of one object on two streams at once
-    other = torch.cuda.Stream()
+    # on two streams at once, each with its object
+    other, second = torch.cuda.Stream(), p.attention()
     outs = []
     for i in range(20):
-        outs.append(attend(p.q, p.k, p.v, p.q_ptr, p.kv_ptr, stream=(stream, other)[i % 2]))
+        outs.append((attend, second)[i % 2](p.q, p.k, p.v, p.q_ptr, p.kv_ptr, stream=(stream, other)[i % 2]))
     torch.cuda.synchronize()
     for out, lse in outs:
         assert torch.equal(out[:n], want[:n]) and torch.equal(lse[:n], want_lse[:n])
