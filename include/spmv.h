@@ -761,7 +761,7 @@ spmv_status_t spmv_paged_load(int32_t requests, int32_t tokens, int32_t heads, i
 /*
  * spmv_paged_attention over caches of codes: the key of position t is its
  * codes times its key scale, and likewise the value (spmv_paged_cache_t has
- * the layout; the scales need not be powers of two).  args->elem is the type
+ * the layout; the scales are finite and positive, powers of two or not).  args->elem is the type
  * of q and out, bf16 or f16; k_cache and v_cache hold codes and their strides
  * count these (multiples of 16); head_dim is a multiple of 16.  q is taken in
  * f16 times a power of two per head, without loss down to 2^-29 of the head's

@@ -51,6 +51,9 @@ enum { kBadQueries = 1, kBadKeys = 2, kGaveUp = 4 };
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 128;
+// The planner waits for whole pieces of work: about a minute (2^31 keys of a head take 20 seconds); the other waits are
+// for a step, and where one of these runs out everybody gives up.
+constexpr long long kPieceClocks = 1ll << 37;
 
 // DP: the head's elements rounded up to 64; NQ: tiles of a block; CUT: the keys of its work are cut into shares.
 template <typename T_, int DP_, int NQ_, bool CUT_>
@@ -505,12 +508,12 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             for (int number = blockIdx.x; number >= 0 && ok;) {
                 Work w;
                 if (finder.find(p, number, lane, w)) {
-                    if (item >= 2) ok = tc::bar_wait(&sh.taken[item & 1], (item - 2) >> 1 & 1, gave_up);
+                    if (item >= 2) ok = tc::bar_wait(&sh.taken[item & 1], (item - 2) >> 1 & 1, gave_up, kPieceClocks);
                     if (!ok) break;
                     publish(w);
                     // No more is taken over before this piece is nearly done: what waits here another block could do
                     // (asking when a piece begins: 263 us instead of 243 for eight chunks of 512 behind 3,500 to 7,000).
-                    ok = tc::bar_wait(&sh.nearly, (item - 1) & 1, gave_up);
+                    ok = tc::bar_wait(&sh.nearly, (item - 1) & 1, gave_up, kPieceClocks);
                     if (!ok) break;
                 }
                 if (lane == 0) tc::ask_block(&sh.answer, &sh.answered);
@@ -522,7 +525,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 tc::shared_to_async();  // read before it is written again
                 __syncwarp();
             }
-            if (ok && item >= 2) ok = tc::bar_wait(&sh.taken[item & 1], (item - 2) >> 1 & 1, gave_up);
+            if (ok && item >= 2) ok = tc::bar_wait(&sh.taken[item & 1], (item - 2) >> 1 & 1, gave_up, kPieceClocks);
             if (ok) publish(Work{});
             if (blockIdx.x == 0)  // the first block looks all requests over
                 for (int r = lane; r < p.a.requests; r += 32) {
@@ -859,10 +862,10 @@ const char *prompt_bad(const spmv_prompt_attention_t &a) {
     if (a.workspace && !aligned_to(a.workspace, 16)) return "the workspace must be 16-byte aligned";
     if (!aligned_to(a.q, 16) || !aligned_to(a.k, 16) || !aligned_to(a.v, 16) || !aligned_to(a.out, 16))
         return "q, k, v and out must be 16-byte aligned";
-    for (int i = 0; i < 2; ++i)
-        if (a.q_stride[i] % 8 || a.k_stride[i] % 8 || a.v_stride[i] % 8 || a.out_stride[i] % 8)
-            return "strides must be multiples of 16 bytes";
     const int sizes[2] = {a.tokens, a.q_heads}, kv_sizes[2] = {a.keys, a.kv_heads};
+    for (int i = 0; i < 2; ++i)  // of a dimension with one element they are not used
+        if ((sizes[i] > 1 && (a.q_stride[i] % 8 || a.out_stride[i] % 8)) || (kv_sizes[i] > 1 && (a.k_stride[i] % 8 || a.v_stride[i] % 8)))
+            return "strides must be multiples of 16 bytes";
     for (int i = 0; i < 2; ++i)  // as tensor copies take them
         if ((sizes[i] > 1 && (a.q_stride[i] < 1 || a.q_stride[i] >= (1LL << 38))) ||
             (kv_sizes[i] > 1 && (a.k_stride[i] < 1 || a.k_stride[i] >= (1LL << 38) || a.v_stride[i] < 1 || a.v_stride[i] >= (1LL << 38))))

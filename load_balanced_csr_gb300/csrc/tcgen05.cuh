@@ -33,14 +33,14 @@ __device__ __forceinline__ void bar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // A whole warp waits until the phase of this parity is over.  It gives up, as
-// everybody of the block does then, after about a second (2^31 clocks) or when
-// `gave_up` is set (null: by its own time alone).  The answer is a vote's, which
+// everybody of the block does then, after `limit` clocks (2^31: about a second)
+// or when `gave_up` is set (null: by its own time alone).  The answer is a vote's, which
 // the compiler knows to be the same on every lane.
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *gave_up, long long limit = 1ll << 31) {
     if (__all_sync(0xffffffffu, tma::mbar_try_wait(bar, parity))) return true;
     const long long start = clock64();
     while (!__all_sync(0xffffffffu, tma::mbar_try_wait(bar, parity)))
-        if (__any_sync(0xffffffffu, (gave_up && *gave_up) || clock64() - start > (1ll << 31))) {
+        if (__any_sync(0xffffffffu, (gave_up && *gave_up) || clock64() - start > limit)) {
             if (gave_up) *gave_up = 1;
             return false;
         }

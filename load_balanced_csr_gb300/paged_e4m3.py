@@ -207,6 +207,8 @@ class PagedAttentionE4M3(PagedAttention):
         of ``table`` (int32).  ``scale``: head_dim ** -0.5 if None.  It has no
         derivative."""
         scales = k_scales, v_scales
+        if k_scales is None or v_scales is None:
+            raise TypeError("k_scales and v_scales must be float32 tensors")
         if _launch.tracked(q, k_cache, v_cache, k_scales, v_scales, out):
             _launch.no_outputs_given("PagedAttentionE4M3", out, lse)
             with _launch.on(stream, self.device):

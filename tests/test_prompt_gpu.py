@@ -297,6 +297,22 @@ def test_outputs_given(dtype):
         assert bool((t == 3).all())
 
 
+def test_dimensions_of_one():
+    """Strides of dimensions with one element are of no matter."""
+    import torch
+    import load_balanced_csr_gb300 as lb
+    ptr = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    x = torch.randn(3, 64, device="cuda").half()
+    q, k, v = (x[i].as_strided((1, 1, 64), (3, 5, 1)) for i in range(3))
+    out, lse = lb.PromptAttention(1, 1, 1, 64, torch.float16)(q, k, v, ptr)
+    assert torch.equal(out, v) and abs(float(lse) - float(q.double().flatten() @ k.double().flatten()) / 8) < 1e-4
+    many = torch.randn(40, 1, 64, device="cuda").half()
+    odd = many.as_strided((40, 1, 64), (64, 3, 1))
+    ptr = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    attend = lb.PromptAttention(1, 1, 1, 64, torch.float16)
+    assert torch.equal(attend(many, many, many, ptr)[0], attend(odd, odd, odd, ptr)[0])
+
+
 def test_bad_pointers():
     """Queries or keys that are not rows of the tensors: the request is left out and flagged."""
     import torch
@@ -415,6 +431,54 @@ def test_a_step_of_chunks_over_an_8_bit_cache():
     out, _ = one(q, *cache, *scales, tables.table, torch.tensor(lens, **i32))
     assert bool((out[2] == 0).all())
     assert float((out[[0, 1, 3]].float() - want[last].float()).norm() / want[last].float().norm()) < 2.0 ** -7
+
+
+def test_steps_one_behind_the_other():
+    """Store, load, prompts and single tokens on one stream without a wait, each step's inputs written over the last one's:
+    the same bits as with a wait behind every call."""
+    import torch
+    import load_balanced_csr_gb300 as lb
+    i32 = dict(dtype=torch.int32, device="cuda")
+    hq, hk, d, page, n = 16, 4, 128, 16, 600
+    lens = [200, 399, 1]
+    held = [-(-x // page) for x in lens]
+    order = torch.randperm(sum(held)).to(**i32)
+    table = torch.zeros(3, max(held), **i32)
+    at = 0
+    for r, h in enumerate(held):
+        table[r, :h] = order[at:at + h]
+        at += h
+    ptr = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), **i32)
+    pos = torch.cat([torch.arange(x) for x in lens]).cuda()
+    req = torch.repeat_interleave(torch.arange(3), torch.tensor(lens)).cuda()
+    slots = (table[req, pos // page] * page + pos % page).to(torch.int32)
+    codes = [torch.zeros(sum(held), page, hk, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.zeros(sum(held), 2, hk, device="cuda") for _ in range(2)]
+    k, v = (torch.empty(n, hk, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    out, lse = torch.empty(n, hq, d, dtype=torch.bfloat16, device="cuda"), torch.empty(n, hq, device="cuda")
+    prompts, one = lb.PromptAttention(3, hq, hk, d, torch.bfloat16), lb.PagedAttentionE4M3(3, hq, hk, d, torch.bfloat16)
+    inputs = [torch.randn(n, hq + 2 * hk, d, device="cuda").bfloat16() * (1 + i) for i in range(12)]
+    dev_lens, last = torch.tensor(lens, **i32), ptr[1:].long() - 1
+
+    def run(wait):
+        kept = []
+        for x in inputs:
+            q, kx, vx = x.split([hq, hk, hk], 1)
+            for step in (lambda: lb.paged_store_e4m3(kx, vx, *codes, *scales, slots),
+                         lambda: lb.paged_load(*codes, table, ptr, n, *scales, dtype=torch.bfloat16, k=k, v=v),
+                         lambda: prompts(q, k, v, ptr, out=out, lse=lse),
+                         lambda: kept.append(one(q[last], *codes, *scales, table, dev_lens)[0]),
+                         lambda: kept.append(out.clone())):
+                step()
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return kept
+
+    want = run(True)
+    for _ in range(5):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
 
 
 def test_refusals():
