@@ -8,8 +8,9 @@
 //
 // A tile of queries is 128 rows of one kv head: neighbouring tokens times the
 // query heads that share it, so that few tokens fill a tile and the keys are
-// read once for all of them.  A block takes two tiles (heads of up to 128
-// elements) and goes through their keys 128 at a time, or one tile and 64 keys.
+// read once for all of them.  A block takes two tiles (heads of up to 192
+// elements) or one, and goes through their keys 128 (heads of up to 128
+// elements) or 64 at a time: what tensor memory holds.
 // Its warps are
 //   one that loads (TMA tensor copies, stages of a step's V and the next K),
 //   one that issues the products (tcgen05, an elected lane),
@@ -37,8 +38,9 @@
 // over 8 heads of 128 bf16, causal (1.10 TFLOP) 640 us, 1,720 TFLOP/s, 0.91 of
 // the library product's; back to back, under the power limit, 715 us.  Heads of
 // 64 elements 940 TFLOP/s, where the softmax takes longer than the products;
-// 192 and 256 about 1,000, one tile's softmax having only its own products to
-// run behind.
+// of 192 1,270 (two tiles, 64 keys at a time; one tile 1,000), of 256 985: one
+// tile's outputs fill half of tensor memory, and a key from L2 serves half as
+// many rows.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -70,14 +72,15 @@ struct Shape {
     using T = T_;
     static constexpr bool CUT = CUT_;
     static constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
-    static constexpr int DP = DP_, NQ = NQ_, KEYS = NQ == 2 ? 128 : 64, HALVES = DP / 64;
-    static constexpr int THREADS = NQ * 128 + 128;  // two of the last four warps have nothing to do
+    static constexpr int DP = DP_, NQ = NQ_, KEYS = DP <= 128 ? 128 : 64, HALVES = DP / 64;
+    static constexpr int THREADS = NQ * 128 + 128;  // one of the last four warps has nothing to do
     static constexpr int QHALF = kRows * 128, QBYTES = HALVES * QHALF;    // 64 elements of a tile's rows; the tile
     static constexpr int KHALF = KEYS * 128, KVBYTES = HALVES * KHALF;
     // A stage holds the tiles that a step takes: V of tile j and K of tile j + 1.  Stage 0 begins with K of tile 0 alone.
-    static constexpr int STAGES = DP == 64 ? 4 : DP == 192 ? 3 : 2, STAGE = 2 * KVBYTES;
+    static constexpr int STAGES = DP == 64 ? 4 : 2, STAGE = 2 * KVBYTES;
     static constexpr int SMEM = 1024 + NQ * QBYTES + STAGES * STAGE;
-    static constexpr uint32_t O = NQ == 2 ? 256 : 128;                    // columns of tensor memory: S at 0 and KEYS, then O
+    static constexpr uint32_t O = 2 * KEYS;                               // columns of tensor memory: S at 0 and KEYS, then O
+    static_assert(O + NQ * DP <= 512 && SMEM <= 231 * 1024, "tensor memory and shared memory");
     // Weights are 2^LIFT times as large.  The maximum they are relative to is raised where a score is RAISE powers of
     // two above it, and looked for where a weight (f16), or a step's sum (bf16), is above LIMIT.  bf16 has the range of
     // 32 bits; f16's weights stay below 2^15, and its smallest step is 2^-35 of a row's largest.
@@ -349,7 +352,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     }
                     __syncwarp();
                 };
-            // Tells the issuer, with the weights of step j, that what the step takes is there: V of tile j, looked over
+                // Tells the issuer, with the weights of step j, that what the step takes is there: V of tile j, looked over
                 // if need be, and the keys behind it.
                 auto announce = [&](int j) {
                     const int last = S::NQ == 2 ? j + 1 : min(j + 2, most);
@@ -852,7 +855,7 @@ template <typename T>
 spmv_status_t launch_prompt_of(const spmv_prompt_attention_t &a, cudaStream_t stream) {
     if (a.head_dim <= 64) return launch_prompt<T, 64, 2>(a, stream);
     if (a.head_dim <= 128) return launch_prompt<T, 128, 2>(a, stream);
-    if (a.head_dim <= 192) return launch_prompt<T, 192, 1>(a, stream);
+    if (a.head_dim <= 192) return launch_prompt<T, 192, 2>(a, stream);
     return launch_prompt<T, 256, 1>(a, stream);
 }
 
@@ -899,7 +902,7 @@ spmv_status_t spmv_prompt_attention_workspace(int32_t q_heads, int32_t kv_heads,
     const int sms = device_sm_count();
     if (sms <= 0) return llm_fail(SPMV_ERR_CUDA, "no CUDA device");
     // the rows of as many pieces of work as there are SMs
-    *bytes = (size_t)sms * (head_dim <= 128 ? 2 : 1) * kRows * 4 * (head_dim + 2);
+    *bytes = (size_t)sms * (head_dim <= 192 ? 2 : 1) * kRows * 4 * (head_dim + 2);
     return SPMV_OK;
 }
 
