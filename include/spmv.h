@@ -733,7 +733,7 @@ typedef struct {
  * spmv_pages_append places them); with block 1 any order will do.  Two tokens
  * must not share a slot.  Where either does not hold, what the blocks
  * concerned hold is not specified.
- * Limits: as spmv_paged_store, tokens * heads < 2^33.
+ * Limits: as spmv_paged_store, tokens * heads < 2^33, heads < 2^24.
  * Errors: INVALID_ARG, CUDA.
  */
 spmv_status_t spmv_paged_store_e4m3(int32_t tokens, int32_t heads, int32_t head_dim, spmv_elem_t elem, const int32_t *slots,
@@ -796,7 +796,7 @@ spmv_status_t spmv_paged_attention_e4m3(const spmv_paged_attention_t *args, int3
  * score of plus infinity or NaN makes its row NaN.
  */
 typedef struct {
-    int32_t requests, tokens, keys; /* tokens: rows of q and out, keys: rows of k and v */
+    int32_t requests, tokens, keys; /* tokens: rows of q and out, keys: rows of k and v; at most 2^31 - 513 */
     int32_t q_heads, kv_heads;      /* q_heads a multiple of kv_heads, at most 128 times as many;
                                        tokens * q_heads < 2^31 */
     int32_t head_dim;               /* a multiple of 8, at most 256 */

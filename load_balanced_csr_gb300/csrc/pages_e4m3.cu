@@ -573,6 +573,7 @@ spmv_status_t spmv_paged_store_e4m3(int32_t tokens, int32_t heads, int32_t head_
     const spmv_paged_cache_t &c = *cache;
     if (c.block < 1 || c.block > kMaxBlock) return llm_bad("block must be in [1, 64]");
     if ((int64_t)tokens * heads >= (1LL << 33)) return llm_bad("tokens * heads must be < 2^33");
+    if (heads >= 1 << 24) return llm_bad("heads must be < 2^24");  // a tile's runs times heads are counted in 32 bits
     if (!elem_ok(elem)) return llm_bad("unknown element type");
     if (!k_stride || !v_stride) return llm_bad("a stride array is NULL");
     if (tokens == 0 || heads == 0 || head_dim == 0 || c.num_pages == 0) return SPMV_OK;

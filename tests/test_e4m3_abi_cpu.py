@@ -47,7 +47,7 @@ def test_store_refusals():
     for bad in (dict(tokens=-1), dict(heads=-1), dict(dim=-1), dict(elem=3), dict(elem=-1), dict(slots=None), dict(slots=ODD), dict(k=None),
                 dict(k=ODD), dict(v=None), dict(ks=None), dict(vs=None), dict(num_pages=-1), dict(page_size=0), dict(num_pages=2 ** 27),
                 dict(block=0), dict(block=-1), dict(block=5), dict(block=128, page_size=128), dict(k_cache=None), dict(v_cache=None),
-                dict(k_scales=None), dict(v_scales=ODD), dict(heads=2 ** 20, dim=2 ** 11), dict(tokens=2 ** 30, heads=2 ** 4)):
+                dict(k_scales=None), dict(v_scales=ODD), dict(heads=2 ** 20, dim=2 ** 11), dict(heads=2 ** 24, dim=1), dict(tokens=2 ** 30, heads=2 ** 4)):
         assert store(**bad) == BAD, bad
         assert L.spmv_last_error()
     assert L.spmv_paged_store_e4m3(1, 2, 64, 0, FAKE, None, FAKE, S2(128, 64), FAKE, S2(128, 64), None) == BAD
@@ -128,7 +128,7 @@ def test_prompt_refusals():
                 dict(q=None), dict(k=None), dict(v=None), dict(q_ptr=None), dict(out=None), dict(status=None), dict(q=0x1008), dict(k=0x1002),
                 dict(v=ODD), dict(out=0x1004), dict(q_ptr=ODD), dict(kv_ptr=ODD), dict(lse=ODD), dict(status=ODD), dict(workspace=0x1008),
                 dict(q_stride=(260, 64)), dict(k_stride=(128, 68)), dict(v_stride=(4, 64)), dict(out_stride=(256, 60)), dict(q_stride=(0, 64)),
-                dict(k_stride=(-128, 64)), dict(v_stride=(128, 0)), dict(q_stride=(2 ** 38, 64))):
+                dict(k_stride=(-128, 64)), dict(v_stride=(128, 0)), dict(q_stride=(2 ** 38, 64)), dict(keys=2 ** 31 - 512), dict(tokens=2 ** 31 - 512, q_heads=1, kv_heads=1)):
         assert L.spmv_prompt_attention(prompt(**bad), None) == BAD, bad
         assert L.spmv_last_error()
     assert L.spmv_prompt_attention(None, None) == BAD
