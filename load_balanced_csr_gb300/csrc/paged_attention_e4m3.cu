@@ -194,7 +194,8 @@ struct TileE4m3 {
                 }
             }
         }
-        const float by_ref = __uint_as_float((254u << 23) - __float_as_uint(ref));  // ref is a power of two
+        // ref is a power of two; the reciprocal of 2^127 is subnormal
+        const float by_ref = __uint_as_float(max((254u << 23) - __float_as_uint(ref), 1u << 22));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float2 scale = *reinterpret_cast<const float2 *>(v_scale + n * 8 + (lane & 3) * 2);

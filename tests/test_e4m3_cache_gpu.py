@@ -528,6 +528,21 @@ def test_attention_scales_that_are_not_finite(scale):
     assert torch.equal(out[0, 4:], clean[0, 4:]) and torch.equal(out[1], clean[1])
 
 
+@pytest.mark.parametrize("heads", [(8, 2), (16, 1)])
+def test_attention_of_the_largest_scale(heads):
+    """2^127, whose reciprocal is subnormal: as with 2^100, times 2^27."""
+    import torch
+    r = Requests([17, 5], *heads, 64, 16, 16, "bf16", seed=12)
+    for lens, page in ((17, 0), (17, 1), (5, 0)):
+        at = int(r.table[0 if lens == 17 else 1, page])
+        r.vc[at].remainder_(9)  # codes of 0 to 2^-6
+        r.vs[at] = 2.0 ** 100
+    small, _ = r.attention()(r.q, *r.caches(), r.table, r.lens)
+    r.vs.mul_(2.0 ** 27)
+    out, _ = r.attention()(r.q, *r.caches(), r.table, r.lens)
+    assert bool((small > 2.0 ** 80).any()) and torch.equal(out.float(), small.float() * 2.0 ** 27)
+
+
 def test_attention_bad_pages_and_lengths():
     import torch
     r = Requests([64, 64, 64], 4, 1, 64, 16, 16, "bf16", seed=9)
