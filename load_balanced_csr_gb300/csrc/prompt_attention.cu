@@ -264,6 +264,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         sh.gave_up = 0;
         tc::bar_init_done();
     }
+    __syncwarp();
     if (warp == kIssuer) tc::alloc(&sh.tmem, 512);
     tc::fence_before();
     __syncthreads();
@@ -568,6 +569,8 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 tc::fence_after();
                 const int left = seen - j * S::KEYS;  // keys that the row sees here
                 const bool cut = j >= first_cut;
+                // The instructions on tensor memory want a whole warp: where lanes may have gone different ways they meet
+                // again before the next one, here and at the outputs.
                 // Loops that few steps go through are not unrolled: the code of a step has to stay in the caches of
                 // instructions beside that of the warp that issues the products.
                 if (cut) {
@@ -579,6 +582,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (c + i >= left) s[i] = -INFINITY;
+                        __syncwarp();
                         tc::store32(at + c, reinterpret_cast<uint32_t *>(s));
                     }
                     tc::store_wait();
@@ -603,6 +607,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                         if (__any_sync(0xffffffffu, raise)) {
                             const float keep = raise ? (m == -INFINITY ? 0.0f : pow2((m - high) * p.scale2)) : 1.0f;
                             if (raise) m = high;
+                            __syncwarp();
                             l *= keep;
                             if (j > 0) {
                                 if constexpr (S::NQ == 1) {  // with two tiles the barrier of S says it
@@ -677,6 +682,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 const float inverse = S::CUT ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
                 const int64_t part = S::CUT ? w.split * p.rows + (int64_t)(w.q0 + token) * p.a.q_heads + head : 0;
                 for (int c = 0; c < p.a.head_dim && (!S::CUT || n > 0); c += 32) {
+                    __syncwarp();
                     uint32_t o[32];
                     if (n > 0) {
                         tc::load32(lanes + S::O + t * S::DP + c, o);
