@@ -964,6 +964,7 @@ __global__ void __launch_bounds__(P::NW * 32, 1) paged_attention_kernel(typename
             tile.begin(p, note.x, h0, heads, qs, lane, note.x == fetched_b && note.y == fetched_vh);
             fetched_b = -1;
             before = note.w & kBefore;
+            __syncwarp();  // lanes without a head read nothing; the chunk's first instruction wants the whole warp
         }
         tile.chunk(p, mine + stage * R::STAGE, qs, (uint32_t)note.z, lane);
         __syncwarp();

@@ -1,4 +1,4 @@
-"""How the kernel of prompts' attention reads: what no run would show."""
+"""How the kernels of prompts' and of single tokens' attention read: what no run would show."""
 import os
 import re
 
@@ -20,3 +20,9 @@ def test_lanes_meet_before_instructions_of_a_whole_warp():
     assert "__syncwarp();" in masks
     raised, = re.findall(r"if \(raise\) m = high;(.*?)tc::bar_wait\(", text, re.S)
     assert "__syncwarp();" in raised
+
+
+def test_lanes_meet_behind_the_queries_of_single_tokens():
+    """Lanes whose head a group does not have read no queries; ldmatrix and mma, of the whole warp, come next."""
+    begun, = re.findall(r"tile\.begin\((.*?)tile\.chunk\(", code("paged_attention.cuh"), re.S)
+    assert "__syncwarp();" in begun
