@@ -236,6 +236,7 @@ struct Shared {
     uint4 answer;
     uint32_t tmem;
     int gave_up, not_finite[2];
+    int queries, pairs;  // copies that the loading warp began in all: of queries, of keys and values
     Work plan[2];
 };
 
@@ -377,12 +378,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 if (S::NQ == 1 && ok && most > 0) announce(most - 1);
                 if (ok) finished(item);
             }
-            // nothing may be on its way into shared memory when the block ends
-            if (*gave_up) {
-                if (queries > 0) tc::bar_wait(&sh.q_full, (queries - 1) & 1, nullptr);
-                for (int i = std::max(0, pairs - S::STAGES); i < pairs; ++i)
-                    tc::bar_wait(&sh.full[i % S::STAGES], i / S::STAGES & 1, nullptr);
-            }
+            if (lane == 0) sh.queries = queries, sh.pairs = pairs;
         } else if (warp == kIssuer) {
             // the whole warp goes through this, one lane issues
             const int n16 = (p.a.head_dim + 15) / 16;
@@ -500,11 +496,6 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     steps[0] += rounds;
                 }
                 if (ok) finished(item);
-            }
-            if (*gave_up) {  // no product may be under way when its memory is given back
-                if (tc::elect()) tc::commit(&sh.last);
-                __syncwarp();
-                tc::bar_wait(&sh.last, 0, nullptr);
             }
         } else if (warp == kPlanner) {
             // Work for the other warps: this block's own, then that of blocks that have not begun, so that loads and first
@@ -725,7 +716,22 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     }
     tc::fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && sh.gave_up) atomicOr(p.a.status, kGaveUp);
+    if (sh.gave_up) {  // every warp has stopped, and all read the same here
+        // Nothing may be on its way into shared memory when the block ends, and no product under way when its memory is
+        // given back.  Not before the barrier: a warp may have come to its end before another one gave up.
+        if (warp == kLoader) {
+            const int queries = sh.queries, pairs = sh.pairs;
+            if (queries > 0) tc::bar_wait(&sh.q_full, (queries - 1) & 1, nullptr);
+            for (int i = std::max(0, pairs - S::STAGES); i < pairs; ++i)
+                tc::bar_wait(&sh.full[i % S::STAGES], i / S::STAGES & 1, nullptr);
+        } else if (warp == kIssuer) {
+            if (tc::elect()) tc::commit(&sh.last);
+            __syncwarp();
+            tc::bar_wait(&sh.last, 0, nullptr);
+        }
+        if (threadIdx.x == 0) atomicOr(p.a.status, kGaveUp);
+        __syncthreads();
+    }
     if (warp == kIssuer) {
         tc::fence_after();
         tc::dealloc(tmem, 512);

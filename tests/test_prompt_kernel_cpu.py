@@ -26,3 +26,18 @@ def test_lanes_meet_behind_the_queries_of_single_tokens():
     """Lanes whose head a group does not have read no queries; ldmatrix and mma, of the whole warp, come next."""
     begun, = re.findall(r"tile\.begin\((.*?)tile\.chunk\(", code("paged_attention.cuh"), re.S)
     assert "__syncwarp();" in begun
+
+
+def test_what_is_under_way_is_waited_for_behind_the_last_barrier():
+    """A warp can come to its end before another one gives up: only where all have stopped is it known that copies and
+    products are to be waited for, and every lane knows the same."""
+    text = code()
+    kernel = text[text.index("prompt_attention_kernel(const __grid_constant__"):text.index("prompt_join_kernel(")]
+    assert "if (*gave_up)" not in kernel  # read lane by lane, and too early
+    work, end = kernel[:kernel.rindex("if (sh.gave_up)")], kernel[kernel.rindex("if (sh.gave_up)"):]
+    assert work.rstrip().endswith("__syncthreads();")
+    drains, rest = end.split("__syncthreads();", 1)
+    assert len(re.findall(r"bar_wait\(&sh\.(q_full|full|last)[^;]*nullptr\);", drains)) == 3 and "tc::commit(&sh.last)" in drains
+    assert "tc::dealloc" in rest and "tc::dealloc" not in work + drains
+    # before, one wait alone is by its own time: the answer about another block, which must not come behind this one's end
+    assert re.findall(r"bar_wait\(&sh\.(\w+)[^;]*nullptr\)", work) == ["answered"]
