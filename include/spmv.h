@@ -818,7 +818,8 @@ typedef struct {
     int32_t *status;                /* device int32; flags are OR-ed in.  Bit 0: a request's queries are
                                        not rows of q, bit 1: its keys are not rows of k; such a request
                                        is left out, its rows of out stay as they were.  Bit 2: a wait
-                                       inside the kernel ran out (a second), and out is not complete */
+                                       inside the kernel ran out (a second, and 256 clocks for each key
+                                       and request of the call), and out is not complete */
     void *workspace;                /* spmv_prompt_attention_workspace bytes (fewer serve in part), 16-byte
                                        aligned, or null: where few queries leave SMs without work, their
                                        keys are cut into shares as far as it goes.  Its contents do not

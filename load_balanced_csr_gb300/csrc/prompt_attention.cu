@@ -62,9 +62,11 @@ enum { kBadQueries = 1, kBadKeys = 2, kGaveUp = 4 };
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 128;
-// The planner waits for whole pieces of work: about a minute (2^31 keys of a head take 20 seconds); the other waits are
-// for a step, and where one of these runs out everybody gives up.
-constexpr long long kPieceClocks = 1ll << 37;
+// Waits end, so that a fault ends with a flag and not with a GPU that hangs; where one runs out everybody gives up.  The
+// planner, and warps that have nothing in a piece of work, wait for a whole piece (20 clocks a key of it where its rows
+// are in step; a row's end can take as long again), and a search of all requests takes a few clocks each.  So what a wait
+// may take goes with the keys and the requests: a second, and this much for each.
+constexpr long long kEachClocks = 256;
 
 // DP: the head's elements rounded up to 64; NQ: tiles of a block; CUT: the keys of its work are cut into shares.
 template <typename T_, int DP_, int NQ_, bool CUT_>
@@ -94,6 +96,7 @@ struct PromptArgs {
     float scale2;                // |scale| / ln 2
     uint32_t negate;             // scale < 0
     int32_t splits;              // shares that each block's keys are cut into
+    int64_t clocks;              // that a wait inside the kernel may take
     int64_t rows;                // tokens * q_heads
     float *sums, *stats;         // workspace of cut rows: [splits][rows][head_dim] sums, [splits][rows][2] m and l
 };
@@ -272,9 +275,10 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     tc::fence_after();
     const uint32_t tmem = sh.tmem;
     volatile int *gave_up = &sh.gave_up;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return tc::bar_wait(bar, parity, gave_up, p.clocks); };
     // The next piece of work; the planner is one ahead of the last warp at work.
     auto next = [&](int item, Work &w) {
-        if (!tc::bar_wait(&sh.planned[item & 1], item >> 1 & 1, gave_up)) return false;
+        if (!wait(&sh.planned[item & 1], item >> 1 & 1)) return false;
         w = sh.plan[item & 1];
         return w.more != 0;
     };
@@ -297,7 +301,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 if (lane == 0) sh.not_finite[item & 1] = 0;
                 __syncwarp();
                 if (most > 0) {
-                    if (queries > 0) ok = tc::bar_wait(&sh.q_empty, (queries - 1) & 1, gave_up);
+                    if (queries > 0) ok = wait(&sh.q_empty, (queries - 1) & 1);
                     if (!ok) break;
                     if (lane == 0) {
                         const uint32_t box = (uint32_t)(p.tile_tokens * p.group * 128 * S::HALVES);
@@ -314,7 +318,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 // pair i: K of tile i, if there is one, and V of the tile before
                 auto load = [&](int i) {
                     const int stage = pairs % S::STAGES, round = pairs / S::STAGES;
-                    ok = round == 0 || tc::bar_wait(&sh.empty[stage], (round - 1) & 1, gave_up);
+                    ok = round == 0 || wait(&sh.empty[stage], (round - 1) & 1);
                     if (!ok) return;
                     if (lane == 0) {
                         tma::mbar_expect_tx(&sh.full[stage], ((i < most) + (i > 0)) * S::KVBYTES);
@@ -327,7 +331,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     ++pairs;
                 };
                 auto wait_pair = [&](int i) {
-                    return tc::bar_wait(&sh.full[(pairs0 + i) % S::STAGES], (pairs0 + i) / S::STAGES & 1, gave_up);
+                    return wait(&sh.full[(pairs0 + i) % S::STAGES], (pairs0 + i) / S::STAGES & 1);
                 };
                 // puts zeros in the place of what is not finite among a stage's values
                 auto look_over = [&](int stage) {
@@ -363,7 +367,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     for (int t = 0; t < S::NQ && ok; ++t) {  // once a phase: the one before has to be over
                         if (j >= of.tiles[t]) continue;
                         const int step = steps[t]++, b = S::NQ == 2 ? t : step & 1, phase = S::NQ == 2 ? step : step >> 1;
-                        if (phase > 0) ok = tc::bar_wait(&sh.weights[b], (phase - 1) & 1, gave_up);
+                        if (phase > 0) ok = wait(&sh.weights[b], (phase - 1) & 1);
                         if (ok && lane == 0) tc::bar_arrive(&sh.weights[b]);
                     }
                 };
@@ -408,7 +412,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             };
             // the weights, and all that their step takes
             auto wait_weights = [&](int buffer, int parity) {
-                const bool there = tc::bar_wait(&sh.weights[buffer], parity, gave_up);
+                const bool there = wait(&sh.weights[buffer], parity);
                 tc::fence_after();
                 return there;
             };
@@ -428,7 +432,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     finished(item);
                     continue;
                 }
-                ok = tc::bar_wait(&sh.q_full, queries++ & 1, gave_up) && tc::bar_wait(&sh.full[stage], stage_phase, gave_up);
+                ok = wait(&sh.q_full, queries++ & 1) && wait(&sh.full[stage], stage_phase);
                 if (!ok) break;
                 if constexpr (S::NQ == 2) {
                     const int own[2] = {tc::uniform(of.tiles[0]), tc::uniform(of.tiles[1])};
@@ -473,7 +477,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     __syncwarp();
                     pass_stage();
                     if (rounds > 1) {
-                        ok = tc::bar_wait(&sh.full[stage], stage_phase, gave_up);
+                        ok = wait(&sh.full[stage], stage_phase);
                         if (ok && tc::elect()) {
                             scores(0, stage, buffer(1) * S::KEYS), tc::commit(&sh.scores[buffer(1)]);
                             if (rounds == 2) tc::commit(&sh.q_empty);
@@ -512,12 +516,12 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             for (int number = blockIdx.x; number >= 0 && ok;) {
                 Work w;
                 if (finder.find(p, number, lane, w)) {
-                    if (item >= 2) ok = tc::bar_wait(&sh.taken[item & 1], (item - 2) >> 1 & 1, gave_up, kPieceClocks);
+                    if (item >= 2) ok = wait(&sh.taken[item & 1], (item - 2) >> 1 & 1);
                     if (!ok) break;
                     publish(w);
                     // No more is taken over before this piece is nearly done: what waits here another block could do
                     // (asking when a piece begins: 263 us instead of 243 for eight chunks of 512 behind 3,500 to 7,000).
-                    ok = tc::bar_wait(&sh.nearly, (item - 1) & 1, gave_up, kPieceClocks);
+                    ok = wait(&sh.nearly, (item - 1) & 1);
                     if (!ok) break;
                 }
                 if (lane == 0) tc::ask_block(&sh.answer, &sh.answered);
@@ -529,7 +533,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 tc::shared_to_async();  // read before it is written again
                 __syncwarp();
             }
-            if (ok && item >= 2) ok = tc::bar_wait(&sh.taken[item & 1], (item - 2) >> 1 & 1, gave_up, kPieceClocks);
+            if (ok && item >= 2) ok = wait(&sh.taken[item & 1], (item - 2) >> 1 & 1);
             if (ok) publish(Work{});
             if (blockIdx.x == 0)  // the first block looks all requests over
                 for (int r = lane; r < p.a.requests; r += 32) {
@@ -555,7 +559,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             for (int j = 0; j < n; ++j) {
                 const int step = steps + j, buffer = S::NQ == 2 ? t : step & 1;
                 const uint32_t at = lanes + buffer * S::KEYS;
-                ok = tc::bar_wait(&sh.scores[buffer], S::NQ == 2 ? step & 1 : step >> 1 & 1, gave_up);
+                ok = wait(&sh.scores[buffer], S::NQ == 2 ? step & 1 : step >> 1 & 1);
                 if (!ok) break;
                 tc::fence_after();
                 const int left = seen - j * S::KEYS;  // keys that the row sees here
@@ -602,7 +606,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                             l *= keep;
                             if (j > 0) {
                                 if constexpr (S::NQ == 1) {  // with two tiles the barrier of S says it
-                                    ok = tc::bar_wait(&sh.product, (step - 1) & 1, gave_up);
+                                    ok = wait(&sh.product, (step - 1) & 1);
                                     if (!ok) break;
                                     tc::fence_after();
                                 }
@@ -660,11 +664,11 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 tc::bar_arrive(&sh.weights[buffer]);
             }
             if (n > 0 && ok) {
-                ok = tc::bar_wait(&sh.done[t], pieces++ & 1, gave_up);
+                ok = wait(&sh.done[t], pieces++ & 1);
                 tc::fence_after();
                 // over long since; what the loading warp noted before it arrived here is read below
                 const int step = steps + n - 1;
-                ok = ok && tc::bar_wait(&sh.weights[S::NQ == 2 ? t : step & 1], S::NQ == 2 ? step & 1 : step >> 1 & 1, gave_up);
+                ok = ok && wait(&sh.weights[S::NQ == 2 ? t : step & 1], S::NQ == 2 ? step & 1 : step >> 1 & 1);
             }
             steps += n;
             if (ok && w.t0 + t * p.tile_tokens < w.nq) {
@@ -834,6 +838,7 @@ spmv_status_t launch_prompt(const spmv_prompt_attention_t &a, cudaStream_t strea
     // weights of masked scores, minus infinity, have to be 0: a scale of 0 is taken as one that no score feels
     p.scale2 = std::max(std::fabs(a.scale) * kLog2e, FLT_MIN);
     p.negate = a.scale < 0.0f;
+    p.clocks = (1ll << 31) + kEachClocks * ((int64_t)a.keys + a.requests);
     CUtensorMap maps[3];
     const bool keys = a.keys > 0;  // without keys nothing is loaded
     if (!make_map(&maps[0], S::BF16, a.q, a.head_dim, a.q_heads, a.tokens, a.q_stride, p.group, p.tile_tokens) ||

@@ -41,3 +41,18 @@ def test_what_is_under_way_is_waited_for_behind_the_last_barrier():
     assert "tc::dealloc" in rest and "tc::dealloc" not in work + drains
     # before, one wait alone is by its own time: the answer about another block, which must not come behind this one's end
     assert re.findall(r"bar_wait\(&sh\.(\w+)[^;]*nullptr\)", work) == ["answered"]
+
+
+def test_waits_for_whole_pieces_of_work_last_as_long_as_these():
+    """A tile without rows waits for the next piece while the other tile goes through all keys of this one, an announcement
+    waits behind a row's end, and so on: no wait on another warp is for a step alone.  A step of 128 keys takes about 2,550
+    clocks; 2^31 of them are the most a piece can have."""
+    text = code()
+    kernel = text[text.index("prompt_attention_kernel(const __grid_constant__"):text.index("prompt_join_kernel(")]
+    assert re.findall(r"auto wait = \[&\]\(uint64_t \*bar, uint32_t parity\) \{ return tc::bar_wait\(bar, parity, gave_up, p\.clocks\); \};", kernel)
+    work = kernel[:kernel.rindex("if (sh.gave_up)")]
+    assert sorted(re.findall(r"bar_wait\(([^,]*),", work)) == ["&sh.answered", "bar"]
+    assert len(re.findall(r"\bwait\(", work)) >= 15
+    each, = map(int, re.findall(r"kEachClocks = (\d+);", text))
+    assert re.findall(r"p\.clocks = \(1ll << 31\) \+ kEachClocks \* \(\(int64_t\)a\.keys \+ a\.requests\);", text)
+    assert each >= 4 * 2550 / 128
