@@ -239,7 +239,6 @@ struct Shared {
     uint4 answer;
     uint32_t tmem;
     int gave_up, not_finite[2];
-    int queries, pairs;  // copies that the loading warp began in all: of queries, of keys and values
     Work plan[2];
 };
 
@@ -285,6 +284,13 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     auto finished = [&](int item) {
         __syncwarp();
         if (lane == 0) tc::bar_arrive(&sh.taken[item & 1]);
+    };
+    // Every warp's last step: all have stopped then, whoever came to its end before another one gave up.  Whether one did,
+    // and all read the same.
+    auto stopped = [&] {
+        tc::fence_before();
+        tc::block_barrier(1, S::THREADS);
+        return sh.gave_up != 0;
     };
     // A row of 128 scores needs more registers than 384 threads have each: three times 168 are 72 + 2 * 216.
     static_assert(S::NQ == 1 || S::THREADS == 384, "the registers of the launch");
@@ -382,7 +388,11 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 if (S::NQ == 1 && ok && most > 0) announce(most - 1);
                 if (ok) finished(item);
             }
-            if (lane == 0) sh.queries = queries, sh.pairs = pairs;
+            if (stopped()) {  // nothing may be on its way into shared memory when the block ends
+                if (queries > 0) tc::bar_wait(&sh.q_full, (queries - 1) & 1, nullptr);
+                for (int i = std::max(0, pairs - S::STAGES); i < pairs; ++i)
+                    tc::bar_wait(&sh.full[i % S::STAGES], i / S::STAGES & 1, nullptr);
+            }
         } else if (warp == kIssuer) {
             // the whole warp goes through this, one lane issues
             const int n16 = (p.a.head_dim + 15) / 16;
@@ -501,6 +511,14 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 }
                 if (ok) finished(item);
             }
+            if (stopped()) {  // no product may be under way when its memory is given back
+                if (tc::elect()) tc::commit(&sh.last);
+                __syncwarp();
+                tc::bar_wait(&sh.last, 0, nullptr);
+            }
+            __syncwarp();
+            tc::fence_after();
+            tc::dealloc(tmem, 512);
         } else if (warp == kPlanner) {
             // Work for the other warps: this block's own, then that of blocks that have not begun, so that loads and first
             // scores run during the last piece's end.
@@ -540,6 +558,9 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     Work w;
                     if (const int flag = Finder<S>::read(p, r, w)) atomicOr(p.a.status, flag);
                 }
+            if (stopped() && lane == 0) atomicOr(p.a.status, kGaveUp);
+        } else {
+            stopped();
         }
     } else {
         if constexpr (S::NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -717,28 +738,7 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             }
             if (ok) finished(item);
         }
-    }
-    tc::fence_before();
-    __syncthreads();
-    if (sh.gave_up) {  // every warp has stopped, and all read the same here
-        // Nothing may be on its way into shared memory when the block ends, and no product under way when its memory is
-        // given back.  Not before the barrier: a warp may have come to its end before another one gave up.
-        if (warp == kLoader) {
-            const int queries = sh.queries, pairs = sh.pairs;
-            if (queries > 0) tc::bar_wait(&sh.q_full, (queries - 1) & 1, nullptr);
-            for (int i = std::max(0, pairs - S::STAGES); i < pairs; ++i)
-                tc::bar_wait(&sh.full[i % S::STAGES], i / S::STAGES & 1, nullptr);
-        } else if (warp == kIssuer) {
-            if (tc::elect()) tc::commit(&sh.last);
-            __syncwarp();
-            tc::bar_wait(&sh.last, 0, nullptr);
-        }
-        if (threadIdx.x == 0) atomicOr(p.a.status, kGaveUp);
-        __syncthreads();
-    }
-    if (warp == kIssuer) {
-        tc::fence_after();
-        tc::dealloc(tmem, 512);
+        stopped();
     }
 }
 

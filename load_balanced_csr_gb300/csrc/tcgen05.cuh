@@ -46,6 +46,11 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
         }
     return true;
 }
+// A barrier of the block's warps, each at a place of its own in the code (0 is __syncthreads').
+__device__ __forceinline__ void block_barrier(int number, int threads) {
+    asm volatile("barrier.sync %0, %1;" ::"r"(number), "r"(threads) : "memory");
+    __syncwarp();
+}
 // what this thread wrote to shared memory, to the copies and matrix instructions that read it
 __device__ __forceinline__ void shared_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 

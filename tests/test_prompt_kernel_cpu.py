@@ -18,7 +18,7 @@ def test_lanes_meet_before_instructions_of_a_whole_warp():
     assert "__syncwarp();" in outputs  # rows without a place, and values that are not finite, go their own way
     masks, = re.findall(r"if \(c \+ i >= left\) s\[i\] = -INFINITY;(.*?)tc::store32\(", text, re.S)
     assert "__syncwarp();" in masks
-    raised, = re.findall(r"if \(raise\) m = high;(.*?)tc::bar_wait\(", text, re.S)
+    raised, = re.findall(r"if \(raise\) m = high;(.*?)\bwait\(", text, re.S)
     assert "__syncwarp();" in raised
 
 
@@ -28,31 +28,38 @@ def test_lanes_meet_behind_the_queries_of_single_tokens():
     assert "__syncwarp();" in begun
 
 
-def test_what_is_under_way_is_waited_for_behind_the_last_barrier():
-    """A warp can come to its end before another one gives up: only where all have stopped is it known that copies and
-    products are to be waited for, and every lane knows the same."""
+def kernel_code():
     text = code()
-    kernel = text[text.index("prompt_attention_kernel(const __grid_constant__"):text.index("prompt_join_kernel(")]
+    return text[text.index("prompt_attention_kernel(const __grid_constant__"):text.index("prompt_join_kernel(")]
+
+
+def test_what_is_under_way_is_waited_for_when_all_warps_have_stopped():
+    """A warp can come to its end before another one gives up: only behind a barrier of them all is it known that copies and
+    products are to be waited for, and do all lanes read the same."""
+    kernel = kernel_code()
     assert "if (*gave_up)" not in kernel  # read lane by lane, and too early
-    work, end = kernel[:kernel.rindex("if (sh.gave_up)")], kernel[kernel.rindex("if (sh.gave_up)"):]
-    assert work.rstrip().endswith("__syncthreads();")
-    drains, rest = end.split("__syncthreads();", 1)
-    assert len(re.findall(r"bar_wait\(&sh\.(q_full|full|last)[^;]*nullptr\);", drains)) == 3 and "tc::commit(&sh.last)" in drains
-    assert "tc::dealloc" in rest and "tc::dealloc" not in work + drains
-    # before, one wait alone is by its own time: the answer about another block, which must not come behind this one's end
-    assert re.findall(r"bar_wait\(&sh\.(\w+)[^;]*nullptr\)", work) == ["answered"]
+    stopped, = re.findall(r"auto stopped = \[&\] \{(.*?)\};", kernel, re.S)
+    assert re.sub(r"\s+", " ", stopped).strip() == "tc::fence_before(); tc::block_barrier(1, S::THREADS); return sh.gave_up != 0;"
+    # each of the five kinds of warp comes to it once, as its last step but for these waits
+    ends = re.split(r"\bstopped\(\)", kernel)[1:]
+    assert len(ends) == 5
+    loader, issuer = ends[0][:ends[0].index("else if")], ends[1][:ends[1].index("else if")]
+    assert re.findall(r"bar_wait\(&sh\.(\w+)[^;]*nullptr\);", loader) == ["q_full", "full"] and len(re.findall("bar_wait", loader)) == 2
+    assert "tc::commit(&sh.last)" in issuer and re.findall(r"bar_wait\(&sh\.(\w+), 0, nullptr\);.*?tc::(dealloc)", issuer, re.S) == [("last", "dealloc")]
+    assert kernel.count("tc::dealloc") == 1
+    for other in ends[2:]:
+        assert not re.findall(r"\bwait\(|bar_wait|load32|store32", other.split("else")[0])
 
 
 def test_waits_for_whole_pieces_of_work_last_as_long_as_these():
     """A tile without rows waits for the next piece while the other tile goes through all keys of this one, an announcement
     waits behind a row's end, and so on: no wait on another warp is for a step alone.  A step of 128 keys takes about 2,550
     clocks; 2^31 of them are the most a piece can have."""
-    text = code()
-    kernel = text[text.index("prompt_attention_kernel(const __grid_constant__"):text.index("prompt_join_kernel(")]
+    kernel = kernel_code()
     assert re.findall(r"auto wait = \[&\]\(uint64_t \*bar, uint32_t parity\) \{ return tc::bar_wait\(bar, parity, gave_up, p\.clocks\); \};", kernel)
-    work = kernel[:kernel.rindex("if (sh.gave_up)")]
-    assert sorted(re.findall(r"bar_wait\(([^,]*),", work)) == ["&sh.answered", "bar"]
-    assert len(re.findall(r"\bwait\(", work)) >= 15
-    each, = map(int, re.findall(r"kEachClocks = (\d+);", text))
-    assert re.findall(r"p\.clocks = \(1ll << 31\) \+ kEachClocks \* \(\(int64_t\)a\.keys \+ a\.requests\);", text)
+    # by their own time alone: the answer about another block, which must not come behind this one's end, and a block's end
+    assert sorted(re.findall(r"bar_wait\(([^,]*),", kernel)) == ["&sh.answered", "&sh.full[i % S::STAGES]", "&sh.last", "&sh.q_full", "bar"]
+    assert len(re.findall(r"\bwait\(", kernel)) >= 15
+    each, = map(int, re.findall(r"kEachClocks = (\d+);", code()))
+    assert re.findall(r"p\.clocks = \(1ll << 31\) \+ kEachClocks \* \(\(int64_t\)a\.keys \+ a\.requests\);", code())
     assert each >= 4 * 2550 / 128
