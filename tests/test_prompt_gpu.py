@@ -524,3 +524,37 @@ def test_nothing_to_do():
     attend(x, x[:, :2], x[:, :2], torch.zeros(1, **i32), out=given)
     attend(x, x[:, :2], x[:, :2], torch.zeros(3, **i32), out=given)
     assert bool((given == 3).all()) and attend.device_status() == 0
+
+
+@pytest.mark.parametrize("size", [2.0 ** 90, 2.0 ** 115])
+@pytest.mark.parametrize("dim", [64, 192, 256])
+def test_large_values_under_rising_scores(dim, size):
+    """Outputs are no larger than the largest value, and so are the sums before the division but for the number of keys:
+    512 times 2^115 is 2^124.  Scores rise by 0.5 to 60 powers of two from a step's keys to the next one's."""
+    import torch
+    for rise in (0.5, 7.0, 20.0, 39.0, 60.0):
+        p = Prompts([300, 3], [512, 300], 4, 2, dim, "bf16", seed=13)
+        p.q.zero_(), p.k.zero_()
+        p.q[:, :, 0] = 1
+        keys = torch.arange(p.k.shape[0], device="cuda")
+        p.k[:, :, 0] = (keys // 64 * rise).to(p.k.dtype)[:, None]
+        p.v *= size
+        for scale in (np.log(2), -np.log(2)):
+            out, lse = p.run(scale=float(scale))
+            assert bool(torch.isfinite(out[:303]).all())
+            p.check(out, lse, scale=float(scale))
+    # one key 39 powers of two above all before it
+    p = Prompts([1], [129], 1, 1, dim, "bf16", seed=14)
+    p.q.zero_(), p.k.zero_(), p.v.fill_(1)
+    p.q[0, 0, 0], p.k[128, 0, 0], p.v[128] = 1, 39, size
+    out, _ = p.run(scale=float(np.log(2)))
+    assert bool((out[0] == size).all())
+
+
+@pytest.mark.parametrize("size", [2.0 ** -90, 2.0 ** -105, 2.0 ** -118])
+@pytest.mark.parametrize("scale", [0.1, 1.5])
+def test_small_values(size, scale):
+    """Values near the bottom of bf16's range keep their bits."""
+    p = Prompts([300, 3], [512, 300], 4, 2, 128, "bf16", seed=15)
+    p.v *= size
+    p.check(*p.run(scale=scale), scale=scale)
