@@ -791,9 +791,14 @@ spmv_status_t spmv_paged_attention_e4m3(const spmv_paged_attention_t *args, int3
  * that a query does not see may hold anything, NaN and infinities included;
  * rows of out and lse that belong to no request are left as they were.  Sums
  * and the softmax are in 32 bits; a weight is rounded to the elements' type
- * once, as the second product's operand.  A score of minus infinity weighs
- * nothing, a row of such scores only gets out = 0 and lse = -infinity, and a
- * score of plus infinity or NaN makes its row NaN.
+ * once, as the second product's operand.  The sums over keys are divided at
+ * the end: exp(s_j - max s) v_j over a row's keys has to stay in the range of
+ * 32 bits.  A score of minus infinity weighs nothing, a row of such scores only
+ * gets out = 0 and lse = -infinity, and a score of plus infinity or NaN makes
+ * its row NaN.  In other rows a value that is not finite counts however little
+ * its key weighs: its element is that infinity, or NaN where the row sees a NaN
+ * or infinities of both signs there (with a score of minus infinity it may
+ * count or not).
  */
 typedef struct {
     int32_t requests, tokens, keys; /* tokens: rows of q and out, keys: rows of k and v; at most 2^31 - 513 */

@@ -112,6 +112,21 @@ __device__ __forceinline__ float pow2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The larger of two, a float or two 16-bit elements each, NaN where one is.
+template <typename T>
+__device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
+    uint32_t y;
+    if constexpr (std::is_same<T, float>::value) asm("max.NaN.f32 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    else if constexpr (std::is_same<T, __half>::value) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+template <typename T>
+__device__ __forceinline__ bool any_nan(uint32_t x) {
+    if constexpr (std::is_same<T, float>::value) return __uint_as_float(x) != __uint_as_float(x);
+    constexpr uint32_t INF = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    return (x & 0x7fffu) > INF || (x >> 16 & 0x7fffu) > INF;
+}
 template <typename T>
 __device__ __forceinline__ uint32_t pack(float lo, float hi);
 template <>
@@ -233,6 +248,43 @@ struct Item {
         }
     }
 };
+
+// Adds to a row's elements what is not finite among the values that the row sees: those of the first `whole` keys, which all
+// rows of the warp see, looked for by all lanes and only where an element is NaN (search), and each row's others up to
+// `end` (0: the row takes no part).  An element that a weight of 0 times an infinity made NaN becomes their sum.
+template <typename T, typename Out>
+__device__ __forceinline__ void add_not_finite(Out *out, int head_dim, const T *v, int64_t stride, bool search, int whole, int end, int lane) {
+    constexpr uint32_t INF = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+#pragma unroll 1
+    for (int c = 0; c < head_dim; c += 8) {
+        __syncwarp();
+        uint32_t found = 0;  // of eight elements: infinity, minus infinity, NaN
+#pragma unroll 1
+        for (int pass = search ? 0 : 1; pass < 2; ++pass) {
+            const int last = pass == 0 ? whole : end, step = pass == 0 ? 32 : 1;
+#pragma unroll 4
+            for (int k = pass == 0 ? lane : whole; k < last; k += step) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(v + k * stride + c);
+                const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t bits = words[i / 2] >> (i % 2 * 16) & 0xffffu, size = bits & 0x7fffu;
+                    if (size >= INF) found |= (size > INF ? 4u : bits >> 15 ? 2u : 1u) << (3 * i);
+                }
+            }
+            __syncwarp();
+            if (pass == 0) found = __reduce_or_sync(0xffffffffu, found);
+        }
+#pragma unroll 1
+        for (int i = 0; i < 8 && end > 0; ++i) {
+            const uint32_t what = found >> (3 * i) & 7u;
+            if (what == 0) continue;
+            const float x = what == 1 ? INFINITY : what == 2 ? -INFINITY : __int_as_float(0x7fffffff), now = to_float(out[c + i]);
+            out[c + i] = from_float<Out>(now == now ? now + x : x);
+        }
+    }
+    __syncwarp();
+}
 
 // Barriers' phases are counted over all work of a block: steps of a tile (scores, weights, and product with one tile),
 // stages (full, empty), pieces of work (the others).
@@ -701,6 +753,10 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 const T *v = static_cast<const T *>(p.a.v) + (int64_t)(w.k0 + of.begin * S::KEYS) * p.a.v_stride[0] + w.kv_head * p.a.v_stride[1];
                 const float inverse = S::CUT ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
                 const int64_t part = S::CUT ? w.split * p.rows + (int64_t)(w.q0 + token) * p.a.q_heads + head : 0;
+                const bool weighs = n > 0 && l != 0.0f;  // some key
+                const int end = S::CUT ? min(seen, n * S::KEYS) : seen, whole = min(first_cut, n) * S::KEYS;
+                uint32_t probe[4] = {};  // NaN where an output is
+                using Out = typename std::conditional<S::CUT, float, T>::type;
                 for (int c = 0; c < p.a.head_dim && (!S::CUT || n > 0); c += 32) {
                     __syncwarp();
                     uint32_t o[32];
@@ -709,30 +765,39 @@ prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                         tc::load32_wait(o);
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = n > 0 ? __float_as_uint(__uint_as_float(o[i]) * inverse) : 0u;
+                    for (int i = 0; i < 32; ++i) o[i] = weighs ? __float_as_uint(__uint_as_float(o[i]) * inverse) : 0u;
                     if (!real) continue;
-                    if (n > 0 && sh.not_finite[item & 1]) {  // values that are not finite and seen by this row
-                        for (int k = first_cut * S::KEYS; k < (S::CUT ? min(seen, n * S::KEYS) : seen); ++k)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c + i < p.a.head_dim) {
-                                    const float x = to_float(v[k * p.a.v_stride[0] + c + i]);
-                                    if (!(fabsf(x) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
-                                }
-                    }
                     if constexpr (S::CUT) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            if (c + i < p.a.head_dim)
+                            if (c + i < p.a.head_dim) {
                                 *reinterpret_cast<uint4 *>(p.sums + part * p.a.head_dim + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                                for (int j = 0; j < 4; ++j) probe[j] = max_nan<float>(probe[j], o[i + j]);
+                            }
                         continue;
                     }
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
-                        if (c + i < p.a.head_dim)
-                            *reinterpret_cast<uint4 *>(out + c + i) =
-                                make_uint4(pack<T>(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), pack<T>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3])),
-                                           pack<T>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5])), pack<T>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
+                        if (c + i < p.a.head_dim) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                x[j] = pack<T>(__uint_as_float(o[i + 2 * j]), __uint_as_float(o[i + 2 * j + 1]));
+                                probe[j] = max_nan<T>(probe[j], x[j]);
+                            }
+                            *reinterpret_cast<uint4 *>(out + c + i) = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                }
+                using Out = typename std::conditional<S::CUT, float, T>::type;
+                // the weights do not explain it
+                // Values that are not finite: taken out of the tiles seen in part, or times a weight of 0.  A sum of weights
+                // that is NaN makes its row NaN whatever they are.
+                const bool takes = real && weighs && l == l;
+                const bool odd = takes && any_nan<Out>(max_nan<Out>(max_nan<Out>(probe[0], probe[1]), max_nan<Out>(probe[2], probe[3])));
+                const bool search = __any_sync(0xffffffffu, odd);
+                if (search || (n > 0 && sh.not_finite[item & 1])) {
+                    if constexpr (S::CUT) add_not_finite<T>(p.sums + part * p.a.head_dim, p.a.head_dim, v, p.a.v_stride[0], search, whole, takes ? end : 0, lane);
+                    else add_not_finite<T>(out, p.a.head_dim, v, p.a.v_stride[0], search, whole, takes ? end : 0, lane);
                 }
                 if constexpr (S::CUT) {
                     if (real) *reinterpret_cast<float2 *>(p.stats + 2 * part) = make_float2(m, l);
@@ -783,7 +848,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptArgs
     float sum = l * weight;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    const uint32_t there = __ballot_sync(0xffffffffu, !(l == 0.0f));
+    const uint32_t there = __ballot_sync(0xffffffffu, !(weight == 0.0f));
+    // of shares whose weight is 0 next to the others' what is not finite counts
+    const uint32_t vanished = __ballot_sync(0xffffffffu, !(l == 0.0f)) & ~there;
     const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
     T *out = static_cast<T *>(p.a.out) + token * p.a.out_stride[0] + head * p.a.out_stride[1];
     for (int c0 = 0; c0 < p.a.head_dim; c0 += 128) {
@@ -795,6 +862,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptArgs
             if (!(there >> i & 1) || c >= p.a.head_dim) continue;
             const float4 x = *reinterpret_cast<const float4 *>(p.sums + (i * p.rows + row) * p.a.head_dim + c);
             o.x = fmaf(wi, x.x, o.x), o.y = fmaf(wi, x.y, o.y), o.z = fmaf(wi, x.z, o.z), o.w = fmaf(wi, x.w, o.w);
+        }
+        for (uint32_t left = c < p.a.head_dim ? vanished : 0; left; left &= left - 1) {
+            const int i = __ffs(left) - 1;
+            const float4 x = *reinterpret_cast<const float4 *>(p.sums + (i * p.rows + row) * p.a.head_dim + c);
+            auto add = [](float &sum, float y) { sum += fabsf(y) < INFINITY ? 0.0f : y; };
+            add(o.x, x.x), add(o.y, x.y), add(o.z, x.z), add(o.w, x.w);
         }
         if (c < p.a.head_dim)
             *reinterpret_cast<uint2 *>(out + c) = make_uint2(pack<T>(o.x * inverse, o.y * inverse), pack<T>(o.z * inverse, o.w * inverse));

@@ -558,3 +558,58 @@ def test_small_values(size, scale):
     p = Prompts([300, 3], [512, 300], 4, 2, 128, "bf16", seed=15)
     p.v *= size
     p.check(*p.run(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 192, 256])
+@pytest.mark.parametrize("requests,nq,nk", [(1, 2, 9000), (30, 260, 700)])
+def test_infinities_whose_weight_vanishes(requests, nq, nk, dim, dtype):
+    """Wherever a key stands, and whatever it weighs: an infinity it brings is its element's, one of the other sign or a NaN
+    makes that NaN, and nothing else changes.  Rows whose scores are all minus infinity stay zero."""
+    import torch
+    hk = 4 if requests > 1 else 1
+    p = Prompts([nq] * requests, [nk] * requests, hk, hk, dim, dtype, seed=16, behind=0)
+    p.q.zero_(), p.k.zero_()
+    p.q[:, :, 0] = 1
+    k, v = p.k.view(requests, nk, hk, dim), p.v.view(requests, nk, hk, dim)
+    for key in (10, 11, 12, 14, 15, nk - 2):
+        k[:, key, :, 0] = -300
+    scale = float(np.log(2))  # 300 powers of two below the others
+    clean, clean_lse = p.run(scale=scale)
+    inf, nan = float("inf"), float("nan")
+    v[:, 10, :, 3], v[:, 11, :, 4], v[:, 12, :, 5], v[:, 13, :, 5], v[:, 14, :, 6] = inf, -inf, inf, -inf, nan
+    v[:, 15, :, 7], v[:, nk - 1, :, 7], v[:, nk - 2, :, 40] = inf, -inf, -inf
+    out, lse = p.run(scale=scale)
+    want = clean.clone().view(requests, nq, hk, dim)
+    want[..., 3], want[..., 4], want[..., 5], want[..., 6], want[..., 7] = inf, -inf, nan, nan, inf
+    want[:, -1, :, 7], want[:, -2:, :, 40] = nan, -inf
+    assert torch.equal(out.nan_to_num(7, 8, 9), want.view(out.shape).nan_to_num(7, 8, 9)) and torch.equal(lse, clean_lse)
+    k[..., 0] = -inf
+    out, lse = p.run(scale=scale)
+    assert bool((out == 0).all()) and bool((lse == -inf).all())
+
+
+def test_infinities_in_shares_whose_weight_vanishes():
+    """All of a share's keys weigh nothing next to another's: its infinities count, its finite values do not."""
+    import torch
+    p = Prompts([2], [20000], 2, 1, 64, "bf16", seed=18, behind=0)
+    p.q.zero_(), p.k.zero_()
+    p.q[:, :, 0] = 1
+    p.k[:15000, 0, 0] = -300
+    clean, lse = p.run(scale=float(np.log(2)))
+    p.check(clean, lse, scale=float(np.log(2)))
+    p.v[5, 0, 3], p.v[9999, 0, 4], p.v[2, 0, 5], p.v[12000, 0, 5], p.v[7000, 0, 6] = np.inf, -np.inf, np.inf, -np.inf, np.nan
+    out, lse2 = p.run(scale=float(np.log(2)))
+    want = clean.clone()
+    want[:, :, 3], want[:, :, 4], want[:, :, 5], want[:, :, 6] = np.inf, -np.inf, np.nan, np.nan
+    assert torch.equal(out.nan_to_num(7, 8, 9), want.nan_to_num(7, 8, 9)) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_values_of_nan_alone(dim):
+    """All rows are NaN, and the call ends."""
+    import torch
+    p = Prompts([700, 1], [3000, 20000], 4, 2, dim, "bf16", seed=17, behind=0)
+    p.v.fill_(float("nan"))
+    out, lse = p.run()
+    assert bool(torch.isnan(out).all()) and bool(torch.isfinite(lse).all())
