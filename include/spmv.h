@@ -766,7 +766,9 @@ spmv_status_t spmv_paged_load(int32_t requests, int32_t tokens, int32_t heads, i
  * count these (multiples of 16); head_dim is a multiple of 16.  q is taken in
  * f16 times a power of two per head, without loss down to 2^-29 of the head's
  * largest element; weights times value scales in 22 bits, in steps of no less
- * than 2^-38 of a row's largest weight times its largest value scale.  A NaN
+ * than 2^-38 of a row's largest weight times its largest value scale.  Dot
+ * products, q times a key scale, and the sums of exp(s_t - max s) v_t have to
+ * stay in the range of 32 bits.  A NaN
  * code of a position makes its score, or its element of the output, NaN.
  * workspace: spmv_paged_attention_e4m3_workspace bytes.  For the rest as
  * spmv_paged_attention.

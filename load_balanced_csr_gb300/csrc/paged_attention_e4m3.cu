@@ -23,14 +23,25 @@
 //   Weights are taken 2^14 times as large, times vs / ref with ref the power of
 // two below the largest value scale so far, as hi + lo; the sums, relative to
 // ref, are rescaled when a larger scale comes.
-#include <cfloat>
-
 #include "e4m3.cuh"
 #include "paged_attention.cuh"
 
 namespace lbcsr {
 
 namespace {
+
+// two 32-bit values at once
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 template <typename T_, int GT_, int DP_, int CH_, int NW_, int STAGES_>
 struct TileE4m3 {
@@ -54,8 +65,7 @@ struct TileE4m3 {
     uint32_t q[DP / 16][2 * H], next[AHEAD ? DP / 16 : 1][2 * H];
     float o[DP / 8][4];  // [32 elements][16 of them][even, odd]
     float m[H], l[H];
-    float scale2[H];     // the scores' scale for q as it was multiplied, and what it was divided by
-    float qf[H];
+    float qf[H];         // what q was divided by
     float ref;           // of o: the same on every lane
 
     __device__ __forceinline__ static void load(const AttendArgs &p, uint32_t (*to)[2 * H], int b, int h0, int heads, int lane) {
@@ -93,7 +103,7 @@ struct TileE4m3 {
             for (int r = 0; r < 2 * H; ++r) q[s][r] ^= p.flip;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-            qf[h] = 1.0f, scale2[h] = p.scale2;
+            qf[h] = 1.0f;
             if (!BF16) continue;
             uint32_t top = 0;  // the largest element's bits
 #pragma unroll
@@ -106,7 +116,6 @@ struct TileE4m3 {
             const int shift = min(max(14 - ((int)(top >> 7) - 127), -114), 126);
             const float up = __int_as_float((127 + shift) << 23);
             qf[h] = __int_as_float((127 - shift) << 23);
-            scale2[h] = fmaxf(p.scale2 * qf[h], FLT_MIN);
 #pragma unroll
             for (int s = 0; s < DP / 16; ++s)
 #pragma unroll
@@ -157,7 +166,13 @@ struct TileE4m3 {
         for (int n = 0; n < NT; ++n) {
             const float2 scale = *reinterpret_cast<const float2 *>(k_scale + n * 8 + (lane & 3) * 2);
 #pragma unroll
-            for (int h = 0; h < H; ++h) s[n][h][0] = sums[n][2 * h] * scale.x, s[n][h][1] = sums[n][2 * h + 1] * scale.y;
+            for (int h = 0; h < H; ++h) {
+                // What q was divided by goes onto the key scale first: a large one and small queries meet here, and the sum
+                // of q's lifted products times the scale alone could pass 32 bits.
+                uint64_t by = pair2(scale.x, scale.y);
+                if (BF16) by = mul2(by, pair2(qf[h], qf[h]));
+                unpair2(mul2(pair2(sums[n][2 * h], sums[n][2 * h + 1]), by), s[n][h][0], s[n][h][1]);
+            }
         }
         if (mask != FULL_MASK<CH>) {  // their weights are 0: scale2 is not
 #pragma unroll
@@ -184,7 +199,7 @@ struct TileE4m3 {
             ref = ref_now;
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                const float keep = worth(m[h], top[h], scale2[h]), keep_o = keep * down;
+                const float keep = worth(m[h], top[h], p.scale2), keep_o = keep * down;
                 l[h] *= keep;
                 m[h] = top[h];
 #pragma unroll
@@ -203,7 +218,7 @@ struct TileE4m3 {
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const float base = base_of(m[h]);
-                float x = pow2(fmaf(s[n][h][0] - base, scale2[h], UP)), y = pow2(fmaf(s[n][h][1] - base, scale2[h], UP));
+                float x = pow2(fmaf(s[n][h][0] - base, p.scale2, UP)), y = pow2(fmaf(s[n][h][1] - base, p.scale2, UP));
                 l[h] += x + y;
                 x *= scale.x, y *= scale.y;
                 const __half2 high = __floats2half2_rn(x, y);
@@ -247,7 +262,6 @@ struct TileE4m3 {
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
             l[h] *= down;
-            if (BF16) m[h] *= qf[h];
         }
 #pragma unroll
         for (int n = 0; n < DP / 8; ++n)

@@ -686,3 +686,14 @@ def test_streams():
     out, lse = attend(r.q, *r.caches(), r.table, r.lens, stream=stream)
     stream.synchronize()
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("heads", [(8, 1), (32, 2)])
+@pytest.mark.parametrize("power,low,high", [(-112, 100, 110), (-122, 112, 121), (100, -114, -104)])
+def test_attention_of_large_key_scales_and_small_queries(power, low, high, heads):
+    """Scores are of the usual size: neither factor's range is the product's."""
+    r = Requests([1, 300, 2000, 17], *heads, 128, 16, 4, "bf16", seed=13, low=low, high=high)
+    r.vs.mul_(2.0 ** (-8 - high))
+    r.q.mul_(2.0 ** power)
+    out, lse = r.attention()(r.q, *r.caches(), r.table, r.lens)
+    r.check(out, lse, 128 ** -0.5)
