@@ -803,7 +803,7 @@ spmv_status_t spmv_paged_attention_e4m3(const spmv_paged_attention_t *args, int3
  * count or not).
  */
 typedef struct {
-    int32_t requests, tokens, keys; /* tokens: rows of q and out, keys: rows of k and v; at most 2^31 - 513 */
+    int32_t requests, tokens, keys; /* tokens: rows of q and out, keys: rows of k and v; each at most 2^31 - 513 */
     int32_t q_heads, kv_heads;      /* q_heads a multiple of kv_heads, at most 128 times as many;
                                        tokens * q_heads < 2^31 */
     int32_t head_dim;               /* a multiple of 8, at most 256 */

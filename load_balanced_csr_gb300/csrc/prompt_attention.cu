@@ -960,8 +960,8 @@ const char *prompt_bad(const spmv_prompt_attention_t &a) {
     if (a.kv_heads < 1 || a.q_heads % a.kv_heads) return "q_heads must be a multiple of kv_heads";
     if (a.q_heads / a.kv_heads > 128) return "q_heads must be at most 128 times kv_heads";
     if ((int64_t)a.tokens * a.q_heads >= (1LL << 31)) return "tokens * q_heads must be < 2^31";
-    // rows are counted up to the end of a block's tiles
-    if (std::max(a.tokens, a.keys) > INT32_MAX - 512) return "tokens and keys must be at most 2^31 - 513";
+    // rows are counted up to the end of a block's tiles, requests 128 at a time
+    if (std::max(std::max(a.tokens, a.keys), a.requests) > INT32_MAX - 512) return "requests, tokens and keys must be at most 2^31 - 513";
     if (a.requests == 0 || a.tokens == 0 || a.q_heads == 0) return nullptr;
     if (!a.q || !a.q_ptr || !a.out || !a.status) return "q, q_ptr, out or status is NULL";
     if (a.keys > 0 && (!a.k || !a.v)) return "k or v is NULL";
