@@ -434,7 +434,7 @@ __device__ __forceinline__ int32_t slot_of_row(const LoadArgs &a, const int32_t 
     if (i >= a.tokens || i < ptr[0] || i >= ptr[a.requests]) return -1;
     int lo = 0, hi = a.requests - 1;  // the last request that begins at or before i
     while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
+        const int mid = lo + ((hi - lo + 1) >> 1);  // lo + hi can pass 32 bits
         if (ptr[mid] <= i) lo = mid;
         else hi = mid - 1;
     }

@@ -697,3 +697,19 @@ def test_attention_of_large_key_scales_and_small_queries(power, low, high, heads
     r.q.mul_(2.0 ** power)
     out, lse = r.attention()(r.q, *r.caches(), r.table, r.lens)
     r.check(out, lse, 128 ** -0.5)
+
+
+def test_load_of_more_than_2_30_requests():
+    """Nearly all of them empty: the search for a row's request goes up to the last."""
+    import torch
+    import load_balanced_csr_gb300 as lb
+    requests = 2 ** 30 + 9
+    ptr = torch.zeros(requests + 1, dtype=torch.int32, device="cuda")  # 4 GiB
+    ptr[requests - 4:] = 2
+    ptr[requests:] = 5
+    cache = torch.randn(3, 4, 1, 8, device="cuda")
+    table = torch.tensor([[2, 1]], dtype=torch.int32, device="cuda").expand(requests, 2)
+    k, v = lb.paged_load(cache, cache + 1, table, ptr, 5)
+    # two rows of request 2^30 + 4, three of the last
+    want = cache[2, [0, 1, 0, 1, 2]]
+    assert torch.equal(k, want) and torch.equal(v, want + 1)
