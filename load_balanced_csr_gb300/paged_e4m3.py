@@ -165,12 +165,12 @@ def paged_load(k_cache, v_cache, table, token_ptr, tokens: int, k_scales=None, v
     codes need their scales and the rows' ``dtype``; others are copied.  Rows
     behind the last request, if ``tokens`` are more, are left as they were.  It
     has no derivative."""
-    if _launch.tracked(k_cache, v_cache, k, v):
+    if _launch.tracked(k_cache, v_cache, k_scales, v_scales, k, v):
         _launch.no_outputs_given("paged_load", k, v)
         with _launch.on(stream, k_cache.device):
             return _launch.NoDerivative.apply(
                 "paged_load", lambda: _load(k_cache, v_cache, table, token_ptr, tokens, k_scales, v_scales, dtype, None, None, None),
-                k_cache, v_cache)
+                k_cache, v_cache, k_scales, v_scales)
     return _load(k_cache, v_cache, table, token_ptr, tokens, k_scales, v_scales, dtype, k, v, stream)
 
 

@@ -713,3 +713,23 @@ def test_load_of_more_than_2_30_requests():
     # two rows of request 2^30 + 4, three of the last
     want = cache[2, [0, 1, 0, 1, 2]]
     assert torch.equal(k, want) and torch.equal(v, want + 1)
+
+
+def test_load_keeps_no_gradient_of_scales_without_a_word():
+    """The rows are codes times scales: a scale that requires a gradient is told that there is none."""
+    import torch
+    import load_balanced_csr_gb300 as lb
+    kc, vc, ks, vs = Cache8(4, 16, 2, 64, 16).args()
+    table, ptr = torch.zeros(1, 4, dtype=torch.int32, device="cuda"), torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    want = lb.paged_load(kc, vc, table, ptr, 3, ks, vs, dtype=torch.float32)
+    for which in (0, 1):
+        scales = [ks.clone(), vs.clone()]
+        scales[which].requires_grad_()
+        got = lb.paged_load(kc, vc, table, ptr, 3, *scales, dtype=torch.float32)
+        assert got[0].requires_grad and all(torch.equal(a.nan_to_num(7), b.nan_to_num(7)) for a, b in zip(got, want))
+        with pytest.raises(RuntimeError, match="no derivative"):
+            got[which].sum().backward()
+        with pytest.raises(RuntimeError, match="outputs given"):
+            lb.paged_load(kc, vc, table, ptr, 3, *scales, dtype=torch.float32, k=torch.empty_like(want[0]))
+        with torch.no_grad():
+            assert not lb.paged_load(kc, vc, table, ptr, 3, *scales, dtype=torch.float32)[0].requires_grad
