@@ -109,6 +109,12 @@ def cuda_device(device):
     return device if device.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
+def counts(*sizes) -> None:
+    """Checks sizes that the library counts in 32 bits: ctypes would drop what is above, and a few rows of many be taken."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"sizes are counted in 32 bits, got {max(sizes)}")
+
+
 def rows(name, t, shape, dtype, device):
     """Checks a row-major matrix (unit stride in a row) and returns its row stride."""
     if t.dtype != dtype or t.device != device:

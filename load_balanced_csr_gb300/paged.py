@@ -107,6 +107,7 @@ def _check_store(k, v, k_cache, v_cache):
     vc = _cache_strides("v_cache", v_cache, heads, dim, dtype, d)
     if k_cache.shape != v_cache.shape:
         raise ValueError("k_cache and v_cache differ in shape")
+    _launch.counts(*k.shape, *k_cache.shape)
     return (d, (tokens, heads, dim, _launch.elem(dtype)), tuple(k_cache.shape[:2]),
             _I64x2(*ks[:2]), _I64x2(*vs[:2]), _I64x3(*kc[:3]), _I64x3(*vc[:3]))
 
@@ -154,6 +155,7 @@ class PagedAttention:
         a.elem = _launch.elem(dtype)
         self.max_batch = int(max_batch)
         self.q_heads, self.kv_heads, self.head_dim = int(q_heads), int(kv_heads), int(head_dim)
+        _launch.counts(self.max_batch, self.q_heads, self.kv_heads, self.head_dim)
         a.q_heads, a.kv_heads, a.head_dim = self.q_heads, self.kv_heads, self.head_dim
         size = ctypes.c_size_t()
         with torch.cuda.device(self.device):
@@ -239,6 +241,7 @@ class PagedAttention:
             raise ValueError("table must have a row for each request")
         a.table_stride = _launch.rows("table", table, table.shape, torch.int32, d)
         _launch.vector("lens", lens, batch, torch.int32, d)
+        _launch.counts(*k_cache.shape, table.shape[1])
         a.batch = batch
         a.num_pages, a.page_size = k_cache.shape[:2]
         a.max_pages = table.shape[1]

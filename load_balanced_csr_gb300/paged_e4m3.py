@@ -58,6 +58,7 @@ def _cache_args(k_cache, v_cache, k_scales, v_scales, heads, dim, dtype, device)
     vs = _cache_strides("v_cache", v_cache, heads, dim, dtype, device)
     if k_cache.shape != v_cache.shape:
         raise ValueError("k_cache and v_cache differ in shape")
+    _launch.counts(*k_cache.shape)
     a = PagedCacheArgs()
     a.num_pages, a.page_size = k_cache.shape[:2]
     a.k_stride[:], a.v_stride[:] = ks[:3], vs[:3]
@@ -102,6 +103,7 @@ def _check_store(k, v, k_cache, v_cache, k_scales, v_scales):
     tokens, heads, dim = k.shape
     if k_cache.dtype != CODES:
         raise TypeError(f"k_cache must be a {CODES} tensor, got {k_cache.dtype}")
+    _launch.counts(tokens)
     return (d, (tokens, heads, dim, _launch.elem(dtype)), _cache_args(k_cache, v_cache, k_scales, v_scales, heads, dim, CODES, d),
             _token_strides("k", k, k.shape, dtype, d), _token_strides("v", v, k.shape, dtype, d))
 
@@ -151,6 +153,7 @@ def _check_load(k_cache, v_cache, table, token_ptr, tokens, k_scales, v_scales, 
     requests = token_ptr.numel() - 1
     if requests < 0 or table.shape[0] < requests:
         raise ValueError("token_ptr must have an entry more than there are requests, and table a row for each")
+    _launch.counts(requests, tokens, table.shape[1])
     stride = _launch.rows("table", table, table.shape, torch.int32, d)
     _launch.vector("token_ptr", token_ptr, requests + 1, torch.int32, d)
     dense = _I64x2(heads * dim, dim)

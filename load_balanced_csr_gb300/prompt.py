@@ -45,6 +45,7 @@ class PromptAttention:
             raise TypeError("prompts are attended to in bfloat16 or float16")
         self.max_requests = int(max_requests)
         self.q_heads, self.kv_heads, self.head_dim = int(q_heads), int(kv_heads), int(head_dim)
+        _launch.counts(self.q_heads, self.kv_heads, self.head_dim)
         a.q_heads, a.kv_heads, a.head_dim = self.q_heads, self.kv_heads, self.head_dim
         size = ctypes.c_size_t()
         _launch.call(self._L.spmv_prompt_attention_workspace, "spmv_prompt_attention_workspace", self.device, self.q_heads,
@@ -122,6 +123,7 @@ class PromptAttention:
         _launch.vector("q_ptr", q_ptr, n, torch.int32, d)
         if kv_ptr is not None:
             _launch.vector("kv_ptr", kv_ptr, n, torch.int32, d)
+        _launch.counts(n - 1, q.shape[0], k.shape[0])
         a.requests, a.tokens, a.keys = n - 1, q.shape[0], k.shape[0]
         a.q_stride[:], a.k_stride[:], a.v_stride[:] = q.stride()[:2], k.stride()[:2], v.stride()[:2]
 

@@ -733,3 +733,35 @@ def test_load_keeps_no_gradient_of_scales_without_a_word():
             lb.paged_load(kc, vc, table, ptr, 3, *scales, dtype=torch.float32, k=torch.empty_like(want[0]))
         with torch.no_grad():
             assert not lb.paged_load(kc, vc, table, ptr, 3, *scales, dtype=torch.float32)[0].requires_grad
+
+
+def test_sizes_past_32_bits_are_refused():
+    """ctypes drops the bits above: 2^32 + 3 rows would be taken as 3."""
+    import torch
+    import load_balanced_csr_gb300 as lb
+    many, i32 = 2 ** 32 + 3, dict(dtype=torch.int32, device="cuda")
+    c = Cache8(4, 16, 2, 64, 16).args()
+    big = [t[:1].expand(many, *t.shape[1:]) for t in c]
+    table, ptr, lens = torch.zeros(1, 4, **i32), torch.tensor([0, 3], **i32), torch.ones(1, **i32)
+    x = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    rows, wide = x.expand(many, 2, 64), torch.empty(1, many, **i32)  # 16 GiB: its rows have to be contiguous
+    attend8, attend = (kind(1, 2, 2, 64, torch.bfloat16) for kind in (lb.PagedAttentionE4M3, lb.PagedAttention))
+    whole = torch.zeros(1, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    prompts = lb.PromptAttention(1, 2, 2, 64, torch.bfloat16)
+    load = dict(dtype=torch.bfloat16, k=rows, v=rows)
+    for call in (lambda: lb.paged_load(*c[:2], table, ptr, many, *c[2:], **load),
+                 lambda: lb.paged_load(*big[:2], table, ptr, 3, *big[2:], dtype=torch.bfloat16),
+                 lambda: lb.paged_load(*c[:2], wide, ptr, 3, *c[2:], dtype=torch.bfloat16),
+                 lambda: lb.paged_store_e4m3(rows, rows, *c, lens),
+                 lambda: lb.paged_store_e4m3(x, x, *big, lens),
+                 lambda: lb.paged_store(x, x, whole.expand(many, 16, 2, 64), whole.expand(many, 16, 2, 64), lens),
+                 lambda: attend8(x, *big, table, lens),
+                 lambda: attend8(x, *c, wide, lens),
+                 lambda: attend(x, whole.expand(many, 16, 2, 64), whole.expand(many, 16, 2, 64), table, lens),
+                 lambda: prompts(rows, x, x, ptr),
+                 lambda: prompts(x, rows, rows, ptr),
+                 lambda: lb.PromptAttention(1, many + 1, 2, 64, torch.bfloat16),
+                 lambda: lb.PagedAttentionE4M3(1, 2 ** 32 + 2, 2, 64, torch.bfloat16),
+                 lambda: lb.PagedAttention(2 ** 32 + 2, 2, 2, 64, torch.bfloat16)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
