@@ -44,6 +44,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <cstdlib>
 #include <mutex>
 #include <type_traits>
 
@@ -916,6 +917,9 @@ spmv_status_t launch_prompt(const spmv_prompt_attention_t &a, cudaStream_t strea
     p.scale2 = std::max(std::fabs(a.scale) * kLog2e, FLT_MIN);
     p.negate = a.scale < 0.0f;
     p.clocks = (1ll << 31) + kEachClocks * ((int64_t)a.keys + a.requests);
+#ifdef SPMV_DEBUG
+    if (const char *clocks = std::getenv("SPMV_PROMPT_CLOCKS")) p.clocks = std::atoll(clocks);  // waits that run out
+#endif
     CUtensorMap maps[3];
     const bool keys = a.keys > 0;  // without keys nothing is loaded
     if (!make_map(&maps[0], S::BF16, a.q, a.head_dim, a.q_heads, a.tokens, a.q_stride, p.group, p.tile_tokens) ||
