@@ -811,7 +811,9 @@ typedef struct {
     int32_t causal;
     float scale;
     int32_t reserved;
-    int64_t q_stride[2];            /* row, head (elements); multiples of 16 bytes, as are the addresses */
+    int64_t q_stride[2];            /* row, head (elements); multiples of 16 bytes, as are the addresses;
+                                       those of q, k and v are positive and less than 2^38.  Of a
+                                       dimension of one element they are of no matter */
     int64_t k_stride[2];
     int64_t v_stride[2];
     int64_t out_stride[2];

@@ -63,6 +63,8 @@ class PromptAttention:
         ``q_ptr[r]`` .. ``q_ptr[r + 1] - 1`` (int32), its keys those of
         ``kv_ptr`` (None: the same rows).  Its last query stands at its last
         key; with ``causal`` a query sees the keys up to its own place.
+        Rows and heads of q, k and v are multiples of 16 bytes apart, and not
+        0 (expanded).
         ``scale``: head_dim ** -0.5 if None.  Rows of no request are left as
         they were.  It has no derivative."""
         if _launch.tracked(q, k, v, out):
