@@ -18,8 +18,10 @@
 // into [2^14, 2^15): bf16's 8 bits fit whole as far down as 2^-29 of it, and
 // what is lost below is 2^-39 of it, less than the 32-bit sums round.
 //   131,071 positions of 8 heads of 128, 8 query heads each (269 MB) 62 us: 0.64
-// of the copy's rate.  Half the bytes leave the instructions as its bound, 760
-// a warp for a chunk of 32 positions, two warps a scheduler.
+// of the copy's rate.  Bound by latency: 760 instructions a warp for a chunk of
+// 32 positions, each held up by the one before, and two warps a scheduler,
+// which registers allow, fill 37 % of the issue slots while memory is at half
+// of its peak; start and join take about 13 us.
 //   Weights are taken 2^14 times as large, times vs / ref with ref the power of
 // two below the largest value scale so far, as hi + lo; the sums, relative to
 // ref, are rescaled when a larger scale comes.

@@ -32,15 +32,26 @@
 // are zero, which a NaN or infinity in V would survive as NaN: in tiles that
 // any row sees in part the loading warp looks V over, puts zeros in the place
 // of what is not finite and notes it; the rows that do see such a value then
-// add it at the end.
+// add it at the end, and where an output is NaN all the row's values are looked
+// through.
 //
-// Bound by the matrix instructions where there are many rows: 8,192 tokens, 64
-// over 8 heads of 128 bf16, causal (1.10 TFLOP) 640 us, 1,720 TFLOP/s, 0.91 of
-// the library product's; back to back, under the power limit, 715 us.  Heads of
-// 64 elements 940 TFLOP/s, where the softmax takes longer than the products;
-// of 192 1,270 (two tiles, 64 keys at a time; one tile 1,000), of 256 985: one
-// tile's outputs fill half of tensor memory, and a key from L2 serves half as
-// many rows.
+// A weight is rounded to the elements' type, as an operand of the second
+// product has to be; the sum it is divided by takes it whole.  That is an error
+// of 2^-8 (f16 2^-11) of sum p |v| at most, and errors against 64 bits are 1.2
+// to 1.4 times those of a softmax in 32 bits whose output is rounded once.  To
+// keep more of it would take a product of what the rounding left: three where
+// there are two, in a kernel that waits for products.
+//
+// 8,192 tokens, 64 over 8 heads of 128 bf16, causal (1.10 TFLOP): back to back,
+// under the power limit, 706 us, 1,557 TFLOP/s, 0.92 of the library product's
+// under the same limit; 20 at a time 647 us, 1,700 TFLOP/s, 0.90 of the library
+// product's burst.  Bound by the matrix instructions: a step's 2,048 clocks of
+// them take about 2,500.  Heads of 64 elements 957 TFLOP/s: matrix instructions
+// 41 % of the time, the exponential unit too, for a tile's products wait while
+// a thread goes through its row's 128 scores.  Of 192 1,270 (two tiles, 64 keys
+// at a time; one tile 1,000).  Of 256 985: one tile, whose outputs fill half of
+// tensor memory; matrix instructions 42 %, L2 24 %, 17 % of the issue slots: a
+// step's chain of waits.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
