@@ -102,7 +102,9 @@ def debug_lib() -> ctypes.CDLL:
     """Load libspmv_debug.so, the build with device-side checks of the column
     indices gathered with (-DSPMV_DEBUG), building it first if needed.  Same
     functions as lib(); an index outside [0, n) sets bit 2 of the plan's
-    device status instead of reading outside x."""
+    device status instead of reading outside x.  Waits inside the kernel of
+    prompts' attention run out after SPMV_PROMPT_CLOCKS clocks, where that is
+    set."""
     global _debug_lib
     if _debug_lib is None:
         _debug_lib = _load(_build.build(debug=True))
